@@ -724,6 +724,96 @@ int skv_prefill_attend(int nq, int Hq, int Hkv, int d, const uint16_t *q, const 
                        int32_t *dev_status, void *stream);
 
 /* ========================================================================== */
+/* Dense layers beside the sparse ones: projections to cache rows, and the    */
+/* attention of new tokens over a paged cache.                                */
+/* ========================================================================== */
+/*
+ * skv_norm_rope_append -- the step between a layer's projections and its
+ * attention, in one pass: queries and keys are normed per head and rotated by
+ * position, and keys and values become cache rows.  For token i, each head x
+ * of d values of q and k:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   (fp32; weight NULL: y = x)
+ *   z = y, but for dims [0, rot): with t = positions[i] * inv_freq[f],
+ *       (z_a, z_b) = (y_a cos t - y_b sin t, y_b cos t + y_a sin t) for the
+ *       pairs (a, b) = (f, f + rot/2), or (2f, 2f + 1) when interleaved
+ * q_out[i] = bf16(z).  The row out_rows[i] of k_pool takes bf16(z) of the
+ * keys and that of v_pool the values, in the kv_kind row encoding:
+ * SKV_KV_BF16 as they are, SKV_KV_INT8 as skv_quantize_int8_rows encodes the
+ * bf16 values.  The angle is reduced modulo one turn before it is rounded to
+ * fp32, so far positions lose nothing (about 2e-7 rad up to 2^24).
+ *   q  bf16 [n_tok][Hq][d], k and v  bf16 [n_tok][Hkv][d]: a token's heads are
+ *      consecutive, tokens q_stride / k_stride / v_stride elements apart (views
+ *      of a fused projection).  Each of the three may be NULL: that part is
+ *      left out (with only q and k and out_rows NULL the call norms and
+ *      rotates q and k into plain arrays, for skv_decode_layer_step)
+ *   q_weight, k_weight  fp32 [d] or NULL     inv_freq  fp32 [rot/2]
+ *   positions  int32 [n_tok]
+ *   q_out    bf16 [n_tok][Hq][d]
+ *   out_rows int64 [n_tok], or NULL (token i -> row i); a negative row: the
+ *            token has none (padding) and only its q_out is written; a row >=
+ *            n_pool_rows is skipped and sets SKV_DEV_RANGE.  Two tokens with
+ *            the same row leave either's bytes there
+ *   k_pool, v_pool  bf16 or int8 [n_pool_rows][Hkv][d]
+ *   k_scale, v_scale  fp16 [n_pool_rows][Hkv] (SKV_KV_INT8 only)
+ * Constraints: d in {64, 128, 256}; rot a multiple of 16, 0 <= rot <= d;
+ * strides multiples of 8; q, k, v, q_out and the pools 16-byte aligned; no
+ * output overlaps an input.
+ * Errors: SKV_EUNSUPPORTED for another d, SKV_EINVAL for the rest.
+ */
+int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int rot, int interleaved,
+                         const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                         const uint16_t *v, int64_t v_stride, const float *q_weight,
+                         const float *k_weight, float eps, const int32_t *positions,
+                         const float *inv_freq, uint16_t *q_out, int kv_kind,
+                         const int64_t *out_rows, int64_t n_pool_rows, void *k_pool, void *v_pool,
+                         uint16_t *k_scale, uint16_t *v_scale, int32_t *dev_status, void *stream);
+
+/*
+ * skv_paged_attend -- exact attention of each request's newest tokens over
+ * its paged cache: a chunk of a prompt, a few drafted tokens, or one token
+ * per request.  Request b owns the tokens [q_start[b], q_start[b+1]) of q,
+ * the last of its lengths[b] cached tokens (their K and V rows are in the
+ * cache already, see skv_norm_rope_append); with n_b of them, token i stands
+ * at p = lengths[b] - n_b + i and sees the keys
+ *   t <= p, and with W > 0 only those with t > p - W or t < S
+ * (a sliding window of W tokens, itself included, and S sinks).  Query head g
+ * reads KV head g / (Hq/Hkv):
+ *   out[i][g] = sum_t softmax_t(softmax_scale q[i][g] . k[t]) v[t]
+ * A token that sees nothing (p < 0) gets zeros.  Key t of request b is pool
+ * row block_table[b][t / page] * page + t % page, rows in the kv_kind
+ * encoding.  Only pages with visible keys are looked up (pages before a
+ * window may be gone); a page beyond n_pages or the pool is skipped and sets
+ * SKV_DEV_RANGE.
+ *   q  bf16 [n_tok][Hq][d], tokens q_stride elements apart
+ *   k_pool, v_pool  bf16 or int8 [n_pool_rows][Hkv][d]
+ *   k_scale, v_scale  fp16 [n_pool_rows][Hkv] (SKV_KV_INT8 only)
+ *   block_table int32 [B][n_pages]     lengths int32 [B]
+ *   q_start  int32 [B+1], ascending (a request may have no token), or NULL:
+ *            one token per request (n_tok == B).  Tokens before q_start[0] and
+ *            from q_start[B] on are padding: their output is left as it was.
+ *            A q_start that descends or leaves [0, n_tok] sets SKV_DEV_RANGE
+ *   out      bf16 [n_tok][Hq][d]
+ *   workspace  skv_paged_attend_workspace_size(...) bytes, zero-filled before
+ *            first use; a workspace of the largest size serves every smaller
+ *            call, in any order
+ * Constraints: d in {128, 256}; Hq / Hkv <= 128; page a multiple of 8;
+ * q_stride a multiple of 8; q, out, pools and workspace 16-byte aligned; B <=
+ * 4096.  Errors: SKV_EUNSUPPORTED outside the first three, SKV_ENOMEM for a
+ * short workspace, SKV_EINVAL for the rest.
+ * Accuracy: logits accumulate exact products in fp32, the probabilities
+ * (times the value scale for int8 rows) are rounded to bf16 for the tensor
+ * cores, and each row is divided by the sum of its rounded probabilities.
+ */
+size_t skv_paged_attend_workspace_size(int B, int n_tok, int Hq, int Hkv, int d);
+int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, int d, const uint16_t *q,
+                     int64_t q_stride, const void *k_pool, const void *v_pool,
+                     const uint16_t *k_scale, const uint16_t *v_scale, int64_t n_pool_rows,
+                     int page, const int32_t *block_table, int64_t n_pages,
+                     const int32_t *q_start, const int32_t *lengths, int S, int W,
+                     float softmax_scale, uint16_t *out, void *workspace, size_t workspace_bytes,
+                     int32_t *dev_status, void *stream);
+
+/* ========================================================================== */
 /* Pressure-driven residency ([P2] "vLLM's Hybrid HiSparse ...", "Three       */
 /* residency states, one block pool": KV stays on the GPU while there is room */
 /* and gives up residency page by page as the pool runs short; completed      */

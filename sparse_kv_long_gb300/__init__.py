@@ -102,6 +102,11 @@ def _load():
                 "skv_prefill_index_scores": ([i32, P, P, i64, P, i64, P, P], i32),
                 "skv_prefill_attend": ([i32, i32, i32, i32, P, P, P, i64, P, P, i64, P, i32, P, f32, P, P, P, P],
                                        i32),
+                "skv_norm_rope_append": ([i64, i32, i32, i32, i32, i32, P, i64, P, i64, P, i64, P, P, f32, P, P, P, i32,
+                                          P, i64, P, P, P, P, P, P], i32),
+                "skv_paged_attend_workspace_size": ([i32, i32, i32, i32, i32], sz),
+                "skv_paged_attend": ([i32, i32, i32, i32, i32, i32, P, i64, P, P, P, P, i64, i32, P, i64, P, P, i32,
+                                      i32, f32, P, P, sz, P, P], i32),
                 "skv_residency_create": ([i32, i32, i32, i64, i32, ctypes.POINTER(ctypes.c_void_p)], i32),
                 "skv_residency_destroy": ([P], None),
                 "skv_residency_add": ([P, i32, i64, i32], i32),
@@ -448,6 +453,58 @@ def prefill_attend(q, k_src, v_src, n_tokens, k_stage, v_stage, idx, count, soft
         nq, Hq, Hkv, d, _ptr(q), _addr(k_src), _addr(v_src), int(n_tokens), _ptr(k_stage), _ptr(v_stage),
         int(chunk), _ptr(idx), idx.shape[1], _ptr(count), float(softmax_scale), _ptr(state), _ptr(out),
         _ptr(status), _stream(stream)))
+    return out
+
+
+# ---- dense layers: projections to rows, new tokens over a paged cache ---------------
+
+def _heads(t):
+    """(heads, d, token stride) of a [n][heads][d] tensor whose tokens' heads are consecutive."""
+    if t is None:
+        return 0, 0, 0
+    n, H, d = t.shape
+    if (H > 1 and t.stride(1) != d) or (d > 1 and t.stride(2) != 1):
+        raise ValueError("a token's heads must be consecutive")
+    return H, d, t.stride(0) if n > 1 else H * d
+
+
+def norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pool, v_pool, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, kv_kind=KV_BF16, k_scale=None, v_scale=None, out_rows=None, status=None,
+                     stream=None):
+    """q bf16 [n][Hq][d], k, v bf16 [n][Hkv][d] (views with any token stride; each may be None): q and k normed per
+    head (weights fp32 [d] or None) and rotated over 2 * len(inv_freq) dims by positions int32 [n]; q -> q_out,
+    k and v -> rows out_rows (int64 [n], negative: none; None: row i) of the pools [rows][Hkv][d]."""
+    some = next(t for t in (q, k, v) if t is not None)
+    n, d = some.shape[0], some.shape[2]
+    Hq, _, qs = _heads(q)
+    kh, _, ks = _heads(k)
+    vh, _, vs = _heads(v)
+    if any(t is not None and (t.shape[0] != n or t.shape[2] != d) for t in (q, k, v)) or (kh and vh and kh != vh):
+        raise ValueError("q, k and v differ in tokens, head dimension or KV heads")
+    pool = k_pool if k_pool is not None else v_pool
+    _check("skv_norm_rope_append", _load().skv_norm_rope_append(
+        n, Hq, kh or vh, d, 0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), _ptr(q), qs, _ptr(k),
+        ks, _ptr(v), vs, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), _ptr(q_out),
+        kv_kind, _ptr(out_rows), 0 if pool is None else pool.shape[0], _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
+        _ptr(v_scale), _ptr(status), _stream(stream)))
+    return q_out
+
+
+def paged_attend_workspace_size(B, n_tok, Hq, Hkv, d) -> int:
+    return int(_load().skv_paged_attend_workspace_size(B, n_tok, Hq, Hkv, d))
+
+
+def paged_attend(kv_kind, q, k_pool, v_pool, block_table, page, lengths, softmax_scale, out, workspace, q_start=None,
+                 S=0, W=0, k_scale=None, v_scale=None, status=None, stream=None):
+    """q bf16 [n][Hq][d] (any token stride): the newest tokens of each request, request b's at q_start[b] ..
+    q_start[b+1] (None: one each); pools [rows][Hkv][d]; block_table int32 [B][n_pages] -> out bf16 [n][Hq][d]."""
+    Hq, d, qs = _heads(q)
+    B, n_pages = block_table.shape
+    _check("skv_paged_attend", _load().skv_paged_attend(
+        kv_kind, B, q.shape[0], Hq, k_pool.shape[1], d, _ptr(q), qs, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
+        _ptr(v_scale), k_pool.shape[0], page, _ptr(block_table), n_pages, _ptr(q_start), _ptr(lengths), S, W,
+        float(softmax_scale), _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+        _stream(stream)))
     return out
 
 

@@ -1,0 +1,73 @@
+"""Refusals of skv_norm_rope_append and skv_paged_attend: decided on the host,
+before anything is launched, so they run without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+P = ctypes.c_void_p
+OK, EINVAL, EUNSUPPORTED, ENOMEM = 0, 1, 2, 4
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_kv_long_gb300 import _build
+    _build.build()
+    import sparse_kv_long_gb300 as skv
+    return skv.lib()
+
+
+NORM = dict(n_tok=4, Hq=8, Hkv=2, d=256, rot=64, inter=0, q=P(256), qs=2048, k=P(256), ks=512, v=P(256), vs=512,
+            qw=None, kw=None, eps=1e-6, pos=P(256), inv=P(256), q_out=P(256), kind=0, rows=P(256), n_rows=64,
+            kp=P(256), vp=P(256), ksc=None, vsc=None, st=None, stream=None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(n_tok=0), OK), (dict(n_tok=-1), EINVAL), (dict(d=96), EUNSUPPORTED), (dict(d=512), EUNSUPPORTED),
+    (dict(rot=72), EINVAL), (dict(rot=272), EINVAL), (dict(rot=-16), EINVAL), (dict(inter=2), EINVAL),
+    (dict(q=None, k=None, v=None), EINVAL), (dict(inv=None), EINVAL), (dict(pos=None), EINVAL),
+    (dict(q_out=None), EINVAL), (dict(q=P(8)), EINVAL), (dict(qs=2052), EINVAL), (dict(qs=2040), EINVAL),
+    (dict(kp=None), EINVAL), (dict(vp=None), EINVAL), (dict(kp=P(24)), EINVAL), (dict(ks=256), EINVAL),
+    (dict(kind=2), EINVAL), (dict(kind=1), EINVAL), (dict(kind=1, ksc=P(256)), EINVAL), (dict(eps=-1.0), EINVAL),
+    (dict(eps=float("nan")), EINVAL), (dict(rows=None, n_rows=3), EINVAL), (dict(Hq=0), EINVAL),
+    (dict(Hkv=0), EINVAL), (dict(n_rows=-1), EINVAL),
+])
+def test_norm_rope_append_refuses(lib, change, want):
+    assert lib.skv_norm_rope_append(*{**NORM, **change}.values()) == want
+
+
+ATT = dict(kind=0, B=2, n_tok=6, Hq=8, Hkv=2, d=256, q=P(256), qs=2048, kp=P(256), vp=P(256), ksc=None, vsc=None,
+           n_rows=1024, page=16, table=P(256), n_pages=8, q_start=P(256), lengths=P(256), S=0, W=0, scale=0.1,
+           out=P(256), ws=P(256), wsn=1 << 40, st=None, stream=None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(B=0), OK), (dict(n_tok=0), OK), (dict(kind=2), EINVAL), (dict(B=-1), EINVAL), (dict(n_tok=-1), EINVAL),
+    (dict(B=4097), EINVAL), (dict(Hkv=3), EINVAL), (dict(Hkv=0), EINVAL), (dict(S=-1), EINVAL), (dict(W=-1), EINVAL),
+    (dict(d=64), EUNSUPPORTED), (dict(Hq=258, Hkv=2, qs=258 * 256), EUNSUPPORTED), (dict(page=4), EUNSUPPORTED),
+    (dict(page=20), EUNSUPPORTED), (dict(page=0), EUNSUPPORTED), (dict(q=None), EINVAL), (dict(kp=None), EINVAL),
+    (dict(vp=P(8)), EINVAL), (dict(table=None), EINVAL), (dict(n_pages=0), EINVAL), (dict(lengths=None), EINVAL),
+    (dict(out=P(8)), EINVAL), (dict(n_rows=15), EINVAL), (dict(kind=1), EINVAL), (dict(kind=1, ksc=P(256)), EINVAL),
+    (dict(q_start=None), EINVAL), (dict(qs=2044), EINVAL), (dict(qs=1024), EINVAL), (dict(ws=None), ENOMEM),
+    (dict(wsn=8), ENOMEM), (dict(ws=P(8)), ENOMEM),
+])
+def test_paged_attend_refuses(lib, change, want):
+    assert lib.skv_paged_attend(*{**ATT, **change}.values()) == want
+
+
+def test_workspace_sizes(lib):
+    size = lib.skv_paged_attend_workspace_size
+    assert size(1, 1, 8, 2, 256) > 0
+    assert size(4, 400, 8, 2, 256) >= size(4, 40, 8, 2, 256) >= size(1, 1, 8, 2, 256)
+    for bad in [(0, 1, 8, 2, 256), (1, 0, 8, 2, 256), (1, 1, 8, 3, 256), (1, 1, 8, 2, 96), (1, 1, 258, 2, 256)]:
+        assert size(*bad) == 0
+
+
+def test_binding_refuses_scattered_heads():
+    import sparse_kv_long_gb300 as skv
+    x = torch.zeros((4, 256, 8), dtype=torch.bfloat16).transpose(1, 2)  # a head's values 8 apart
+    with pytest.raises(ValueError):
+        skv.norm_rope_append(x, None, None, None, None, None, None, None)
+    q, k = torch.zeros((4, 8, 256), dtype=torch.bfloat16), torch.zeros((5, 2, 256), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        skv.norm_rope_append(q, k, None, None, None, None, None, None)
