@@ -797,8 +797,8 @@ int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int rot, int int
  *            first use; a workspace of the largest size serves every smaller
  *            call, in any order
  * Constraints: d in {128, 256}; Hq / Hkv <= 128; page a multiple of 8;
- * q_stride a multiple of 8; q, out, pools and workspace 16-byte aligned; B <=
- * 4096.  Errors: SKV_EUNSUPPORTED outside the first three, SKV_ENOMEM for a
+ * softmax_scale > 0; q_stride a multiple of 8; q, out, pools and workspace
+ * 16-byte aligned; B <= 4096; n_pages * page < 2^31 - 1024.  Errors: SKV_EUNSUPPORTED outside the first three, SKV_ENOMEM for a
  * short workspace, SKV_EINVAL for the rest.
  * Accuracy: logits accumulate exact products in fp32, the probabilities
  * (times the value scale for int8 rows) are rounded to bf16 for the tensor

@@ -6,22 +6,73 @@
 // included) stands at p = T - n_b + i and sees the keys t <= p that lie in the
 // window (W == 0, or t > p - W) or among the first S:
 //   out = sum_t softmax_t(scale q.k_t) v_t over the visible t; none: 0.
+//
+// One kernel on the tcgen05 tensor cores.  A query tile is 128 rows of one KV
+// head per CTA, row = (token, query head of the group), so the group's heads
+// share every K and V row read.  Keys come in tiles of KT; per tile
+//   S = Q K^T   (M = 128 rows, N = KT, fp32 in tensor memory),
+//   P = exp2(S scale log2e - m)  (one thread per row; bf16, written over S),
+//   O += P V    (P from tensor memory, V from shared memory, fp32 in TMEM),
+// with S double-buffered so that the softmax of one tile runs under the
+// products of its neighbours.  m moves only when a row's maximum grows by
+// more than 2^kLazy; then the row's O is rescaled.  The row sum adds the
+// rounded weights (bf16 rows), so the weights applied sum to one.
+//
+// Long prompts run as CTA pairs (cta_group::2, CTAS = 2): 256 query rows, 128
+// keys a tile, each CTA holding half of the tile's keys (K) and half of its
+// dims (V).  That halves the bytes that L2 has to hand to each SM: at M = 128
+// a 256-dim tile needs 60 B per clock and SM, more than L2 gives.  Single
+// tokens and drafts run as single CTAs with 64-key tiles; they are bound by
+// reading the cache, and shared memory holds mostly the ring of K/V tiles.
+//
+// K and V tiles are 5-dimensional TMA boxes of whole pages (or the largest
+// power-of-two part of one), laid out as [8-row group][64-column block][8 x
+// 128 B], 128-byte swizzle: one box per page brings all dims.  int8 rows
+// arrive in a staging ring and four warps widen them to bf16 (exact); the K
+// scales multiply the logits, the V scales the weights.
+//
+// Work list: items (request, query tile, KV head), each cut into pieces of
+// about c key tiles; c is chosen on the device from the lengths by the cost
+// of a few candidates (plan()).  Whole items write bf16 output, pieces write
+// fp32 partials that merge_kernel joins in piece order.
+#include <cuda.h>
+
 #include "common.cuh"
+#include "tc.cuh"
 
 namespace skv {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 128;         // query rows per CTA (tensor-memory lanes)
+constexpr int kMaxStages = 12;     // K/V ring
+constexpr int kMaxStaging = 12;    // int8 staging ring
+constexpr int kPieces = 4;         // piece descriptors in flight
+constexpr int kTileInfo = 16;      // tiles whose page validity is kept (more than the ring holds)
+constexpr int kScaleRing = 4;      // tiles whose int8 scales are kept
+constexpr int kCand = 64;          // split candidates
+constexpr float kLazy = 8.f;       // log2 units a maximum may grow before O is rescaled
+constexpr int kSplitPerSm = 4;     // pieces that write partials, per SM
+constexpr uint32_t kSCol = 256;    // tensor memory: O in [0, D), S/P buffers from here
+constexpr int kMaxSmem = 227 * 1024;
+
+struct Piece {
+  int tok0, rows;     // first token, valid rows of the whole tile (tokens * G)
+  int pos0;           // position of the first token
+  int b, h;
+  int lo, nsink;      // first window tile, sink tiles before it
+  int j0, n;          // this piece's tiles: j0 .. j0 + n of the item's list
+  int slot;           // partial slot, -1: whole item
+  int last;           // no piece follows
+};
 
 struct PagedArgs {
-  int B, n_tok, Hq, Hkv;
+  int B, n_tok, Hkv, G, tpt;  // tpt: tokens per query tile
   const uint16_t* q;
   int64_t q_stride;
-  const void *k_pool, *v_pool;
+  const uint16_t* v_pool;     // bf16 rows, for the non-finite pass only
   const __half *k_scale, *v_scale;
   int64_t n_blocks;
-  int page;
+  int page, rb;               // rows per TMA box
   const int32_t* block_table;
   int64_t n_pages;
   const int32_t *q_start, *lengths;
@@ -29,89 +80,1167 @@ struct PagedArgs {
   float scale_log2;
   uint16_t* out;
   int32_t* status;
+  int stages, staging;        // ring depths
+  int q_bytes;                // shared memory of the query tile
+  int part_rows;              // rows of a partial slot
+  int max_split;              // partial slots
+  int* ws_head;               // [0]: split items of this call
+  int4* ws_item;              // per split item: (tok0, rows, h, first slot), (pieces, 0, 0, 0)
+  float2* ws_ml;              // [slot][row]: running max (log2 units), row sum
+  float* ws_o;                // [slot][row][D]
 };
 
-// One CTA per (token, query head): warp w takes keys w, w + 4, ...; each lane
-// holds D / 32 dims.  Online softmax per warp, the warps joined at the end.
-template <int D, bool INT8>
-__global__ void __launch_bounds__(kThreads) paged_kernel(const PagedArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float so[kWarps][D], sm_m[kWarps], sm_l[kWarps];
-  const int tok = blockIdx.x, g = blockIdx.y, h = g / (a.Hq / a.Hkv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Every row of work here is a dot product per key on the plain cores: right
-  // for every case, bound by their instruction rate.
-  int b = tok, start = tok, end = tok + 1;
+struct alignas(16) Aux {
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  // Two barriers where a waiter may skip tiles: when S(t + 1) is there, O of
+  // t - 1 is done and of t may not be, and one parity could not tell them apart.
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full, o_free, mma_idle;
+  uint64_t pc_full[kPieces], pc_empty[kPieces];
+  Piece pc[kPieces];
+  uint32_t tile_bad[kTileInfo];  // bit i: rows [8 i, 8 i + 8) of the tile have no page
+  int cand_p[kCand], cand_s[kCand];
+  int nmax, units, split_c, split_items;
+  uint32_t tmem_base;
+  int dirty;  // a value that only some queries of a tile see was not finite
+  int abort;
+};
+
+struct alignas(16) Aux8 {  // int8 rows only
+  uint64_t st_full[kMaxStaging], st_empty[kMaxStaging];
+  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
+  alignas(16) float ks[kScaleRing][kRows], vs[kScaleRing][kRows];
+};
+
+static_assert(sizeof(Aux) <= 2048, "the bf16 pair kernel's shared memory is full");
+
+// ---- work list -------------------------------------------------------------------
+
+struct Req {
+  int start, nq, T;  // first token, new tokens, cached tokens
+  int nqt, ntmax;    // query tiles, key tiles of the last one
+};
+
+// Key tiles of query tile qt of a request: window tiles [lo, lo + n - nsink) after the sink tiles [0, nsink).
+template <int KT>
+__device__ __forceinline__ void tile_range(const PagedArgs& a, const Req& r, int qt, int& lo, int& nsink, int& n) {
+  const int first = qt * a.tpt, m = min(a.tpt, r.nq - first);
+  const int p_lo = max(0, r.T - r.nq + first);
+  int p_hi = r.T - r.nq + first + m - 1;
+  const int64_t cap = a.n_pages * a.page;
+  if (p_hi >= cap) p_hi = static_cast<int>(cap) - 1;
+  lo = nsink = n = 0;
+  if (p_hi < 0 || m <= 0) return;
+  if (a.W > 0) {
+    lo = max(0, p_lo - a.W + 1) / KT;
+    nsink = min((min(a.S, p_hi + 1) + KT - 1) / KT, lo);
+  }
+  n = nsink + max(0, p_hi / KT - lo + 1);
+}
+
+template <int KT>
+__device__ __forceinline__ Req request(const PagedArgs& a, int b, bool report) {
+  Req r;
+  if (b >= a.B) return Req{0, 0, 0, 0, 0};
+  r.T = a.lengths[b];
   if (a.q_start) {
-    if (tok == 0 && g == 0)
-      for (int r = threadIdx.x; r < a.B; r += kThreads)
-        if (a.q_start[r] < 0 || a.q_start[r + 1] < a.q_start[r] || a.q_start[r + 1] > a.n_tok)
-          set_status(a.status, SKV_DEV_RANGE);
-    int lo = 0, hi = a.B;  // last b with q_start[b] <= tok
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.q_start[mid] <= tok) lo = mid; else hi = mid;
-    }
-    b = lo;
-    start = a.q_start[b];
-    end = a.q_start[b + 1];
-    if (tok < start || tok >= end) return;  // behind the last sequence: left as it was
+    const int s = a.q_start[b], e = a.q_start[b + 1];
+    const bool bad = s < 0 || e < s || e > a.n_tok;
+    if (bad && report) set_status(a.status, SKV_DEV_RANGE);
+    r.start = s;
+    r.nq = bad ? 0 : e - s;
+  } else {
+    r.start = b;
+    r.nq = 1;
   }
-  const int T = a.lengths[b];
-  const int p = T - (end - start) + (tok - start);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; e++) {
-    q[e] = bf16_bits_to_f32(a.q[tok * a.q_stride + static_cast<int64_t>(g) * D + E * lane + e]) * a.scale_log2;
-    o[e] = 0.f;
-  }
-  const int w0 = a.W ? max(0, p - a.W + 1) : 0;
-  for (int t = warp; t <= p; t += kWarps) {
-    if (t >= a.S && t < w0) continue;
-    const int64_t pg = t / a.page;
-    const int64_t blk = pg < a.n_pages ? a.block_table[b * a.n_pages + pg] : -1;
-    if (blk < 0 || blk >= a.n_blocks) {
-      if (lane == 0) set_status(a.status, SKV_DEV_RANGE);
-      continue;
+  if (r.nq > 0 && r.T > a.n_pages * a.page && report) set_status(a.status, SKV_DEV_RANGE);
+  r.nqt = (r.nq + a.tpt - 1) / a.tpt;
+  r.ntmax = 0;
+  if (r.nqt > 0) {
+    int lo, ns;
+    tile_range<KT>(a, r, r.nqt - 1, lo, ns, r.ntmax);
+    if (r.nqt > 1) {  // the last tile may hold fewer tokens, and so a tile less
+      int n2;
+      tile_range<KT>(a, r, r.nqt - 2, lo, ns, n2);
+      r.ntmax = max(r.ntmax, n2);
     }
-    const int64_t vec = (blk * a.page + t % a.page) * a.Hkv + h;
-    float s = 0.f, v[E];
-    for (int e = 0; e < E; e++) {
-      const int64_t at = vec * D + E * lane + e;
-      if (INT8) {
-        s += q[e] * static_cast<const int8_t*>(a.k_pool)[at];
-        v[e] = static_cast<const int8_t*>(a.v_pool)[at] * __half2float(a.v_scale[vec]);
-      } else {
-        s += q[e] * bf16_bits_to_f32(static_cast<const uint16_t*>(a.k_pool)[at]);
-        v[e] = bf16_bits_to_f32(static_cast<const uint16_t*>(a.v_pool)[at]);
+  }
+  return r;
+}
+
+__device__ __forceinline__ int pieces_of(int ntmax, int c) { return c > 0 && ntmax > c ? (ntmax + c - 1) / c : 1; }
+
+// ---- helpers ---------------------------------------------------------------------
+
+template <int CTAS>
+__device__ __forceinline__ uint32_t leader_addr(uint64_t* bar) {
+  const uint32_t l = tc::smem_addr(bar);
+  if (CTAS == 1) return l;
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(l));
+  return r;
+}
+
+// Arrive on the leader CTA's barrier.
+template <int CTAS>
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+  if (CTAS == 1)
+    tc::bar_arrive(bar);
+  else
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr<CTAS>(bar))
+                 : "memory");
+}
+
+// A box of the pool to this CTA's shared memory.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int sub, int rg, int h, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(0), "r"(sub), "r"(rg), "r"(h), "r"(tc::smem_addr(bar))
+      : "memory");
+}
+
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int b_mn) {
+  return tc::idesc_f16(M, N, b_mn) | (1u << 7) | (1u << 10);  // A and B bf16
+}
+
+template <int CTAS>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  if (CTAS == 1)
+    tc::mma_f16(d, a, b, idesc, acc);
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0));
+}
+
+template <int CTAS>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  if (CTAS == 1)
+    tc::mma_f16_ts(d, a, b, idesc, acc);
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0));
+}
+
+// Completion of the earlier products, signalled on the barrier of every CTA of the pair.
+template <int CTAS>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (CTAS == 1)
+    tc::mma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            tc::smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two int8 codes (bytes 0 and 1, or 2 and 3, of x) -> two bf16, exact: a
+// byte's low 7 bits under the exponent of 128 give 128 + low7, its sign bit
+// there gives 128 or 256, and their difference is the code.
+template <int HI>
+__device__ __forceinline__ uint32_t int8_to_bf16x2(uint32_t x) {
+  const uint32_t w = prmt(x, 0x43434343u, HI ? 0x4342u : 0x4140u);
+  const uint32_t lo = w & 0xff7fff7fu, sg = w & 0xff80ff80u;
+  const __nv_bfloat162 r =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&sg));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Copies and products take the K and V tiles of a piece in the order K0, K1,
+// V0, K2, V1, ..., V(n-1); this is the place of V(j) in it.
+__device__ __forceinline__ uint32_t fill_v(int j, int n) { return j + 1 < n ? 2u * j + 2u : 2u * n - 1u; }
+
+struct Ring {  // a stage index and the parity of its current use
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int depth) {
+    if (++s == depth) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+template <int D, int CTAS, bool INT8>
+__global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                 const PagedArgs a) {
+  constexpr int KT = 64 * CTAS;          // keys per tile
+  constexpr int NSUB = D / 64;           // 64-column blocks of a row
+  constexpr int VSUB = NSUB / CTAS;      // those of this CTA's part of V
+  constexpr int STAGE = 64 * D * 2;      // bytes of a K or V stage (either part)
+  constexpr int THREADS = INT8 ? 384 : 256;
+  constexpr uint32_t SBO_K = NSUB * 1024, SBO_V = VSUB * 1024;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
+  unsigned char* sQ = sm;
+  unsigned char* sKV = sQ + a.q_bytes;
+  unsigned char* sI8 = sKV + a.stages * STAGE;
+  Aux* ax = reinterpret_cast<Aux*>(sI8 + (INT8 ? a.staging * (STAGE / 2) : 0));
+  Aux8* a8 = reinterpret_cast<Aux8*>(ax + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CTAS == 1 ? 0u : tc::cluster_rank();
+  const int unit = blockIdx.x / CTAS, n_units = gridDim.x / CTAS;
+  volatile int* abort = &ax->abort;
+
+  allow_dependent_launch();  // the merge may be scheduled as SMs come free; it waits for this grid
+  if (tid == 0) {
+    for (int s = 0; s < kMaxStages; s++) {
+      // int8: the widening warps of both CTAs; bf16: the copies, and on the leader a note from the peer's
+      tc::bar_init(&ax->kv_full[s], INT8 ? 4 * CTAS : (rank == 0 ? CTAS : 1));
+      tc::bar_init(&ax->kv_empty[s], 1);
+    }
+    for (int s = 0; s < 2; s++) {
+      tc::bar_init(&ax->s_full[s], 1);
+      tc::bar_init(&ax->p_full[s], 4 * CTAS);
+      tc::bar_init(&ax->pv_done[s], 1);
+    }
+    tc::bar_init(&ax->q_full, 4 * CTAS);
+    tc::bar_init(&ax->o_free, 4 * CTAS);
+    tc::bar_init(&ax->mma_idle, 1);
+    for (int s = 0; s < kPieces; s++) {
+      tc::bar_init(&ax->pc_full[s], 1);
+      tc::bar_init(&ax->pc_empty[s], INT8 ? 11 : 5);  // MMA thread, softmax warps, (scale and widening warps)
+    }
+    if (INT8) {
+      for (int s = 0; s < kMaxStaging; s++) {
+        tc::bar_init(&a8->st_full[s], 1);
+        tc::bar_init(&a8->st_empty[s], 4);
+      }
+      for (int s = 0; s < kScaleRing; s++) {
+        tc::bar_init(&a8->sc_full[s], 1);
+        tc::bar_init(&a8->sc_empty[s], 4);
       }
     }
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    if (INT8) s *= __half2float(a.k_scale[vec]);
-    const float mn = fmaxf(m, s);
-    const float c = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(s - (mn == -INFINITY ? 0.f : mn));
-    m = mn;
-    l = l * c + w;
-    for (int e = 0; e < E; e++) o[e] = o[e] * c + w * v[e];
+    ax->abort = 0;
+    ax->dirty = 0;
+    ax->nmax = 0;
+    ax->units = 0;
+    ax->split_items = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int e = 0; e < E; e++) so[warp][E * lane + e] = o[e];
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-  }
-  __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < kWarps; w++) M = fmaxf(M, sm_m[w]);
-  for (int x = threadIdx.x; x < D; x += kThreads) {
-    float acc = 0.f;
-    L = 0.f;
-    for (int w = 0; w < kWarps; w++) {
-      const float f = sm_m[w] == -INFINITY ? 0.f : exp2f(sm_m[w] - M);
-      L += f * sm_l[w];
-      acc += f * so[w][x];
+  if (tid < kCand) ax->cand_p[tid] = ax->cand_s[tid] = 0;
+  if (warp == 1) {
+    if (CTAS == 1) {
+      tc::tmem_alloc<512>(&ax->tmem_base);
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+          tc::smem_addr(&ax->tmem_base)));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
-    const __nv_bfloat16 r = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
-    a.out[(static_cast<int64_t>(tok) * a.Hq + g) * D + x] = *reinterpret_cast<const uint16_t*>(&r);
   }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+
+  // ---- plan: tiles per piece -----------------------------------------------------
+  // Candidate k cuts the longest item into k pieces of c = ceil(nmax / k)
+  // tiles and every other item into ceil(tiles / c).  Its cost is the number
+  // of waves over the CTAs times a piece (the last wave at full length), a
+  // piece paying kOvh tiles for filling and draining its pipeline, and a
+  // split paying kJoin tiles once for writing and joining partials.
+  {
+    constexpr float kOvh = 3.f, kJoin = CTAS == 1 ? 4.f : 3.f;
+    int nmax = 0, units = 0;
+    for (int b = tid; b < a.B; b += THREADS) {
+      const Req r = request<KT>(a, b, unit == 0 && rank == 0);
+      nmax = max(nmax, r.ntmax);
+      units += r.nqt * r.ntmax;
+    }
+    nmax = __reduce_max_sync(0xffffffffu, nmax);
+    units = __reduce_add_sync(0xffffffffu, units);
+    if (lane == 0 && nmax > 0) {
+      atomicMax(&ax->nmax, nmax);
+      atomicAdd(&ax->units, units);
+    }
+    __syncthreads();
+    nmax = ax->nmax;
+    const int c0 = (nmax + lane) / (lane + 1), c1 = (nmax + lane + 32) / (lane + 33);
+    int p0 = 0, p1 = 0, s0 = 0, s1 = 0;
+    if (nmax > 1)
+      for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+        const int m = min(32, a.B - b0 - warp * 32);
+        if (m <= 0) break;
+        const Req r = request<KT>(a, b0 + tid, false);
+        for (int i = 0; i < m; i++) {
+          const int nqt = __shfl_sync(0xffffffffu, r.nqt, i), nt = __shfl_sync(0xffffffffu, r.ntmax, i);
+          const int k0 = pieces_of(nt, c0), k1 = pieces_of(nt, c1);
+          p0 += nqt * k0;
+          p1 += nqt * k1;
+          s0 += k0 > 1 ? nqt * k0 : 0;
+          s1 += k1 > 1 ? nqt * k1 : 0;
+        }
+      }
+    if (nmax > 1) {
+      if (p0) atomicAdd(&ax->cand_p[lane], p0);
+      if (p1) atomicAdd(&ax->cand_p[lane + 32], p1);
+      if (s0) atomicAdd(&ax->cand_s[lane], s0);
+      if (s1) atomicAdd(&ax->cand_s[lane + 32], s1);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      float best = 3e38f;
+      int c_best = nmax;
+      for (int i = lane; i < kCand; i += 32) {
+        const float P = static_cast<float>(ax->cand_p[i]) * a.Hkv;
+        const int c = i == lane ? c0 : c1;
+        const bool fits = static_cast<int64_t>(ax->cand_s[i]) * a.Hkv <= a.max_split;
+        if (nmax > 1 && i < nmax && fits && P > 0.f) {
+          const float avg = static_cast<float>(ax->units) * a.Hkv / P;
+          const float waves = ceilf(P / n_units);
+          const float cost = (waves - 1.f) * (avg + kOvh) + c + kOvh + (i > 0 ? kJoin : 0.f);
+          if (cost < best) {
+            best = cost;
+            c_best = c;
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const float ob = __shfl_xor_sync(0xffffffffu, best, o);
+        const int oc = __shfl_xor_sync(0xffffffffu, c_best, o);
+        if (ob < best || (ob == best && oc > c_best)) {
+          best = ob;
+          c_best = oc;
+        }
+      }
+      if (lane == 0) ax->split_c = max(1, c_best);
+    }
+    if (CTAS == 2)
+      tc::cluster_sync();  // also: the peer's barriers exist before any remote access
+    else
+      __syncthreads();
+  }
+  const int c = ax->split_c;
+  const uint32_t tm = ax->tmem_base;
+
+  if (warp == 0) {
+    // ---------------- pieces and copies ----------------
+    int b32 = 0, base = 0, ibase = 0, sbase = 0;  // first request of the window; pieces, split items, slots before it
+    Req r = request<KT>(a, lane, false);
+    int pp, ii, ss, ns;  // inclusive sums over the window's requests
+    auto scan = [&]() {
+      ns = pieces_of(r.ntmax, c);
+      const int items = r.nqt * a.Hkv;
+      pp = items * ns;
+      ii = ns > 1 ? items : 0;
+      ss = ns > 1 ? items * ns : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, pp, o), y = __shfl_up_sync(0xffffffffu, ii, o),
+                  z = __shfl_up_sync(0xffffffffu, ss, o);
+        if (lane >= o) {
+          pp += x;
+          ii += y;
+          ss += z;
+        }
+      }
+    };
+    scan();
+    const uint32_t full = 0xffffffffu;
+    const int boxes = KT / a.rb;                 // per tile; this CTA copies boxes_k of them for K, all for V
+    const int boxes_k = 64 / a.rb;
+    const uint32_t box_k = static_cast<uint32_t>(a.rb) * D * (INT8 ? 1 : 2), box_v = box_k / CTAS;
+    Ring st;  // K/V stage (bf16) or staging slot (int8)
+    const int depth = INT8 ? a.staging : a.stages;
+    uint64_t* fulls = INT8 ? a8->st_full : ax->kv_full;
+    uint64_t* empties = INT8 ? a8->st_empty : ax->kv_empty;
+    unsigned char* ring = INT8 ? sI8 : sKV;
+    constexpr int SLOT = INT8 ? STAGE / 2 : STAGE;
+    uint32_t uses = 0, tile_no = 0;
+    bool ok = true;
+    for (int k = 0; ok; k++) {
+      // every other round backwards: pieces come longest first, so this evens the CTAs' shares
+      const int id = k * n_units + ((k & 1) ? n_units - 1 - unit : unit);
+      while (b32 < a.B && id >= base + __shfl_sync(full, pp, 31)) {
+        base += __shfl_sync(full, pp, 31);
+        ibase += __shfl_sync(full, ii, 31);
+        sbase += __shfl_sync(full, ss, 31);
+        b32 += 32;
+        r = request<KT>(a, b32 + lane, false);
+        scan();
+      }
+      Piece pc;
+      pc.last = 0;
+      const bool any = b32 < a.B;
+      if (any) {
+        const int w = __ffs(__ballot_sync(full, id < base + pp)) - 1;
+        Req q;
+        q.start = __shfl_sync(full, r.start, w);
+        q.nq = __shfl_sync(full, r.nq, w);
+        q.T = __shfl_sync(full, r.T, w);
+        q.nqt = __shfl_sync(full, r.nqt, w);
+        const int nsw = __shfl_sync(full, ns, w);
+        const int items = q.nqt * a.Hkv;
+        int idx = id - base - (__shfl_sync(full, pp, w) - items * nsw);
+        const int ib = ibase + __shfl_sync(full, ii, w) - (nsw > 1 ? items : 0);
+        const int sb = sbase + __shfl_sync(full, ss, w) - (nsw > 1 ? items * nsw : 0);
+        pc.h = idx % a.Hkv;
+        idx /= a.Hkv;
+        const int seg = idx % nsw, qi = idx / nsw;
+        const int qt = q.nqt - 1 - qi, item = qi * a.Hkv + pc.h;
+        int nt;
+        tile_range<KT>(a, q, qt, pc.lo, pc.nsink, nt);
+        pc.b = b32 + w;
+        pc.tok0 = q.start + qt * a.tpt;
+        pc.rows = min(a.tpt, q.nq - qt * a.tpt) * a.G;
+        pc.pos0 = q.T - q.nq + qt * a.tpt;
+        pc.j0 = static_cast<int>(static_cast<int64_t>(nt) * seg / nsw);
+        pc.n = static_cast<int>(static_cast<int64_t>(nt) * (seg + 1) / nsw) - pc.j0;
+        pc.slot = nsw > 1 ? sb + item * nsw + seg : -1;
+        if (nsw > 1 && seg == 0 && rank == 0 && lane == 0) {
+          a.ws_item[2 * (ib + item)] = make_int4(pc.tok0, pc.rows, pc.h, pc.slot);
+          a.ws_item[2 * (ib + item) + 1] = make_int4(nsw, 0, 0, 0);
+        }
+      } else {
+        pc.last = 1;
+        pc.n = 0;
+        pc.rows = 0;
+        pc.slot = -1;
+      }
+      const int slot = k % kPieces;
+      if (k >= kPieces) ok = tc::bar_wait(&ax->pc_empty[slot], ((k / kPieces) - 1) & 1, abort);
+      if (!__all_sync(full, ok)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        ax->pc[slot] = pc;
+        tc::bar_arrive(&ax->pc_full[slot]);
+      }
+      if (pc.last) break;
+      // Copies, in the order the products take them.  Lane i holds the block of
+      // rows [i rb, i rb + rb) of a tile; ids are read one tile ahead.
+      auto tile_of = [&](int j) { return j < pc.nsink ? j : pc.lo + j - pc.nsink; };
+      auto block_of = [&](int j) -> int {
+        if (j >= pc.n || lane >= boxes) return -1;
+        const int64_t t = static_cast<int64_t>(tile_of(pc.j0 + j)) * KT + lane * a.rb;
+        const int64_t pg = t / a.page;
+        return pg < a.n_pages ? a.block_table[pc.b * a.n_pages + pg] : -1;
+      };
+      const int64_t p_hi = pc.pos0 + pc.rows / a.G - 1;  // keys past it are not copied
+      int cur = block_of(0), prev = -1;
+      for (int j = 0; ok && j <= pc.n; j++) {
+        const int nxt = block_of(j + 1);
+        for (int v = 0; v < 2; v++) {  // K(j), then V(j - 1)
+          const int jj = v ? j - 1 : j;
+          if (jj < 0 || jj >= pc.n) continue;
+          const int blk = v ? prev : cur;
+          const int64_t t0 = static_cast<int64_t>(tile_of(pc.j0 + jj)) * KT;
+          const int64_t t = t0 + lane * a.rb;
+          // some row of the box is visible to some query of the tile
+          const bool want = lane < boxes && t <= p_hi && (a.W == 0 || t + a.rb - 1 > pc.pos0 - a.W || t < a.S);
+          const bool good = want && blk >= 0 && blk < a.n_blocks;
+          if (!v) {  // which 8-row groups have no page (the table's end counts; rows past p_hi are masked anyway)
+            if (__any_sync(full, want && !good)) {
+              if (lane == 0 && rank == 0) set_status(a.status, SKV_DEV_RANGE);
+              uint32_t m = 0;
+              const uint32_t bad = __ballot_sync(full, want && !good);
+              for (int g = 0; g < KT / 8; g++) m |= ((bad >> (8 * g / a.rb)) & 1u) << g;
+              if (lane == 0) ax->tile_bad[tile_no % kTileInfo] = m;
+            } else if (lane == 0) {
+              ax->tile_bad[tile_no % kTileInfo] = 0;
+            }
+            tile_no++;
+          }
+          const int kfirst = static_cast<int>(rank) * boxes_k;
+          const bool mine = good && (v || (lane >= kfirst && lane < kfirst + boxes_k));
+          if (uses >= static_cast<uint32_t>(depth)) ok = tc::bar_wait(&empties[st.s], st.ph ^ 1, abort);
+          if (!__all_sync(full, ok)) {
+            ok = false;
+            break;
+          }
+          const uint32_t cnt = __popc(__ballot_sync(full, mine));
+          const uint32_t bytes = v ? box_v : box_k;
+          if (lane == 0) tc::bar_arrive_expect_tx(&fulls[st.s], cnt * bytes);
+          __syncwarp();
+          if (mine) {
+            const int at = v ? lane : lane - kfirst;
+            const int64_t row = static_cast<int64_t>(blk) * a.page + t % a.page;
+            constexpr int kSubV = INT8 ? (D / CTAS >= 128 ? D / CTAS / 128 : 1) : VSUB;  // column blocks of the V box
+            tma_rows(tc::smem_addr(ring + st.s * SLOT) + at * bytes, v ? &v_map : &k_map,
+                     v ? static_cast<int>(rank) * kSubV : 0, static_cast<int>(row / 8), pc.h, &fulls[st.s]);
+          }
+          __syncwarp();
+          uses++;
+          st.next(depth);
+        }
+        prev = cur;
+        cur = nxt;
+      }
+    }
+    if (!ok) {  // gave up: let the copies in flight land before the CTA leaves
+      if (lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
+      const uint64_t t0 = tc::global_ns();
+      for (int i = 0; i < 1000000 && tc::global_ns() - t0 < 20000000ull; i++) __nanosleep(1000);
+    }
+    // split items of this call, for the merge
+    if (unit == 0 && rank == 0) {
+      int items = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const Req x = request<KT>(a, b0 + lane, false);
+        items += pieces_of(x.ntmax, c) > 1 ? x.nqt * a.Hkv : 0;
+      }
+      items = __reduce_add_sync(full, items);
+      if (lane == 0) a.ws_head[0] = items;
+    }
+  } else if (warp == 1) {
+    // ---------------- products (one thread of the leader) ----------------
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_bf16(kRows * CTAS, KT, 0), id_pv = idesc_bf16(kRows * CTAS, D, 1);
+      const uint32_t aQ = tc::smem_addr(sQ), aKV = tc::smem_addr(sKV);
+      Ring st;
+      uint32_t g = 0, np = 0;  // tiles, pieces with work so far
+      bool ok = true;
+      for (int k = 0; ok; k++) {
+        const int slot = k % kPieces;
+        ok = tc::bar_wait(&ax->pc_full[slot], (k / kPieces) & 1, abort);
+        if (!ok) break;
+        const int n = ax->pc[slot].n, last = ax->pc[slot].last;
+        tc::bar_arrive(&ax->pc_empty[slot]);
+        if (last) break;
+        if (rank != 0) {  // the peer passes on to the leader that its stages are full
+          for (int f = 0; !INT8 && ok && f < 2 * n; f++) {
+            ok = tc::bar_wait(&ax->kv_full[st.s], st.ph, abort);
+            if (ok) arrive_leader<CTAS>(&ax->kv_full[st.s]);
+            st.next(a.stages);
+          }
+          continue;
+        }
+        if (n == 0) continue;
+        ok = tc::bar_wait(&ax->q_full, np & 1, abort, CTAS == 2);
+        for (int j = 0; ok && j <= n; j++) {
+          if (j < n) {
+            ok = tc::bar_wait(&ax->kv_full[st.s], st.ph, abort, CTAS == 2);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t kv = aKV + st.s * STAGE;
+            const uint32_t d = tm + kSCol + ((g + j) & 1) * 128;
+#pragma unroll
+            for (int x = 0; x < D / 16; x++) {
+              const uint32_t off = (x >> 2) * 1024 + (x & 3) * 32;
+              mma_ss<CTAS>(d, tc::sw128_desc(aQ + off, 16, SBO_K), tc::sw128_desc(kv + off, 16, SBO_K), id_qk, x > 0);
+            }
+            commit<CTAS>(&ax->kv_empty[st.s]);
+            commit<CTAS>(&ax->s_full[(g + j) & 1]);
+            st.next(a.stages);
+          }
+          if (j >= 1) {
+            const uint32_t t = g + j - 1;
+            if (j == 1 && np > 0) ok = tc::bar_wait(&ax->o_free, (np - 1) & 1, abort, CTAS == 2);
+            ok = ok && tc::bar_wait(&ax->p_full[t & 1], (t >> 1) & 1, abort, CTAS == 2);
+            ok = ok && tc::bar_wait(&ax->kv_full[st.s], st.ph, abort, CTAS == 2);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t kv = aKV + st.s * STAGE;
+            const uint32_t p = tm + kSCol + (t & 1) * 128;
+#pragma unroll
+            for (int x = 0; x < KT / 16; x++)
+              mma_ts<CTAS>(tm, p + 8 * x, tc::sw128_desc(kv + x * 2 * SBO_V, 1024, SBO_V), id_pv, j > 1 || x > 0);
+            commit<CTAS>(&ax->kv_empty[st.s]);
+            commit<CTAS>(&ax->pv_done[t & 1]);
+            st.next(a.stages);
+          }
+        }
+        g += n;
+        np++;
+      }
+      if (!ok) set_status(a.status, SKV_DEV_TIMEOUT);
+      if (rank == 0) commit<CTAS>(&ax->mma_idle);  // nothing of this thread's may run when tensor memory is released
+      if (!tc::bar_drain(&ax->mma_idle, 0, 4000000000ull)) set_status(a.status, SKV_DEV_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---------------- int8: row scales (warp 2 even tiles, warp 3 odd) ----------------
+    if (INT8) {
+      uint32_t g = 0;  // tiles so far
+      bool ok = true;
+      for (int k = 0; ok; k++) {
+        const int slot = k % kPieces;
+        ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->pc_full[slot], (k / kPieces) & 1, abort));
+        if (!ok) break;
+        const Piece pc = ax->pc[slot];
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&ax->pc_empty[slot]);
+        if (pc.last) break;
+        const int64_t p_hi = pc.pos0 + pc.rows / a.G - 1;
+        auto row_of = [&](int j, int e) -> int64_t {  // pool row of key lane + 32 e of tile j, -1: none
+          if (j >= pc.n) return -1;
+          const int tl = pc.j0 + j < pc.nsink ? pc.j0 + j : pc.lo + pc.j0 + j - pc.nsink;
+          const int64_t t = static_cast<int64_t>(tl) * KT + lane + 32 * e, pg = t / a.page;
+          if (t > p_hi || pg >= a.n_pages) return -1;
+          const int blk = a.block_table[pc.b * a.n_pages + pg];
+          return blk >= 0 && blk < a.n_blocks ? static_cast<int64_t>(blk) * a.page + t % a.page : -1;
+        };
+        int j = static_cast<int>((g ^ (warp & 1)) & 1);  // first tile of this warp's parity
+        int64_t row[KT / 32];
+#pragma unroll
+        for (int e = 0; e < KT / 32; e++) row[e] = row_of(j, e);
+        for (; j < pc.n; j += 2) {
+          float ks[KT / 32], vs[KT / 32];
+#pragma unroll
+          for (int e = 0; e < KT / 32; e++) {
+            const int64_t vec = row[e] * a.Hkv + pc.h;
+            ks[e] = row[e] >= 0 ? __half2float(a.k_scale[vec]) * a.scale_log2 : 0.f;
+            vs[e] = row[e] >= 0 ? __half2float(a.v_scale[vec]) : 0.f;
+            row[e] = row_of(j + 2, e);
+          }
+          const uint32_t t = g + j, s = t % kScaleRing;
+          if (t >= kScaleRing) ok = __all_sync(0xffffffffu, tc::bar_wait(&a8->sc_empty[s], (t / kScaleRing - 1) & 1, abort));
+          if (!ok) break;
+#pragma unroll
+          for (int e = 0; e < KT / 32; e++) {
+            a8->ks[s][lane + 32 * e] = ks[e];
+            a8->vs[s][lane + 32 * e] = vs[e];
+          }
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&a8->sc_full[s]);
+        }
+        g += pc.n;
+      }
+    }
+  } else if (warp < 8) {
+    // ---------------- softmax and output: thread = row ----------------
+    const int r = tid - 128;                        // row within this CTA
+    const int rt = static_cast<int>(rank) * kRows + r;  // row within the tile
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const int warp_row = static_cast<int>(rank) * kRows + 32 * (warp & 3);
+    uint32_t g = 0, fills = 0;
+    bool ok = true;
+
+    // Query rows of a piece: 16-byte copies into the swizzled tile.
+    auto load_q = [&](const Piece& pc) {
+      constexpr int CH = D / 8;
+      const int rows = min(kRows, pc.rows - static_cast<int>(rank) * kRows);
+      for (int i = r; i < rows * CH; i += 128) {
+        const int row = i / CH, ch = i % CH, rr = static_cast<int>(rank) * kRows + row;
+        const int tok = pc.tok0 + rr / a.G;
+        const uint16_t* src = a.q + tok * a.q_stride + static_cast<int64_t>(pc.h * a.G + rr % a.G) * D + ch * 8;
+        const uint32_t dst = tc::smem_addr(sQ) + (row >> 3) * SBO_K + (ch >> 3) * 1024 + (row & 7) * 128 +
+                             (((ch & 7) ^ (row & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto q_ready = [&]() {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_leader<CTAS>(&ax->q_full);
+    };
+    auto get = [&](int k, Piece& pc) -> bool {  // descriptor k; empty ones are handed on after use
+      const int slot = k % kPieces;
+      if (!__all_sync(0xffffffffu, tc::bar_wait(&ax->pc_full[slot], (k / kPieces) & 1, abort))) return false;
+      pc = ax->pc[slot];
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&ax->pc_empty[slot]);
+      return true;
+    };
+
+    Piece pc;
+    ok = get(0, pc);
+    bool q_loaded = false;
+    for (int k = 0; ok && !pc.last; k++) {
+      Piece next;
+      next.last = 1;
+      const int tok_i = rt / a.G;
+      const bool live = rt < pc.rows;
+      const int p = live ? pc.pos0 + tok_i : -1;   // this row's position: keys 0 .. p
+      const bool warp_live = warp_row < pc.rows;
+      float m_ref = -INFINITY, l = 0.f;
+      bool have_next = false;
+      if (pc.n > 0 && !q_loaded) {
+        load_q(pc);
+        q_ready();
+      }
+      q_loaded = false;
+      const int p_last = pc.pos0 + pc.rows / a.G - 1;
+      for (int j = 0; ok && j < pc.n; j++) {
+        const uint32_t t = g + j;
+        const int tl = pc.j0 + j < pc.nsink ? pc.j0 + j : pc.lo + pc.j0 + j - pc.nsink;
+        const int t0 = tl * KT;
+        ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->s_full[t & 1], (t >> 1) & 1, abort));
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint32_t bad = ax->tile_bad[t % kTileInfo];
+        // every row of the tile sees every key unless one of these holds
+        const bool masked = t0 + KT - 1 > pc.pos0 || bad != 0 ||
+                            (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S);
+        const uint32_t scol = tm + lane_base + kSCol + (t & 1) * 128;
+        const uint32_t sc = t % kScaleRing;
+        if (INT8) {
+          ok = __all_sync(0xffffffffu, tc::bar_wait(&a8->sc_full[sc], (t / kScaleRing) & 1, abort));
+          if (!ok) break;
+        }
+        if (warp_live) {
+          float x[KT];
+#pragma unroll
+          for (int c0 = 0; c0 < KT; c0 += 32) tc::tmem_ld32(scol + c0, reinterpret_cast<uint32_t(&)[32]>(x[c0]));
+          tc::tmem_wait_ld();
+          if (INT8) {
+#pragma unroll
+            for (int i = 0; i < KT; i += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&a8->ks[sc][i]);
+              x[i] *= f.x;
+              x[i + 1] *= f.y;
+              x[i + 2] *= f.z;
+              x[i + 3] *= f.w;
+            }
+          }
+          if (masked) {
+            const int hi = p - t0, lo = a.W > 0 ? p - a.W - t0 : -1, sk = a.W > 0 ? a.S - t0 : 0;
+#pragma unroll
+            for (int i = 0; i < KT; i++) {
+              const bool see = i <= hi && (i > lo || i < sk) && !((bad >> (i >> 3)) & 1u);
+              x[i] = see ? x[i] : -INFINITY;
+            }
+          }
+          float mp[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < KT; i++) mp[i & 3] = fmaxf(mp[i & 3], x[i]);
+          const float f = INT8 ? 1.f : a.scale_log2;
+          const float mc = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * f;
+          bool rescale = false;
+          float alpha = 1.f;
+          if (mc > m_ref + kLazy || (m_ref == -INFINITY && mc > m_ref)) {
+            alpha = tc::ex2_approx(m_ref - mc);
+            rescale = j > 0;
+            m_ref = mc;
+          }
+          if (__any_sync(0xffffffffu, rescale)) {
+            ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort));
+            if (!ok) break;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
+              tc::tmem_ld32(tm + lane_base + c0, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tc::tmem_st32(tm + lane_base + c0, o);
+            }
+            l *= alpha;
+          }
+          const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t pk[KT / 2];
+#pragma unroll
+          for (int i = 0; i < KT; i += 2) {
+            float p0 = tc::ex2_approx(fmaf(x[i], f, -m_use)), p1 = tc::ex2_approx(fmaf(x[i + 1], f, -m_use));
+            if (INT8) {
+              ls[(i >> 1) & 3] += p0 + p1;
+              float v0 = p0 * a8->vs[sc][i], v1 = p1 * a8->vs[sc][i + 1];
+              if (masked) {  // a scale that this row does not see may be anything
+                v0 = x[i] == -INFINITY ? 0.f : v0;
+                v1 = x[i + 1] == -INFINITY ? 0.f : v1;
+              }
+              pk[i >> 1] = pack_bf16(v0, v1);
+            } else {
+              const uint32_t w = pack_bf16(p0, p1);
+              pk[i >> 1] = w;
+              ls[(i >> 1) & 3] += __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
+            }
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+#pragma unroll
+          for (int c0 = 0; c0 < KT / 2; c0 += 32) tc::tmem_st32(scol + c0, reinterpret_cast<uint32_t(&)[32]>(pk[c0]));
+          tc::tmem_wait_st();
+        }  // a warp without rows leaves S as its weights: rows are independent, and its are not used
+        if (!INT8 && masked) {
+          // Zero weights do not stop a NaN: rows of V without a token become
+          // zero, and so does every value that is not finite (put back for
+          // the queries that see it by the non-finite pass below).
+          const uint32_t fv = fills + fill_v(j, pc.n);
+          const uint32_t vs = fv % a.stages;
+          ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->kv_full[vs], (fv / a.stages) & 1, abort, CTAS == 2));
+          if (!ok) break;
+          unsigned char* V = sKV + vs * STAGE;
+          bool found = false;
+          for (int i = r; i < STAGE / 16; i += 128) {
+            const int grp = i / (VSUB * 64), row = grp * 8 + ((i >> 3) & 7);  // 64 16-byte pieces per 1024 B block
+            uint4* at = reinterpret_cast<uint4*>(V + i * 16);
+            const int key = t0 + row;  // seen by no query of the tile: its page may not have been read
+            const bool dead = key > p_last || (a.W > 0 && key <= pc.pos0 - a.W && key >= a.S) || ((bad >> grp) & 1u);
+            uint4 w = dead ? make_uint4(0u, 0u, 0u, 0u) : *at;
+            uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+            bool change = dead;
+#pragma unroll
+            for (int y = 0; y < 4; y++) {
+              if ((e[y] & 0x7f80u) == 0x7f80u) {
+                e[y] &= 0xffff0000u;
+                change = found = true;
+              }
+              if ((e[y] & 0x7f800000u) == 0x7f800000u) {
+                e[y] &= 0x0000ffffu;
+                change = found = true;
+              }
+            }
+            if (change) *at = w;
+          }
+          if (found) {
+            *reinterpret_cast<volatile int*>(&ax->dirty) = 1;
+            if (CTAS == 2)
+              asm volatile(
+                  "{\n.reg .b32 ra;\nmapa.shared::cluster.u32 ra, %0, %1;\nst.shared::cluster.u32 [ra], %2;\n}\n" ::"r"(
+                      tc::smem_addr(&ax->dirty)),
+                  "r"(rank ^ 1u), "r"(1)
+                  : "memory");
+          }
+          tc::fence_async_smem();
+        }
+        if (INT8) {
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&a8->sc_empty[sc]);
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader<CTAS>(&ax->p_full[t & 1]);
+      }
+      if (!ok) break;
+      // The last logits have been read, so the query tile is free: fetch the next one under the last product.
+      ok = get(k + 1, next);
+      if (!ok) break;
+      have_next = !next.last && next.n > 0 && pc.n > 0;
+      if (have_next) load_q(next);
+      if (pc.n > 0) {
+        const uint32_t t = g + pc.n - 1;
+        ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->pv_done[t & 1], (t >> 1) & 1, abort));
+        if (!ok) break;
+        tc::tc_fence_after();
+      }
+      if (have_next) {
+        q_ready();
+        q_loaded = true;
+      }
+      // ---- output ----
+      if (warp_live) {
+        const bool whole = pc.slot < 0;
+        const float inv = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+        const bool dirty = !INT8 && *reinterpret_cast<volatile int*>(&ax->dirty) != 0;
+        const int64_t tok = static_cast<int64_t>(pc.tok0) + tok_i;
+        uint16_t* orow = a.out + (tok * (a.Hkv * a.G) + pc.h * a.G + rt % a.G) * D;
+        const int64_t prow = static_cast<int64_t>(pc.slot) * a.part_rows + rt;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          __syncwarp();
+          if (pc.n > 0) {
+            tc::tmem_ld32(tm + lane_base + c0, o);
+            tc::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i++) o[i] = 0u;
+          }
+          if (dirty && live) {
+            for (int j = 0; j < pc.n; j++) {
+              const int tl = pc.j0 + j < pc.nsink ? pc.j0 + j : pc.lo + pc.j0 + j - pc.nsink;
+              const int t0 = tl * KT;
+              if (!(t0 + KT - 1 > pc.pos0 || (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S))) {
+                // unmasked: its values went through the products as they are, unless a page of it is bad
+                bool gap = false;
+                for (int x = 0; x < KT; x += 8) {
+                  const int64_t pg = (static_cast<int64_t>(t0) + x) / a.page;
+                  const int blk = pg < a.n_pages ? a.block_table[pc.b * a.n_pages + pg] : -1;
+                  gap |= blk < 0 || blk >= a.n_blocks;
+                }
+                if (!gap) continue;
+              }
+              for (int x = 0; x < KT; x++) {
+                const int key = t0 + x;
+                if (key > p || !(a.W == 0 || key > p - a.W || key < a.S)) continue;
+                const int64_t pg = key / a.page;
+                const int blk = pg < a.n_pages ? a.block_table[pc.b * a.n_pages + pg] : -1;
+                if (blk < 0 || blk >= a.n_blocks) continue;
+                const uint16_t* v = a.v_pool + ((static_cast<int64_t>(blk) * a.page + key % a.page) * a.Hkv + pc.h) * D + c0;
+#pragma unroll
+                for (int i = 0; i < 32; i++)
+                  if ((v[i] & 0x7f80u) == 0x7f80u)
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) + bf16_bits_to_f32(v[i]));
+              }
+            }
+          }
+          if (!live) continue;
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 w;
+              w.x = pack_bf16(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+              w.y = pack_bf16(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+              w.z = pack_bf16(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
+              w.w = pack_bf16(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+              *reinterpret_cast<uint4*>(orow + c0 + i) = w;
+            }
+          } else if (pc.n > 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(a.ws_o + prow * D + c0 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        if (!whole && live) a.ws_ml[prow] = make_float2(m_ref, l);
+      }
+      if (pc.n > 0) {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader<CTAS>(&ax->o_free);
+      }
+      g += pc.n;
+      fills += 2 * pc.n;
+      pc = next;
+    }
+    if (!ok) {
+      if (lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  } else if (INT8) {
+    // ---------------- int8 -> bf16 (warps 8-11) ----------------
+    const int ct = tid - 256;
+    Ring st, sg;
+    uint32_t uses = 0;
+    bool ok = true;
+    for (int k = 0; ok; k++) {
+      const int slot = k % kPieces;
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->pc_full[slot], (k / kPieces) & 1, abort));
+      if (!ok) break;
+      const int n = ax->pc[slot].n, last = ax->pc[slot].last;
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&ax->pc_empty[slot]);
+      if (last) break;
+      for (int f = 0; f < 2 * n; f++) {
+        const bool is_v = !(f == 0 || ((f & 1) && f != 2 * n - 1));
+        ok = __all_sync(0xffffffffu, tc::bar_wait(&a8->st_full[sg.s], sg.ph, abort));
+        if (ok && uses >= static_cast<uint32_t>(a.stages))
+          ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->kv_empty[st.s], st.ph ^ 1, abort));
+        if (!ok) break;
+        const unsigned char* src = sI8 + sg.s * (STAGE / 2);
+        unsigned char* dst = sKV + st.s * STAGE;
+        // Thread -> 16 codes of one row: lane % 8 is the row of its 8-row
+        // group, so eight lanes read eight rows' swizzled pieces (distinct
+        // banks) and write them the same way.
+        auto widen = [&](int row_bytes_log) {
+          const int pcs = 1 << (row_bytes_log - 4);  // 16-code pieces per row
+          const int nsub = row_bytes_log == 6 ? 1 : (1 << row_bytes_log) / 64;
+#pragma unroll 4
+          for (int i = ct; i < STAGE / 32; i += 128) {
+            const int row = (i & 7) + 8 * ((i >> 3) / pcs), pce = (i >> 3) % pcs;
+            const unsigned char* s;
+            if (row_bytes_log == 6)  // 64-byte rows, 64-byte swizzle
+              s = src + row * 64 + ((pce ^ ((row >> 1) & 3)) << 4);
+            else  // [8-row group][128-byte block][8 rows], 128-byte swizzle
+              s = src + (((row >> 3) << (row_bytes_log - 7)) + (pce >> 3)) * 1024 + (row & 7) * 128 +
+                  (((pce & 7) ^ (row & 7)) << 4);
+            const uint4 w = *reinterpret_cast<const uint4*>(s);
+            unsigned char* d = dst + ((row >> 3) * nsub + (pce >> 2)) * 1024 + (row & 7) * 128;
+            const int ch = (pce & 3) * 2;
+            *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) =
+                make_uint4(int8_to_bf16x2<0>(w.x), int8_to_bf16x2<1>(w.x), int8_to_bf16x2<0>(w.y), int8_to_bf16x2<1>(w.y));
+            *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) << 4)) =
+                make_uint4(int8_to_bf16x2<0>(w.z), int8_to_bf16x2<1>(w.z), int8_to_bf16x2<0>(w.w), int8_to_bf16x2<1>(w.w));
+          }
+        };
+        constexpr int LD = D == 256 ? 8 : 7;
+        if (is_v && CTAS == 2)
+          widen(LD - 1);
+        else
+          widen(LD);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::bar_arrive(&a8->st_empty[sg.s]);
+          arrive_leader<CTAS>(&ax->kv_full[st.s]);
+        }
+        uses++;
+        st.next(a.stages);
+        sg.next(a.staging);
+      }
+    }
+    if (!ok && lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
+  }
+
+  __syncwarp();
+  tc::tc_fence_before();
+  if (CTAS == 2)
+    tc::cluster_sync();  // no CTA leaves while its peer may still signal it
+  else
+    __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    if (CTAS == 1)
+      tc::tmem_dealloc<512>(tm);
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tm));
+  }
+  if (CTAS == 2) tc::cluster_sync();
+}
+
+// Joins the pieces of split items, one warp per row, in piece order.
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head, const int4* __restrict__ item,
+                                                    const float2* __restrict__ ml, const float* __restrict__ o,
+                                                    int part_rows, int G, int Hq, uint16_t* __restrict__ out) {
+  constexpr int E = D / 32;
+  grid_dependency_wait();  // launched early: the partials are complete from here on
+  const int lane = threadIdx.x & 31;
+  const int64_t tasks = static_cast<int64_t>(head[0]) * part_rows;
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); w < tasks;
+       w += static_cast<int64_t>(gridDim.x) * 8) {
+    const int64_t it = w / part_rows;
+    const int row = static_cast<int>(w - it * part_rows);
+    const int4 x = item[2 * it];
+    const int n = item[2 * it + 1].x;
+    if (row >= x.y) continue;
+    const int64_t first = static_cast<int64_t>(x.w) * part_rows + row;
+    float m = -INFINITY;
+    for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[first + static_cast<int64_t>(s) * part_rows].x);
+#pragma unroll
+    for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+    float den = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; e++) acc[e] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < n; s++) {
+      const int64_t at = first + static_cast<int64_t>(s) * part_rows;
+      const float2 v = ml[at];
+      if (v.x == -INFINITY && v.y == 0.f) continue;  // no visible key in this piece (its O may be unwritten)
+      const float f = exp2f(v.x - m);
+      den += f * v.y;
+      const float* src = o + at * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src + e);
+        acc[e] += f * y.x;
+        acc[e + 1] += f * y.y;
+        acc[e + 2] += f * y.z;
+        acc[e + 3] += f * y.w;
+      }
+    }
+    const float inv = den != 0.f ? 1.f / den : 0.f;
+    uint16_t* dst = out + (static_cast<int64_t>(x.x + row / G) * Hq + x.z * G + row % G) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+// ---- host ------------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::atomic<EncodeFn> fn{nullptr};
+  EncodeFn f = fn.load(std::memory_order_acquire);
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult res;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &res) != cudaSuccess ||
+      res != cudaDriverEntryPointSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  f = reinterpret_cast<EncodeFn>(p);
+  fn.store(f, std::memory_order_release);
+  return f;
+}
+
+// Rows as [KV head][8-row group][column block][8 rows][column block's values]:
+// a box of `rows` rows and `subs` column blocks lands as the tensor cores read it.
+bool encode_rows(CUtensorMap* map, const void* pool, bool int8, int Hkv, int d, int64_t n_rows, int block, int subs,
+                 int rows) {
+  const int es = int8 ? 1 : 2;
+  const cuuint64_t pitch = static_cast<cuuint64_t>(Hkv) * d * es;
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(block), 8, static_cast<cuuint64_t>(d / block),
+                              static_cast<cuuint64_t>(n_rows / 8), static_cast<cuuint64_t>(Hkv)};
+  const cuuint64_t strides[4] = {pitch, static_cast<cuuint64_t>(block) * es, 8 * pitch,
+                                 static_cast<cuuint64_t>(d) * es};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(block), 8, static_cast<cuuint32_t>(subs),
+                             static_cast<cuuint32_t>(rows / 8), 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return encode_fn()(map, int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                     const_cast<void*>(pool), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     block * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Layout {  // workspace
+  int max_split, part_rows;
+  size_t item, ml, o, total;
+};
+
+// Rows of a query tile that can hold a token: the tile's tokens, or all there are.
+int tile_rows(int n_tok, int G, int ctas) {
+  const int tpt = ctas * kRows / G;
+  return (n_tok < tpt ? n_tok : tpt) * G;
+}
+
+Layout layout(int n_tok, int G, int d, int ctas, int sms) {
+  Layout w;
+  w.max_split = kSplitPerSm * sms / ctas;
+  w.part_rows = tile_rows(n_tok, G, ctas);
+  w.item = 256;
+  w.ml = w.item + static_cast<size_t>(w.max_split) * 2 * sizeof(int4);
+  w.o = w.ml + ((static_cast<size_t>(w.max_split) * w.part_rows * sizeof(float2) + 255) & ~static_cast<size_t>(255));
+  w.total = w.o + static_cast<size_t>(w.max_split) * w.part_rows * d * sizeof(float);
+  return w;
+}
+
+template <int D, int CTAS, bool INT8>
+int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int smem, int sms, cudaStream_t st) {
+  static std::atomic<int> configured[kMaxDevices];
+  auto kernel = paged_kernel<D, CTAS, INT8>;
+  if (smem_limit_once(configured, kernel, kMaxSmem) != SKV_OK) return SKV_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms / CTAS * CTAS, 1, 1);
+  cfg.blockDim = dim3(INT8 ? 384 : 256, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CTAS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, km, vm, a) != cudaSuccess) {
+    cudaGetLastError();
+    return SKV_ECUDA;
+  }
+  cfg.gridDim = dim3(2 * sms, 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  const int* head = a.ws_head;
+  const int4* item = a.ws_item;
+  const float2* ml = a.ws_ml;
+  const float* o = a.ws_o;
+  if (cudaLaunchKernelEx(&cfg, merge_kernel<D>, head, item, ml, o, a.part_rows, a.G, a.Hkv * a.G, a.out) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return SKV_ECUDA;
+  }
+  return SKV_OK;
+}
+
+template <int D, int CTAS>
+int launch_kind(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, bool int8, int smem, int sms,
+                cudaStream_t st) {
+  return int8 ? launch<D, CTAS, true>(a, km, vm, smem, sms, st) : launch<D, CTAS, false>(a, km, vm, smem, sms, st);
+}
+
+// CTA pairs from about two query tiles of rows per request on.
+int ctas_for(int B, int n_tok, int G, bool single) {
+  return !single && static_cast<int64_t>(n_tok) * G > static_cast<int64_t>(B) * kRows ? 2 : 1;
 }
 
 }  // namespace
@@ -121,7 +1250,10 @@ using namespace skv;
 
 SKV_EXPORT size_t skv_paged_attend_workspace_size(int B, int n_tok, int Hq, int Hkv, int d) {
   if (B < 1 || n_tok < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv || Hq / Hkv > 128 || (d != 128 && d != 256)) return 0;
-  return 16;
+  const int sms = sm_count() > 0 ? sm_count() : 152;
+  const int G = Hq / Hkv;
+  const size_t one = layout(n_tok, G, d, 1, sms).total, two = layout(n_tok, G, d, 2, sms).total;
+  return one > two ? one : two;
 }
 
 SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, int d, const uint16_t* q,
@@ -131,31 +1263,94 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
                                 float softmax_scale, uint16_t* out, void* workspace, size_t workspace_bytes,
                                 int32_t* dev_status, void* stream) {
   if (kv_kind != SKV_KV_BF16 && kv_kind != SKV_KV_INT8) return SKV_EINVAL;
-  if (B < 0 || B > 4096 || n_tok < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || S < 0 || W < 0 || n_pages < 0) return SKV_EINVAL;
+  if (B < 0 || B > 4096 || n_tok < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || S < 0 || W < 0 || n_pages < 0)
+    return SKV_EINVAL;
   if ((d != 128 && d != 256) || Hq / Hkv > 128 || page < 8 || page % 8) return SKV_EUNSUPPORTED;
   if (B == 0 || n_tok == 0) return SKV_OK;
   if (!q || !k_pool || !v_pool || !block_table || !lengths || !out || n_pages < 1 || n_pool_rows < page)
     return SKV_EINVAL;
-  if (kv_kind == SKV_KV_INT8 && (!k_scale || !v_scale)) return SKV_EINVAL;
+  const bool int8 = kv_kind == SKV_KV_INT8;
+  if (int8 && (!k_scale || !v_scale)) return SKV_EINVAL;
   if (!q_start && n_tok != B) return SKV_EINVAL;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || q_stride % 8 ||
       q_stride < static_cast<int64_t>(Hq) * d)
     return SKV_EINVAL;
+  if (!(softmax_scale > 0.f) || softmax_scale > 3.0e38f) return SKV_EINVAL;
+  // 32-bit positions, tile coordinates and work-list counts
+  if (n_pages * page > INT32_MAX - 1024 || n_pool_rows > (static_cast<int64_t>(1) << 33)) return SKV_EINVAL;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < skv_paged_attend_workspace_size(B, n_tok, Hq, Hkv, d))
     return SKV_ENOMEM;
-  PagedArgs a{B, n_tok, Hq, Hkv, q, q_stride, k_pool, v_pool, reinterpret_cast<const __half*>(k_scale),
-              reinterpret_cast<const __half*>(v_scale), n_pool_rows / page, page, block_table, n_pages, q_start,
-              lengths, S, W, softmax_scale * kLog2e, out, dev_status};
-  const dim3 grid(n_tok, Hq);
+  const int sms = sm_count();
+  if (sms <= 1 || !encode_fn()) return SKV_ECUDA;
+  const int G = Hq / Hkv;
+  const int ctas = ctas_for(B, n_tok, G, !q_start);
+  const int stage = 64 * d * 2;
+
+  PagedArgs a{};
+  a.B = B;
+  a.n_tok = n_tok;
+  a.Hkv = Hkv;
+  a.G = G;
+  a.tpt = ctas * kRows / G;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.v_pool = int8 ? nullptr : static_cast<const uint16_t*>(v_pool);
+  a.k_scale = reinterpret_cast<const __half*>(k_scale);
+  a.v_scale = reinterpret_cast<const __half*>(v_scale);
+  a.n_blocks = n_pool_rows / page;
+  a.page = page;
+  a.rb = 8;  // rows per box: the largest power of two up to 64 that divides the page
+  while (a.rb < 64 && page % (2 * a.rb) == 0) a.rb *= 2;
+  a.block_table = block_table;
+  a.n_pages = n_pages;
+  a.q_start = q_start;
+  a.lengths = lengths;
+  a.S = S;
+  a.W = W;
+  a.scale_log2 = softmax_scale * kLog2e;
+  a.out = out;
+  a.status = dev_status;
+  const Layout w = layout(n_tok, G, d, ctas, sms);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.part_rows = w.part_rows;
+  a.max_split = w.max_split;
+  a.ws_head = reinterpret_cast<int*>(ws);
+  a.ws_item = reinterpret_cast<int4*>(ws + w.item);
+  a.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.ws_o = reinterpret_cast<float*>(ws + w.o);
+
+  // Shared memory: the query rows that can hold a token (the products read
+  // 128 rows from there on; what they read past these is never used), then as
+  // many stages as fit.
+  const int q_rows = q_start ? tile_rows(n_tok, G, ctas) : G;
+  a.q_bytes = ((q_rows < kRows ? q_rows : kRows) + 7) / 8 * 8 * d * 2;
+  const int aux = static_cast<int>(sizeof(Aux)) + (int8 ? static_cast<int>(sizeof(Aux8)) : 0);
+  const int room = kMaxSmem - 1024 - aux - a.q_bytes;
+  if (int8) {
+    a.stages = ctas == 2 ? 3 : 4;
+    if (d == 128) a.stages *= 2;
+    a.staging = (room - a.stages * stage) / (stage / 2);
+    if (a.staging > kMaxStaging) a.staging = kMaxStaging;
+  } else {
+    a.stages = room / stage;
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+  }
+  const int smem = 1024 + a.q_bytes + a.stages * stage + a.staging * (stage / 2) + aux;
+
+  CUtensorMap km, vm;
+  const int block = int8 ? 128 : 64;                         // columns of a 128-byte block
+  const int vcols = d / ctas, vblock = vcols < block ? vcols : block;
+  if (!encode_rows(&km, k_pool, int8, Hkv, d, n_pool_rows, block, d / block, a.rb) ||
+      !encode_rows(&vm, v_pool, int8, Hkv, d, n_pool_rows, vblock, vcols / vblock, a.rb))
+    return SKV_ECUDA;
   cudaStream_t st = as_stream(stream);
-  if (d == 128 && kv_kind == SKV_KV_BF16)
-    paged_kernel<128, false><<<grid, kThreads, 0, st>>>(a);
-  else if (d == 128)
-    paged_kernel<128, true><<<grid, kThreads, 0, st>>>(a);
-  else if (kv_kind == SKV_KV_BF16)
-    paged_kernel<256, false><<<grid, kThreads, 0, st>>>(a);
+  int e;
+  if (d == 128)
+    e = ctas == 2 ? launch_kind<128, 2>(a, km, vm, int8, smem, sms, st)
+                  : launch_kind<128, 1>(a, km, vm, int8, smem, sms, st);
   else
-    paged_kernel<256, true><<<grid, kThreads, 0, st>>>(a);
-  return launch_status();
+    e = ctas == 2 ? launch_kind<256, 2>(a, km, vm, int8, smem, sms, st)
+                  : launch_kind<256, 1>(a, km, vm, int8, smem, sms, st);
+  return e;
 }

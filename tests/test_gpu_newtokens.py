@@ -239,8 +239,10 @@ class Case:
         got = f64(out)
         assert (got[m:] == 123).all()  # rows behind the last request are left as they were
         err, tol = np.abs(got[:m] - ref), 2.0 ** -8 * np.abs(ref) + 2 * (2.0 ** -8 + 2.0 ** -10) * (spread + np.abs(ref))
-        assert np.isfinite(got).all()
-        assert (err <= tol).all(), (err / np.maximum(tol, 1e-300)).max()
+        finite = bool(np.isfinite(got).all())
+        assert finite
+        worst = float((err / np.maximum(tol, 1e-300)).max())
+        assert worst <= 1
 
 
 KINDS = ["bf16", "int8"]

@@ -49,7 +49,8 @@ ATT = dict(kind=0, B=2, n_tok=6, Hq=8, Hkv=2, d=256, q=P(256), qs=2048, kp=P(256
     (dict(vp=P(8)), EINVAL), (dict(table=None), EINVAL), (dict(n_pages=0), EINVAL), (dict(lengths=None), EINVAL),
     (dict(out=P(8)), EINVAL), (dict(n_rows=15), EINVAL), (dict(kind=1), EINVAL), (dict(kind=1, ksc=P(256)), EINVAL),
     (dict(q_start=None), EINVAL), (dict(qs=2044), EINVAL), (dict(qs=1024), EINVAL), (dict(ws=None), ENOMEM),
-    (dict(wsn=8), ENOMEM), (dict(ws=P(8)), ENOMEM),
+    (dict(wsn=8), ENOMEM), (dict(ws=P(8)), ENOMEM), (dict(scale=0.0), EINVAL), (dict(scale=-1.0), EINVAL),
+    (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(n_pages=1 << 28), EINVAL),
 ])
 def test_paged_attend_refuses(lib, change, want):
     assert lib.skv_paged_attend(*{**ATT, **change}.values()) == want
