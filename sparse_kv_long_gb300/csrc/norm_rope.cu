@@ -9,17 +9,27 @@
 //   q_out = bf16(z); a key is bf16(z), then the cache's row encoding.
 //
 // The angle.  A position of a million at frequency 1 needs t mod 2 pi to 1e-7
-// of a turn: 45 bits.  inv_freq / 2 pi (fp64, once per thread) is kept as a
-// 64-bit fixed-point fraction of a turn; p times it modulo 2^64 is the angle
-// modulo one turn, exactly as unsigned integers wrap, and its top 32 bits go
-// to sincospif.  Error: 2^-26 of a turn from the fp32 argument, plus
-// |p| * inv_freq / 2 pi * 2^-53 turns from the fp64 quotient.
+// of a turn: 45 bits.  inv_freq / 2 pi is kept as a 64-bit fixed-point
+// fraction of a turn, made with integers (the fp32 mantissa times 2^66 / 2 pi,
+// shifted; this GPU's fp64 rate would cost more than the whole pass).  p times
+// it modulo 2^64 is the angle modulo one turn, exactly as unsigned integers
+// wrap, and its top 32 bits go to sincospif: 2^-26 of a turn from the fp32
+// argument, |p| 2^-64 from the fraction.
 //
-// Bound: memory.  Every value is read once and written once, 16 bytes per
-// lane; d / 8 lanes share a head, so a head's sum is a shuffle reduction and
-// no value passes through shared memory.  A warp takes a token's heads one
-// after the other and computes the token's sines once; with few tokens a
-// token's heads are spread over several warps instead (launch rule below).
+// Weights and rotation are folded: with wc = w cos and ws = -+ w' sin (w' the
+// partner's weight) a value is inv (x wc + x' ws), x' the partner's input.
+//
+// A lane holds both members of its pairs: four dims x of a head and their
+// partners x + rot/2 (eight consecutive dims where pairs are neighbours or
+// nothing is rotated), so the rotation needs no exchange and the products run
+// two to an instruction (f32x2).
+//
+// Bound: memory, then instruction issue (about 60 per head and warp): every
+// value is read once and written once; d / 8 lanes share a head, so a head's
+// sum is a shuffle reduction and no value passes through shared memory.  A
+// warp takes a token's heads one after the other, four in flight, and
+// computes the token's sines once; with few tokens a token's heads are spread
+// over several warps instead (launch rule below).
 #include "common.cuh"
 
 namespace skv {
@@ -27,14 +37,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 4;
 constexpr int kBatch = 4;  // heads per lane group whose loads are in flight together
 
 struct NormArgs {
   int64_t n_tok;
   int Hq, Hkv, rot;
-  int slots;        // heads handled per token: those of q, then of k, then of v that are given
-  int slots_q, slots_k;
-  int chunk, chunks;  // heads per work item, work items per token
+  int steps_q, steps_k, steps_v;  // warp steps (32 lanes: 256 / d heads) per token; 0: part left out
+  int chunk, chunks;              // steps per work item, work items per token
   const uint16_t *q, *k, *v;
   int64_t q_stride, k_stride, v_stride;
   const float *q_weight, *k_weight;
@@ -49,188 +59,273 @@ struct NormArgs {
   int32_t* status;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int e = 0; e < 4; e++) {
-    x[2 * e] = __uint_as_float(w[e] << 16);
-    x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-  }
+// Two fp32 values in one 64-bit register.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2_out(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ F2 unpack2(uint32_t w) {
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint32_t pack2(F2 a) {
+  const float2 x = f2_out(a);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One lane's 8 values of an int8 row: scale = fp16(max|x| / 127) over the
-// head's lanes, codes = rint(x / scale), as skv_quantize_int8_rows.
+__device__ __forceinline__ uint2 ld_stream8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// A lane's eight values of a head: words 0, 1 at dims xa .., words 2, 3 at dims xb ..
+struct Vals {
+  uint32_t w[4];
+};
+
+// 1 / (2 pi) in units of 2^-66.
+constexpr uint64_t kInvTwoPi = 0xA2F9836E4E44152Aull;
+
+// f / 2 pi modulo one turn, in units of 2^-64 turns (f finite).
+__device__ __forceinline__ uint64_t turn_of(float f) {
+  const uint32_t u = __float_as_uint(f);
+  const int e = max(1, static_cast<int>((u >> 23) & 255u));
+  const uint64_t m = (u & 0x7fffffu) | (((u >> 23) & 255u) ? 0x800000u : 0u);  // f = m 2^(e - 150)
+  const uint64_t lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
+  const int s = 152 - e;  // m kInvTwoPi 2^(e - 150 - 66 + 64)
+  uint64_t t;
+  if (s <= 0)
+    t = s > -64 ? lo << -s : 0;
+  else if (s < 64)
+    t = (lo >> s) | (hi << (64 - s));
+  else
+    t = s < 128 ? hi >> (s - 64) : 0;
+  return u >> 31 ? 0 - t : t;
+}
+
+// A lane's part of an int8 row: scale = fp16(max|x| / 127) over the head's
+// lanes, codes = rint(x / scale), as skv_quantize_int8_rows.  The quotients
+// come from a reciprocal (off by at most 127 * 3 * 2^-24 < 3e-5) unless one
+// lies that near a half-integer, about one head in 40; then from the
+// correctly rounded division.
 template <int LPH>
-__device__ __forceinline__ void store_int8(const uint4& bits, int8_t* codes, __half* scale, bool write, bool first) {
+__device__ __forceinline__ void store_int8(const Vals& z, int8_t* row, int xa, int xb, __half* scale, bool write,
+                                           bool first) {
   float x[8];
-  unpack8(bits, x);
   float m = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[e]));
+  for (int e = 0; e < 4; e++) {
+    x[2 * e] = __uint_as_float(z.w[e] << 16);
+    x[2 * e + 1] = __uint_as_float(z.w[e] & 0xffff0000u);
+    m = fmaxf(m, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+  }
 #pragma unroll
   for (int o = LPH / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const __half sh = __float2half_rn(__fdiv_rn(m, 127.f));
   const float s = __half2float(sh);
   uint32_t w[2] = {0u, 0u};
   if (s != 0.f) {
+    const float inv = __frcp_rn(s);
+    float y[8];
+    bool near = !(s < 3.0e38f);
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-      w[e >> 2] |= static_cast<uint32_t>(rint_clamp(__fdiv_rn(x[e], s), -127, 127) & 255) << (8 * (e & 3));
+    for (int e = 0; e < 8; e++) {
+      y[e] = x[e] * inv;
+      near |= !(fabsf(y[e] - rintf(y[e])) < 0.49995f);  // also where x is not finite
+    }
+    if (near) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) y[e] = __fdiv_rn(x[e], s);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) w[e >> 2] |= static_cast<uint32_t>(rint_clamp(y[e], -127, 127) & 255) << (8 * (e & 3));
   }
   if (write) {
-    *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint32_t*>(row + xa) = w[0];
+    *reinterpret_cast<uint32_t*>(row + xb) = w[1];
     if (first) *scale = sh;
   }
 }
 
+enum { kQ = 0, kK = 1, kV = 2 };
+
+// Steps [lo, hi) of one token's heads of one kind.
+template <int D, bool INTER, bool INT8, int KIND>
+__device__ __forceinline__ void run_heads(const NormArgs& a, int64_t tok, int64_t row, bool keep, int lo, int hi,
+                                          int lane, bool rotated, int xa, int xb, const F2 (&wc)[4], const F2 (&ws)[4]) {
+  constexpr int LPH = D / 8, HPW = 32 / LPH;
+  const int grp = lane / LPH;
+  const int H = KIND == kQ ? a.Hq : a.Hkv;
+  const uint16_t* src = KIND == kQ ? a.q + tok * a.q_stride
+                                   : KIND == kK ? a.k + tok * a.k_stride : a.v + tok * a.v_stride;
+  const bool normed = KIND == kQ ? a.q_weight != nullptr : a.k_weight != nullptr;
+  for (int s0 = lo; s0 < hi; s0 += kBatch) {
+    Vals raw[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {  // every load of the batch first
+      const int h = (s0 + u) * HPW + grp;
+      raw[u] = Vals{{0u, 0u, 0u, 0u}};
+      if (s0 + u < hi && (HPW == 1 || h < H)) {
+        const uint2 x = ld_stream8(src + h * D + xa), y = ld_stream8(src + h * D + xb);
+        raw[u] = Vals{{x.x, x.y, y.x, y.y}};
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {
+      if (s0 + u >= hi) break;
+      const int h = (s0 + u) * HPW + grp;
+      const bool live = HPW == 1 || h < H;
+      Vals z = raw[u];
+      if (KIND != kV) {
+        F2 x[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[e] = unpack2(raw[u].w[e]);
+        float inv = 1.f;
+        if (normed) {
+          F2 q2 = f2_mul(x[0], x[0]);
+#pragma unroll
+          for (int e = 1; e < 4; e++) q2 = f2_fma(x[e], x[e], q2);
+          const float2 q = f2_out(q2);
+          float ss = q.x + q.y;
+#pragma unroll
+          for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        }
+        const F2 inv2 = f2(inv, inv);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          F2 o;  // the partners: the other half's, or the pair swapped
+          if (INTER) {
+            const float2 y = f2_out(x[e]);
+            o = f2(y.y, y.x);
+          } else {
+            o = x[e ^ 2];
+          }
+          F2 r = f2_mul(x[e], wc[e]);
+          if (rotated) r = f2_fma(o, ws[e], r);  // else an infinite neighbour would make 0 * inf
+          z.w[e] = pack2(f2_mul(r, inv2));
+        }
+      }
+      if (KIND == kQ) {
+        if (live) {
+          uint16_t* dst = a.q_out + (tok * a.Hq + h) * D;
+          *reinterpret_cast<uint2*>(dst + xa) = make_uint2(z.w[0], z.w[1]);
+          *reinterpret_cast<uint2*>(dst + xb) = make_uint2(z.w[2], z.w[3]);
+        }
+      } else {
+        void* pool = KIND == kK ? a.k_pool : a.v_pool;
+        const int64_t vec = row * a.Hkv + h;
+        if (INT8) {
+          store_int8<LPH>(z, static_cast<int8_t*>(pool) + vec * D, xa, xb, (KIND == kK ? a.k_scale : a.v_scale) + vec,
+                          live && keep, lane % LPH == 0);
+        } else if (live && keep) {
+          uint16_t* dst = static_cast<uint16_t*>(pool) + vec * D;
+          *reinterpret_cast<uint2*>(dst + xa) = make_uint2(z.w[0], z.w[1]);
+          *reinterpret_cast<uint2*>(dst + xb) = make_uint2(z.w[2], z.w[3]);
+        }
+      }
+    }
+  }
+}
+
 template <int D, bool INTER, bool INT8>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormArgs a) {
-  constexpr int LPH = D / 8;    // lanes per head
-  constexpr int HPW = 32 / LPH;  // heads a warp takes at once
-  constexpr int NF = INTER ? 4 : 8;  // frequencies per lane
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const NormArgs a) {
+  constexpr int LPH = D / 8;  // lanes per head
   __shared__ __align__(16) float sw[2][D];
+  __shared__ uint64_t turn[D / 2];
+  __shared__ __align__(16) float2 cs[kWarps][D / 2];  // each warp's token: (cos, sin) by frequency
   for (int x = threadIdx.x; x < D; x += kThreads) {
     sw[0][x] = a.q_weight ? a.q_weight[x] : 1.f;
     sw[1][x] = a.k_weight ? a.k_weight[x] : 1.f;
+    if (x < a.rot / 2) turn[x] = turn_of(a.inv_freq[x]);
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane % LPH, grp = lane / LPH;
-  const int x0 = 8 * sub;  // this lane's dims x0 .. x0 + 7 of its head
-  const bool rotated = x0 < a.rot;
+  const int sub = lane % LPH;
   const int half = a.rot / 2;
-  const bool low = x0 < half;  // half-split pairs: this lane holds the first member
-  const int partner = INTER ? lane : (rotated ? (low ? lane + half / 8 : lane - half / 8) : lane);
-  const int px0 = INTER || !rotated ? x0 : (low ? x0 + half : x0 - half);
-  uint64_t turn[NF];  // inv_freq / 2 pi as a 64-bit fraction of a turn
-#pragma unroll
-  for (int e = 0; e < NF; e++) {
-    turn[e] = 0;
-    if (rotated) {
-      const int f = INTER ? x0 / 2 + e : (low ? x0 : x0 - half) + e;
-      const double t = static_cast<double>(a.inv_freq[f]) * 0.15915494309189535;  // 1 / (2 pi)
-      const double frac = t - floor(t);
-      turn[e] = static_cast<uint64_t>(frac * 18446744073709551616.0);  // 2^64; frac < 1
-    }
-  }
+  const bool rotated = sub < a.rot / 8;
+  // this lane's dims xa .. xa + 3 and xb .. xb + 3, and the frequency of dim xa
+  const int xa = !INTER && rotated ? 4 * sub : 8 * sub, xb = !INTER && rotated ? xa + half : xa + 4;
   __syncthreads();
 
   const int64_t items = a.n_tok * a.chunks;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int off_k = a.steps_q, off_v = off_k + a.steps_k, end = off_v + a.steps_v;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items; item += step) {
-    const int64_t tok = item / a.chunks;
-    const int s0 = static_cast<int>(item - tok * a.chunks) * a.chunk;
-    const int s1 = min(a.slots, s0 + a.chunk);
-    const int64_t pos = a.positions[tok];
+    const int64_t tok = a.chunks == 1 ? item : item / a.chunks;
+    const int p0 = static_cast<int>(item - tok * a.chunks) * a.chunk, p1 = min(end, p0 + a.chunk);
     int64_t row = tok;
     if (a.out_rows) row = a.out_rows[tok];
+    const int32_t pos = a.positions[tok];
     const bool bad = row >= a.n_pool_rows;
-    if (bad && s1 > a.slots_q && lane == 0) set_status(a.status, SKV_DEV_RANGE);
+    if (bad && p1 > off_k && lane == 0) set_status(a.status, SKV_DEV_RANGE);
     const bool keep = row >= 0 && !bad;
-    float co[NF], si[NF];
-    bool have_angles = false;
-
-    for (int sb = s0; sb < s1; sb += HPW * kBatch) {
-      uint4 raw[kBatch];
-      // every load of the batch first
-#pragma unroll
-      for (int u = 0; u < kBatch; u++) {
-        const int s = sb + u * HPW + grp;
-        raw[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (s < s1) {
-          const uint16_t* src;
-          if (s < a.slots_q)
-            src = a.q + tok * a.q_stride + static_cast<int64_t>(s) * D;
-          else if (s < a.slots_q + a.slots_k)
-            src = a.k + tok * a.k_stride + static_cast<int64_t>(s - a.slots_q) * D;
-          else
-            src = a.v + tok * a.v_stride + static_cast<int64_t>(s - a.slots_q - a.slots_k) * D;
-          raw[u] = ld_stream16(src + x0);
-        }
+    if (p0 < off_v) {
+      __syncwarp();  // the previous token's values have been read
+      for (int f = lane; f < half; f += 32) {
+        const uint64_t t = turn[f];
+        const uint32_t lo = static_cast<uint32_t>(t), hi = static_cast<uint32_t>(t >> 32);
+        // top half of the low 64 bits of pos * t (pos sign-extended)
+        uint32_t top = static_cast<uint32_t>(pos) * hi + __umulhi(static_cast<uint32_t>(pos), lo);
+        if (pos < 0) top -= lo;
+        float sn, cn;
+        sincospif(static_cast<float>(static_cast<int32_t>(top)) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
+        cs[warp][f] = make_float2(cn, sn);
       }
-      if (!have_angles) {  // the sines overlap the first batch's loads
-        have_angles = true;
-#pragma unroll
-        for (int e = 0; e < NF; e++) {
-          const uint64_t t = static_cast<uint64_t>(pos) * turn[e];
-          const float h = static_cast<float>(static_cast<int32_t>(t >> 32)) * 4.656612873077393e-10f;  // 2^-31
-          sincospif(h, &si[e], &co[e]);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; u++) {
-        const int s = sb + u * HPW + grp;
-        if (sb + u * HPW >= s1) break;  // uniform in the warp
-        const bool live = s < s1;
-        const bool is_q = s < a.slots_q, is_v = s >= a.slots_q + a.slots_k;
-        const int h = is_q ? s : (is_v ? s - a.slots_q - a.slots_k : s - a.slots_q);
-        uint4 z = raw[u];
-        // A warp of one head (D = 256) skips this for a value; where heads
-        // share a warp all lanes take part in the shuffles.
-        if (HPW > 1 || !is_v) {
-          float x[8];
-          unpack8(raw[u], x);
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-          for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const bool normed = is_q ? a.q_weight != nullptr : a.k_weight != nullptr;
-          const float inv = normed ? rsqrtf(ss * (1.f / D) + a.eps) : 1.f;
-          const float* w = sw[is_q ? 0 : 1];
-          float wv[8];
-          *reinterpret_cast<float4*>(wv) = *reinterpret_cast<const float4*>(w + x0);
-          *reinterpret_cast<float4*>(wv + 4) = *reinterpret_cast<const float4*>(w + x0 + 4);
-          float y[8];
-#pragma unroll
-          for (int e = 0; e < 8; e++) y[e] = x[e] * inv * wv[e];
-          float r[8];
-          if (INTER) {
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-              r[2 * e] = y[2 * e] * co[e % NF] - y[2 * e + 1] * si[e % NF];
-              r[2 * e + 1] = y[2 * e + 1] * co[e % NF] + y[2 * e] * si[e % NF];
-            }
-          } else {
-            uint4 other;  // the pairs' other members, as they were loaded
-            other.x = __shfl_sync(0xffffffffu, raw[u].x, partner);
-            other.y = __shfl_sync(0xffffffffu, raw[u].y, partner);
-            other.z = __shfl_sync(0xffffffffu, raw[u].z, partner);
-            other.w = __shfl_sync(0xffffffffu, raw[u].w, partner);
-            float xo[8], wo[8];
-            unpack8(other, xo);
-            *reinterpret_cast<float4*>(wo) = *reinterpret_cast<const float4*>(w + px0);
-            *reinterpret_cast<float4*>(wo + 4) = *reinterpret_cast<const float4*>(w + px0 + 4);
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-              const float yo = xo[e] * inv * wo[e];
-              const float sn = low ? -si[e % NF] : si[e % NF];
-              r[e] = y[e] * co[e % NF] + yo * sn;
-            }
-          }
-          if (!is_v)
-            z = rotated ? make_uint4(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]), pack_bf16(r[4], r[5]),
-                                     pack_bf16(r[6], r[7]))
-                        : make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                                     pack_bf16(y[6], y[7]));
-        }
-        if (live && is_q)
-          *reinterpret_cast<uint4*>(a.q_out + (tok * a.Hq + h) * D + x0) = z;
-        const bool write = live && !is_q && keep;
-        const int64_t vec = row * a.Hkv + h;
-        if (INT8) {
-          if (HPW > 1 || !is_q)
-            store_int8<LPH>(z, static_cast<int8_t*>(is_v ? a.v_pool : a.k_pool) + vec * D + x0,
-                            (is_v ? a.v_scale : a.k_scale) + vec, write, sub == 0);
-        } else if (write) {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool) + vec * D + x0) = z;
-        }
-      }
+      __syncwarp();
     }
+    F2 wc[4], ws[4];
+    auto fold = [&](const float* w) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const int x = (e < 2 ? xa : xb) + 2 * (e & 1);         // dims x, x + 1
+        const int f = INTER ? x / 2 : xa + 2 * (e & 1);        // frequency of dim x (and, interleaved, of x + 1)
+        float2 c0 = make_float2(1.f, 0.f), c1 = c0;
+        if (rotated) {
+          c0 = cs[warp][f];
+          c1 = INTER ? c0 : cs[warp][f + 1];
+        }
+        wc[e] = f2(w[x] * c0.x, w[x + 1] * c1.x);
+        if (INTER) {
+          ws[e] = f2(-w[x + 1] * c0.y, w[x] * c0.y);
+        } else {
+          const int y = (e < 2 ? xb : xa) + 2 * (e & 1);       // the partners' dims
+          ws[e] = e < 2 ? f2(-w[y] * c0.y, -w[y + 1] * c1.y) : f2(w[y] * c0.y, w[y + 1] * c1.y);
+        }
+      }
+    };
+    if (p0 < off_k) {
+      fold(sw[0]);
+      run_heads<D, INTER, INT8, kQ>(a, tok, row, keep, p0, min(p1, off_k), lane, rotated, xa, xb, wc, ws);
+    }
+    if (p0 < off_v && p1 > off_k) {
+      fold(sw[1]);
+      run_heads<D, INTER, INT8, kK>(a, tok, row, keep, max(p0, off_k) - off_k, min(p1, off_v) - off_k, lane, rotated, xa,
+                                    xb, wc, ws);
+    }
+    if (p1 > off_v)
+      run_heads<D, INTER, INT8, kV>(a, tok, row, keep, max(p0, off_v) - off_v, p1 - off_v, lane, rotated, xa, xb, wc, ws);
   }
 }
 
@@ -284,9 +379,10 @@ SKV_EXPORT int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int r
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.rot = rot;
-  a.slots_q = q ? Hq : 0;
-  a.slots_k = k ? Hkv : 0;
-  a.slots = a.slots_q + a.slots_k + (v ? Hkv : 0);
+  const int hpw = 256 / d;
+  a.steps_q = q ? (Hq + hpw - 1) / hpw : 0;
+  a.steps_k = k ? (Hkv + hpw - 1) / hpw : 0;
+  a.steps_v = v ? (Hkv + hpw - 1) / hpw : 0;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -306,18 +402,25 @@ SKV_EXPORT int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int r
   a.k_scale = reinterpret_cast<__half*>(k_scale);
   a.v_scale = reinterpret_cast<__half*>(v_scale);
   a.status = dev_status;
-  // Work items: enough of them for every resident warp, so a token's heads
-  // are split over up to slots / HPW warps when there are few tokens.
-  const int hpw = 32 / (d / 8);
-  const int64_t warps = static_cast<int64_t>(sms) * 4 * kWarps;
-  const int steps = (a.slots + hpw - 1) / hpw;
-  int64_t chunks = (warps + n_tok - 1) / n_tok;
-  if (chunks > steps) chunks = steps;
-  const int per = static_cast<int>((steps + chunks - 1) / chunks);
-  a.chunk = per * hpw;
-  a.chunks = (steps + per - 1) / per;
+  // Work items: a token's heads in `chunks` parts, so that the rounds of the
+  // resident warps times the steps of a part (each part paying about three
+  // steps for its position and sines) come out lowest.
+  const int64_t warps = static_cast<int64_t>(sms) * kCtasPerSm * kWarps;
+  const int steps = a.steps_q + a.steps_k + a.steps_v;
+  int64_t best = INT64_MAX;
+  for (int c = 1; c <= steps; c++) {
+    const int per = (steps + c - 1) / c, parts = (steps + per - 1) / per;
+    const int64_t cost = (n_tok * parts + warps - 1) / warps * (per + 3);
+    if (cost < best) {
+      best = cost;
+      a.chunk = per;
+      a.chunks = parts;
+    }
+    if (n_tok >= 16 * warps) break;  // whole tokens
+  }
   const int64_t want = (n_tok * a.chunks + kWarps - 1) / kWarps;
-  const int grid = static_cast<int>(want < 4L * sms ? want : 4L * sms);
+  const int64_t cap = static_cast<int64_t>(sms) * kCtasPerSm;
+  const int grid = static_cast<int>(want < cap ? want : cap);
   cudaStream_t st = as_stream(stream);
   if (d == 64)
     launch<64>(a, interleaved, int8, grid, st);
