@@ -55,6 +55,11 @@ constexpr int kSplitPerSm = 4;     // pieces that write partials, per SM
 constexpr uint32_t kSCol = 256;    // tensor memory: O in [0, D), S/P buffers from here
 constexpr int kMaxSmem = 227 * 1024;
 
+// Warp 0 copies, warp 1 issues products, warps 2 and 3 read int8 scales, two
+// groups of four warps take the softmax of the two halves of a tile's keys,
+// and for int8 rows four warps widen them.
+template <bool INT8>
+constexpr int kThreads = INT8 ? 512 : 384;
 struct Piece {
   int tok0, rows;     // first token, valid rows of the whole tile (tokens * G)
   int pos0;           // position of the first token
@@ -73,6 +78,7 @@ struct PagedArgs {
   const __half *k_scale, *v_scale;
   int64_t n_blocks;
   int page, rb;               // rows per TMA box
+  uint32_t page_mul, page_shift;  // t / page = (umulhi(page_mul, t) + t) >> page_shift for t < 2^31
   const int32_t* block_table;
   int64_t n_pages;
   const int32_t *q_start, *lengths;
@@ -95,10 +101,16 @@ struct alignas(16) Aux {
   // Two barriers where a waiter may skip tiles: when S(t + 1) is there, O of
   // t - 1 is done and of t may not be, and one parity could not tell them apart.
   uint64_t s_full[2], p_full[2], pv_done[2], q_full, o_free, mma_idle;
+  uint64_t x_full[2][4];  // per 32 rows: both softmax warps' values are in `x`
   uint64_t pc_full[kPieces], pc_empty[kPieces];
   Piece pc[kPieces];
   uint32_t tile_bad[kTileInfo];  // bit i: rows [8 i, 8 i + 8) of the tile have no page
-  int cand_p[kCand], cand_s[kCand];
+  union {
+    struct {
+      int cand_p[kCand], cand_s[kCand];  // while planning
+    };
+    float x[2][2][kRows];  // [exchange parity][group][row]: maxima of a tile, at a piece's end sums
+  };
   int nmax, units, split_c, split_items;
   uint32_t tmem_base;
   int dirty;  // a value that only some queries of a tile see was not finite
@@ -111,7 +123,7 @@ struct alignas(16) Aux8 {  // int8 rows only
   alignas(16) float ks[kScaleRing][kRows], vs[kScaleRing][kRows];
 };
 
-static_assert(sizeof(Aux) <= 2048, "the bf16 pair kernel's shared memory is full");
+static_assert(sizeof(Aux) <= 3072, "what the bf16 pair kernel's query tile and five stages leave");
 
 // ---- work list -------------------------------------------------------------------
 
@@ -171,6 +183,11 @@ __device__ __forceinline__ int pieces_of(int ntmax, int c) { return c > 0 && ntm
 
 // ---- helpers ---------------------------------------------------------------------
 
+// Page of key t < 2^31; a general division would cost the copying warp as much as the copy's issue.
+__device__ __forceinline__ int page_of(const PagedArgs& a, int t) {
+  return static_cast<int>((__umulhi(a.page_mul, static_cast<uint32_t>(t)) + static_cast<uint32_t>(t)) >> a.page_shift);
+}
+
 template <int CTAS>
 __device__ __forceinline__ uint32_t leader_addr(uint64_t* bar) {
   const uint32_t l = tc::smem_addr(bar);
@@ -180,13 +197,42 @@ __device__ __forceinline__ uint32_t leader_addr(uint64_t* bar) {
   return r;
 }
 
-// Arrive on the leader CTA's barrier.
+// Bounded wait of one thread for the phase of the given parity: gives up after
+// about two seconds, or when *abort is set; sets *abort and returns false.
+// The bound counts clock cycles: reading the global timer takes longer than
+// most of these waits.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (tc::bar_test(bar, parity, false)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; it++) {
+    if (tc::bar_test(bar, parity, false)) return true;
+    if ((it & 15) == 0) {
+      if (*abort) return false;
+      if (clock64() - t0 > 4000000000ll) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// A whole warp waits (one lane asks); false in every lane if it gave up.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = wait(bar, parity, abort);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// Arrive on the leader CTA's barrier.  Default (CTA) scope: what the leader's
+// products read of this CTA is its own tensor and shared memory, ordered by
+// the tcgen05 and proxy fences before the arrival; a release at cluster scope
+// would wait here for every earlier access of the thread, each tile.
 template <int CTAS>
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   if (CTAS == 1)
     tc::bar_arrive(bar);
   else
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr<CTAS>(bar))
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr<CTAS>(bar))
                  : "memory");
 }
 
@@ -197,6 +243,13 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
       "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
       "l"(map), "r"(0), "r"(0), "r"(sub), "r"(rg), "r"(h), "r"(tc::smem_addr(bar))
       : "memory");
+}
+
+// Shared-memory matrix descriptor (128-byte swizzle, as tc::sw128_desc) from
+// its low word, which holds the address, and its constant high word.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t sbo) {
+  return (static_cast<uint64_t>((sbo >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
 }
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int b_mn) {
@@ -243,6 +296,50 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+
+
+// Two fp32 values in one 64-bit register.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2_out(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Two int8 codes (bytes 0 and 1, or 2 and 3, of x) -> two bf16, exact: a
 // byte's low 7 bits under the exponent of 128 give 128 + low7, its sign bit
 // there gives 128 or 256, and their difference is the code.
@@ -270,19 +367,48 @@ struct Ring {  // a stage index and the parity of its current use
   }
 };
 
+// Values that are not finite were zeroed in the tiles that only some queries
+// of the query tile see; this adds up those in columns [c0, c0 + 32) that a
+// query at position p sees.
+template <int D, int KT>
+__device__ __noinline__ void add_nonfinite(const PagedArgs& a, const Piece& pc, int p, int p_last, int c0,
+                                           float (&sum)[32]) {
+  for (int j = 0; j < pc.n; j++) {
+    const int tl = pc.j0 + j < pc.nsink ? pc.j0 + j : pc.lo + pc.j0 + j - pc.nsink;
+    const int t0 = tl * KT;
+    bool masked = t0 + KT - 1 > pc.pos0 || (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S);
+    for (int x = 0; x < KT && !masked; x += 8) {  // or a row without a page
+      const int pg = page_of(a, t0 + x);
+      const int blk = pg < a.n_pages ? a.block_table[pc.b * a.n_pages + pg] : -1;
+      masked = blk < 0 || blk >= a.n_blocks;
+    }
+    if (!masked) continue;  // every query sees the whole tile: its values went through the products as they are
+    for (int x = 0; x < KT; x++) {
+      const int key = t0 + x;
+      if (key > p || !(a.W == 0 || key > p - a.W || key < a.S)) continue;
+      const int pg = page_of(a, key);
+      const int blk = pg < a.n_pages ? a.block_table[pc.b * a.n_pages + pg] : -1;
+      if (blk < 0 || blk >= a.n_blocks) continue;
+      const uint16_t* v = a.v_pool + ((static_cast<int64_t>(blk) * a.page + (key - pg * a.page)) * a.Hkv + pc.h) * D + c0;
+      for (int i = 0; i < 32; i++)
+        if ((v[i] & 0x7f80u) == 0x7f80u)
+          sum[i] += bf16_bits_to_f32(v[i]);
+    }
+  }
+}
+
 template <int D, int CTAS, bool INT8>
-__global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
+__global__ void __launch_bounds__(kThreads<INT8>, 1)
     paged_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                  const PagedArgs a) {
   constexpr int KT = 64 * CTAS;          // keys per tile
   constexpr int NSUB = D / 64;           // 64-column blocks of a row
   constexpr int VSUB = NSUB / CTAS;      // those of this CTA's part of V
   constexpr int STAGE = 64 * D * 2;      // bytes of a K or V stage (either part)
-  constexpr int THREADS = INT8 ? 384 : 256;
+  constexpr int THREADS = kThreads<INT8>;
   constexpr uint32_t SBO_K = NSUB * 1024, SBO_V = VSUB * 1024;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
-  unsigned char* sQ = sm;
+  unsigned char* sQ = smem_raw;  // 1024-byte aligned, as the swizzled tiles need (checked below)
   unsigned char* sKV = sQ + a.q_bytes;
   unsigned char* sI8 = sKV + a.stages * STAGE;
   Aux* ax = reinterpret_cast<Aux*>(sI8 + (INT8 ? a.staging * (STAGE / 2) : 0));
@@ -301,15 +427,19 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
     }
     for (int s = 0; s < 2; s++) {
       tc::bar_init(&ax->s_full[s], 1);
-      tc::bar_init(&ax->p_full[s], 4 * CTAS);
+      tc::bar_init(&ax->p_full[s], 8 * CTAS);
       tc::bar_init(&ax->pv_done[s], 1);
     }
-    tc::bar_init(&ax->q_full, 4 * CTAS);
-    tc::bar_init(&ax->o_free, 4 * CTAS);
+    for (int s = 0; s < 4; s++) {
+      tc::bar_init(&ax->x_full[0][s], 2);
+      tc::bar_init(&ax->x_full[1][s], 2);
+    }
+    tc::bar_init(&ax->q_full, 8 * CTAS);
+    tc::bar_init(&ax->o_free, 8 * CTAS);
     tc::bar_init(&ax->mma_idle, 1);
     for (int s = 0; s < kPieces; s++) {
       tc::bar_init(&ax->pc_full[s], 1);
-      tc::bar_init(&ax->pc_empty[s], INT8 ? 11 : 5);  // MMA thread, softmax warps, (scale and widening warps)
+      tc::bar_init(&ax->pc_empty[s], INT8 ? 15 : 9);  // MMA thread, softmax warps, (scale and widening warps)
     }
     if (INT8) {
       for (int s = 0; s < kMaxStaging; s++) {
@@ -318,10 +448,10 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
       }
       for (int s = 0; s < kScaleRing; s++) {
         tc::bar_init(&a8->sc_full[s], 1);
-        tc::bar_init(&a8->sc_empty[s], 4);
+        tc::bar_init(&a8->sc_empty[s], 8);
       }
     }
-    ax->abort = 0;
+    ax->abort = (tc::smem_addr(smem_raw) & 1023u) != 0;  // every wait would give up at once
     ax->dirty = 0;
     ax->nmax = 0;
     ax->units = 0;
@@ -448,7 +578,7 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
     scan();
     const uint32_t full = 0xffffffffu;
     const int boxes = KT / a.rb;                 // per tile; this CTA copies boxes_k of them for K, all for V
-    const int boxes_k = 64 / a.rb;
+    const int boxes_k = 64 / a.rb, rb_log = 31 - __clz(a.rb);
     const uint32_t box_k = static_cast<uint32_t>(a.rb) * D * (INT8 ? 1 : 2), box_v = box_k / CTAS;
     Ring st;  // K/V stage (bf16) or staging slot (int8)
     const int depth = INT8 ? a.staging : a.stages;
@@ -508,11 +638,7 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
         pc.slot = -1;
       }
       const int slot = k % kPieces;
-      if (k >= kPieces) ok = tc::bar_wait(&ax->pc_empty[slot], ((k / kPieces) - 1) & 1, abort);
-      if (!__all_sync(full, ok)) {
-        ok = false;
-        break;
-      }
+      if (k >= kPieces && !(ok = wait_all(&ax->pc_empty[slot], ((k / kPieces) - 1) & 1, abort))) break;
       if (lane == 0) {
         ax->pc[slot] = pc;
         tc::bar_arrive(&ax->pc_full[slot]);
@@ -521,31 +647,47 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
       // Copies, in the order the products take them.  Lane i holds the block of
       // rows [i rb, i rb + rb) of a tile; ids are read one tile ahead.
       auto tile_of = [&](int j) { return j < pc.nsink ? j : pc.lo + j - pc.nsink; };
-      auto block_of = [&](int j) -> int {
+      auto block_of = [&](int j, int& row) -> int {  // and this lane's row within the block
+        row = 0;
         if (j >= pc.n || lane >= boxes) return -1;
-        const int64_t t = static_cast<int64_t>(tile_of(pc.j0 + j)) * KT + lane * a.rb;
-        const int64_t pg = t / a.page;
+        const int t = tile_of(pc.j0 + j) * KT + lane * a.rb, pg = page_of(a, t);
+        row = t - pg * a.page;
         return pg < a.n_pages ? a.block_table[pc.b * a.n_pages + pg] : -1;
       };
-      const int64_t p_hi = pc.pos0 + pc.rows / a.G - 1;  // keys past it are not copied
-      int cur = block_of(0), prev = -1;
+      const int p_hi = pc.pos0 + pc.rows / a.G - 1;  // keys past it are not copied
+      int blk[4], row[4];  // of tiles j - 1 .. j + 2, at index tile & 3
+      blk[0] = block_of(0, row[0]);
+      blk[1] = block_of(1, row[1]);
       for (int j = 0; ok && j <= pc.n; j++) {
-        const int nxt = block_of(j + 1);
+        // ids are read two tiles ahead
+        int b2, r2;
+        b2 = block_of(j + 2, r2);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (((j + 2) & 3) == i) {
+            blk[i] = b2;
+            row[i] = r2;
+          }
         for (int v = 0; v < 2; v++) {  // K(j), then V(j - 1)
           const int jj = v ? j - 1 : j;
           if (jj < 0 || jj >= pc.n) continue;
-          const int blk = v ? prev : cur;
-          const int64_t t0 = static_cast<int64_t>(tile_of(pc.j0 + jj)) * KT;
-          const int64_t t = t0 + lane * a.rb;
+          int bk = 0, rw = 0;
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if ((jj & 3) == i) {
+              bk = blk[i];
+              rw = row[i];
+            }
+          const int t = tile_of(pc.j0 + jj) * KT + lane * a.rb;
           // some row of the box is visible to some query of the tile
           const bool want = lane < boxes && t <= p_hi && (a.W == 0 || t + a.rb - 1 > pc.pos0 - a.W || t < a.S);
-          const bool good = want && blk >= 0 && blk < a.n_blocks;
+          const bool good = want && bk >= 0 && bk < a.n_blocks;
           if (!v) {  // which 8-row groups have no page (the table's end counts; rows past p_hi are masked anyway)
             if (__any_sync(full, want && !good)) {
               if (lane == 0 && rank == 0) set_status(a.status, SKV_DEV_RANGE);
               uint32_t m = 0;
               const uint32_t bad = __ballot_sync(full, want && !good);
-              for (int g = 0; g < KT / 8; g++) m |= ((bad >> (8 * g / a.rb)) & 1u) << g;
+              for (int g = 0; g < KT / 8; g++) m |= ((bad >> ((8 * g) >> rb_log)) & 1u) << g;
               if (lane == 0) ax->tile_bad[tile_no % kTileInfo] = m;
             } else if (lane == 0) {
               ax->tile_bad[tile_no % kTileInfo] = 0;
@@ -554,28 +696,22 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
           }
           const int kfirst = static_cast<int>(rank) * boxes_k;
           const bool mine = good && (v || (lane >= kfirst && lane < kfirst + boxes_k));
-          if (uses >= static_cast<uint32_t>(depth)) ok = tc::bar_wait(&empties[st.s], st.ph ^ 1, abort);
-          if (!__all_sync(full, ok)) {
-            ok = false;
-            break;
-          }
+          if (uses >= static_cast<uint32_t>(depth) && !(ok = wait_all(&empties[st.s], st.ph ^ 1, abort))) break;
           const uint32_t cnt = __popc(__ballot_sync(full, mine));
           const uint32_t bytes = v ? box_v : box_k;
           if (lane == 0) tc::bar_arrive_expect_tx(&fulls[st.s], cnt * bytes);
           __syncwarp();
           if (mine) {
             const int at = v ? lane : lane - kfirst;
-            const int64_t row = static_cast<int64_t>(blk) * a.page + t % a.page;
+            const int64_t first = static_cast<int64_t>(bk) * a.page + rw;
             constexpr int kSubV = INT8 ? (D / CTAS >= 128 ? D / CTAS / 128 : 1) : VSUB;  // column blocks of the V box
             tma_rows(tc::smem_addr(ring + st.s * SLOT) + at * bytes, v ? &v_map : &k_map,
-                     v ? static_cast<int>(rank) * kSubV : 0, static_cast<int>(row / 8), pc.h, &fulls[st.s]);
+                     v ? static_cast<int>(rank) * kSubV : 0, static_cast<int>(first >> 3), pc.h, &fulls[st.s]);
           }
           __syncwarp();
           uses++;
           st.next(depth);
         }
-        prev = cur;
-        cur = nxt;
       }
     }
     if (!ok) {  // gave up: let the copies in flight land before the CTA leaves
@@ -597,38 +733,39 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
     // ---------------- products (one thread of the leader) ----------------
     if (lane == 0) {
       constexpr uint32_t id_qk = idesc_bf16(kRows * CTAS, KT, 0), id_pv = idesc_bf16(kRows * CTAS, D, 1);
-      const uint32_t aQ = tc::smem_addr(sQ), aKV = tc::smem_addr(sKV);
+      const uint32_t dQ = desc_lo(tc::smem_addr(sQ), 16), dK = desc_lo(tc::smem_addr(sKV), 16),
+                     dV = desc_lo(tc::smem_addr(sKV), 1024);
       Ring st;
       uint32_t g = 0, np = 0;  // tiles, pieces with work so far
       bool ok = true;
       for (int k = 0; ok; k++) {
         const int slot = k % kPieces;
-        ok = tc::bar_wait(&ax->pc_full[slot], (k / kPieces) & 1, abort);
+        ok = wait(&ax->pc_full[slot], (k / kPieces) & 1, abort);
         if (!ok) break;
         const int n = ax->pc[slot].n, last = ax->pc[slot].last;
         tc::bar_arrive(&ax->pc_empty[slot]);
         if (last) break;
         if (rank != 0) {  // the peer passes on to the leader that its stages are full
           for (int f = 0; !INT8 && ok && f < 2 * n; f++) {
-            ok = tc::bar_wait(&ax->kv_full[st.s], st.ph, abort);
+            ok = wait(&ax->kv_full[st.s], st.ph, abort);
             if (ok) arrive_leader<CTAS>(&ax->kv_full[st.s]);
             st.next(a.stages);
           }
           continue;
         }
         if (n == 0) continue;
-        ok = tc::bar_wait(&ax->q_full, np & 1, abort, CTAS == 2);
+        ok = wait(&ax->q_full, np & 1, abort);
         for (int j = 0; ok && j <= n; j++) {
           if (j < n) {
-            ok = tc::bar_wait(&ax->kv_full[st.s], st.ph, abort, CTAS == 2);
+            ok = wait(&ax->kv_full[st.s], st.ph, abort);
             if (!ok) break;
             tc::tc_fence_after();
-            const uint32_t kv = aKV + st.s * STAGE;
+            const uint32_t kv = dK + st.s * (STAGE >> 4);
             const uint32_t d = tm + kSCol + ((g + j) & 1) * 128;
 #pragma unroll
             for (int x = 0; x < D / 16; x++) {
-              const uint32_t off = (x >> 2) * 1024 + (x & 3) * 32;
-              mma_ss<CTAS>(d, tc::sw128_desc(aQ + off, 16, SBO_K), tc::sw128_desc(kv + off, 16, SBO_K), id_qk, x > 0);
+              const uint32_t off = ((x >> 2) * 1024 + (x & 3) * 32) >> 4;
+              mma_ss<CTAS>(d, desc(dQ + off, SBO_K), desc(kv + off, SBO_K), id_qk, x > 0);
             }
             commit<CTAS>(&ax->kv_empty[st.s]);
             commit<CTAS>(&ax->s_full[(g + j) & 1]);
@@ -636,16 +773,16 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
           }
           if (j >= 1) {
             const uint32_t t = g + j - 1;
-            if (j == 1 && np > 0) ok = tc::bar_wait(&ax->o_free, (np - 1) & 1, abort, CTAS == 2);
-            ok = ok && tc::bar_wait(&ax->p_full[t & 1], (t >> 1) & 1, abort, CTAS == 2);
-            ok = ok && tc::bar_wait(&ax->kv_full[st.s], st.ph, abort, CTAS == 2);
+            if (j == 1 && np > 0) ok = wait(&ax->o_free, (np - 1) & 1, abort);
+            ok = ok && wait(&ax->p_full[t & 1], (t >> 1) & 1, abort);
+            ok = ok && wait(&ax->kv_full[st.s], st.ph, abort);
             if (!ok) break;
             tc::tc_fence_after();
-            const uint32_t kv = aKV + st.s * STAGE;
-            const uint32_t p = tm + kSCol + (t & 1) * 128;
+            const uint32_t kv = dV + st.s * (STAGE >> 4);
+            const uint32_t p = tm + kSCol + (t & 1) * 128;  // each half's weights start where its logits did
 #pragma unroll
             for (int x = 0; x < KT / 16; x++)
-              mma_ts<CTAS>(tm, p + 8 * x, tc::sw128_desc(kv + x * 2 * SBO_V, 1024, SBO_V), id_pv, j > 1 || x > 0);
+              mma_ts<CTAS>(tm, p + 8 * x + (x >= KT / 32 ? KT / 4 : 0), desc(kv + x * (2 * SBO_V >> 4), SBO_V), id_pv, j > 1 || x > 0);
             commit<CTAS>(&ax->kv_empty[st.s]);
             commit<CTAS>(&ax->pv_done[t & 1]);
             st.next(a.stages);
@@ -666,20 +803,20 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
       bool ok = true;
       for (int k = 0; ok; k++) {
         const int slot = k % kPieces;
-        ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->pc_full[slot], (k / kPieces) & 1, abort));
+        ok = wait_all(&ax->pc_full[slot], (k / kPieces) & 1, abort);
         if (!ok) break;
         const Piece pc = ax->pc[slot];
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&ax->pc_empty[slot]);
         if (pc.last) break;
-        const int64_t p_hi = pc.pos0 + pc.rows / a.G - 1;
+        const int p_hi = pc.pos0 + pc.rows / a.G - 1;
         auto row_of = [&](int j, int e) -> int64_t {  // pool row of key lane + 32 e of tile j, -1: none
           if (j >= pc.n) return -1;
           const int tl = pc.j0 + j < pc.nsink ? pc.j0 + j : pc.lo + pc.j0 + j - pc.nsink;
-          const int64_t t = static_cast<int64_t>(tl) * KT + lane + 32 * e, pg = t / a.page;
+          const int t = tl * KT + lane + 32 * e, pg = page_of(a, t);
           if (t > p_hi || pg >= a.n_pages) return -1;
           const int blk = a.block_table[pc.b * a.n_pages + pg];
-          return blk >= 0 && blk < a.n_blocks ? static_cast<int64_t>(blk) * a.page + t % a.page : -1;
+          return blk >= 0 && blk < a.n_blocks ? static_cast<int64_t>(blk) * a.page + (t - pg * a.page) : -1;
         };
         int j = static_cast<int>((g ^ (warp & 1)) & 1);  // first tile of this warp's parity
         int64_t row[KT / 32];
@@ -695,7 +832,7 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
             row[e] = row_of(j + 2, e);
           }
           const uint32_t t = g + j, s = t % kScaleRing;
-          if (t >= kScaleRing) ok = __all_sync(0xffffffffu, tc::bar_wait(&a8->sc_empty[s], (t / kScaleRing - 1) & 1, abort));
+          if (t >= kScaleRing) ok = wait_all(&a8->sc_empty[s], (t / kScaleRing - 1) & 1, abort);
           if (!ok) break;
 #pragma unroll
           for (int e = 0; e < KT / 32; e++) {
@@ -708,20 +845,38 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
         g += pc.n;
       }
     }
-  } else if (warp < 8) {
-    // ---------------- softmax and output: thread = row ----------------
-    const int r = tid - 128;                        // row within this CTA
+  } else if (warp < 12) {
+    // ---------------- softmax and output: thread = row, two groups ----------------
+    // Group `wg` takes half of every tile's keys and half of the output's
+    // columns: the logits-to-weights time stands between two products of the
+    // same tile, so it is halved by two warps per 32 rows rather than spread
+    // over two tiles (3.4K against 2.5K clocks a tile).  The two agree on the
+    // tile's maximum through shared memory, so both hold the same running
+    // maximum, and add up their sums at a piece's end.
+    const int wg = (warp - 4) >> 2, quad = warp & 3;
+    const int r = 32 * quad + lane;                     // row within this CTA
     const int rt = static_cast<int>(rank) * kRows + r;  // row within the tile
-    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const int warp_row = static_cast<int>(rank) * kRows + 32 * (warp & 3);
-    uint32_t g = 0, fills = 0;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
+    const int warp_row = static_cast<int>(rank) * kRows + 32 * quad;
+    uint32_t g = 0, fills = 0, xc = 0;  // tiles, ring fills, exchanges so far
     bool ok = true;
+
+    // This thread's value and its partner's (the other group's, same row).
+    auto exchange = [&](float v, float& other) -> bool {
+      ax->x[xc & 1][wg][r] = v;
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&ax->x_full[xc & 1][quad]);
+      if (!wait_all(&ax->x_full[xc & 1][quad], (xc >> 1) & 1, abort)) return false;
+      other = ax->x[xc & 1][wg ^ 1][r];
+      xc++;
+      return true;
+    };
 
     // Query rows of a piece: 16-byte copies into the swizzled tile.
     auto load_q = [&](const Piece& pc) {
       constexpr int CH = D / 8;
       const int rows = min(kRows, pc.rows - static_cast<int>(rank) * kRows);
-      for (int i = r; i < rows * CH; i += 128) {
+      for (int i = tid - 128; i < rows * CH; i += 256) {
         const int row = i / CH, ch = i % CH, rr = static_cast<int>(rank) * kRows + row;
         const int tok = pc.tok0 + rr / a.G;
         const uint16_t* src = a.q + tok * a.q_stride + static_cast<int64_t>(pc.h * a.G + rr % a.G) * D + ch * 8;
@@ -737,9 +892,9 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
       __syncwarp();
       if (lane == 0) arrive_leader<CTAS>(&ax->q_full);
     };
-    auto get = [&](int k, Piece& pc) -> bool {  // descriptor k; empty ones are handed on after use
+    auto get = [&](int k, Piece& pc) -> bool {  // descriptor k
       const int slot = k % kPieces;
-      if (!__all_sync(0xffffffffu, tc::bar_wait(&ax->pc_full[slot], (k / kPieces) & 1, abort))) return false;
+      if (!wait_all(&ax->pc_full[slot], (k / kPieces) & 1, abort)) return false;
       pc = ax->pc[slot];
       __syncwarp();
       if (lane == 0) tc::bar_arrive(&ax->pc_empty[slot]);
@@ -754,119 +909,140 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
       next.last = 1;
       const int tok_i = rt / a.G;
       const bool live = rt < pc.rows;
-      const int p = live ? pc.pos0 + tok_i : -1;   // this row's position: keys 0 .. p
+      const int p = live ? pc.pos0 + tok_i : -1;  // this row's position: keys 0 .. p
       const bool warp_live = warp_row < pc.rows;
-      float m_ref = -INFINITY, l = 0.f;
-      bool have_next = false;
+      float m_ref = -INFINITY, l = 0.f;           // the maximum that l is relative to
       if (pc.n > 0 && !q_loaded) {
         load_q(pc);
         q_ready();
       }
       q_loaded = false;
       const int p_last = pc.pos0 + pc.rows / a.G - 1;
-      for (int j = 0; ok && j < pc.n; j++) {
+      for (int j = 0; j < pc.n; j++) {
         const uint32_t t = g + j;
         const int tl = pc.j0 + j < pc.nsink ? pc.j0 + j : pc.lo + pc.j0 + j - pc.nsink;
         const int t0 = tl * KT;
-        ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->s_full[t & 1], (t >> 1) & 1, abort));
-        if (!ok) break;
+        if (!(ok = wait_all(&ax->s_full[t & 1], (t >> 1) & 1, abort))) break;
         tc::tc_fence_after();
         const uint32_t bad = ax->tile_bad[t % kTileInfo];
         // every row of the tile sees every key unless one of these holds
         const bool masked = t0 + KT - 1 > pc.pos0 || bad != 0 ||
                             (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S);
-        const uint32_t scol = tm + lane_base + kSCol + (t & 1) * 128;
+        constexpr int HC = KT / 2;  // this group's keys of the tile
+        const uint32_t scol = tm + lane_base + kSCol + (t & 1) * 128 + wg * HC;
         const uint32_t sc = t % kScaleRing;
-        if (INT8) {
-          ok = __all_sync(0xffffffffu, tc::bar_wait(&a8->sc_full[sc], (t / kScaleRing) & 1, abort));
-          if (!ok) break;
-        }
+        if (INT8 && !(ok = wait_all(&a8->sc_full[sc], (t / kScaleRing) & 1, abort))) break;
         if (warp_live) {
-          float x[KT];
+          uint32_t s[HC / 32][32];
 #pragma unroll
-          for (int c0 = 0; c0 < KT; c0 += 32) tc::tmem_ld32(scol + c0, reinterpret_cast<uint32_t(&)[32]>(x[c0]));
+          for (int c = 0; c < HC / 32; c++) tc::tmem_ld32(scol + 32 * c, s[c]);
           tc::tmem_wait_ld();
+          F2 x[HC / 2];
+#pragma unroll
+          for (int i = 0; i < HC / 2; i++)
+            x[i] = f2(__uint_as_float(s[i / 16][2 * i % 32]), __uint_as_float(s[i / 16][2 * i % 32 + 1]));
           if (INT8) {
 #pragma unroll
-            for (int i = 0; i < KT; i += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&a8->ks[sc][i]);
-              x[i] *= f.x;
-              x[i + 1] *= f.y;
-              x[i + 2] *= f.z;
-              x[i + 3] *= f.w;
+            for (int i = 0; i < HC / 2; i += 2) {
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&a8->ks[sc][wg * HC + 2 * i]);
+              x[i] = f2_mul(x[i], F2{f.x});
+              x[i + 1] = f2_mul(x[i + 1], F2{f.y});
             }
           }
           if (masked) {
-            const int hi = p - t0, lo = a.W > 0 ? p - a.W - t0 : -1, sk = a.W > 0 ? a.S - t0 : 0;
+            const int f0 = t0 + wg * HC;  // first key of this group
+            const int hi = p - f0, lo = a.W > 0 ? p - a.W - f0 : -1, sk = a.W > 0 ? a.S - f0 : 0;
+            const uint32_t bd = bad >> (wg * HC / 8);
+            auto see = [&](int i) { return i <= hi && (i > lo || i < sk) && !((bd >> (i >> 3)) & 1u); };
 #pragma unroll
-            for (int i = 0; i < KT; i++) {
-              const bool see = i <= hi && (i > lo || i < sk) && !((bad >> (i >> 3)) & 1u);
-              x[i] = see ? x[i] : -INFINITY;
+            for (int i = 0; i < HC / 2; i++) {
+              const float2 v = f2_out(x[i]);
+              x[i] = f2(see(2 * i) ? v.x : -INFINITY, see(2 * i + 1) ? v.y : -INFINITY);
             }
           }
-          float mp[4] = {x[0], x[1], x[2], x[3]};
+          float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 4; i < KT; i++) mp[i & 3] = fmaxf(mp[i & 3], x[i]);
+          for (int i = 0; i < HC / 2; i++) {
+            const float2 v = f2_out(x[i]);
+            mp[i & 3] = max3(mp[i & 3], v.x, v.y);
+          }
           const float f = INT8 ? 1.f : a.scale_log2;
-          const float mc = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * f;
-          bool rescale = false;
-          float alpha = 1.f;
-          if (mc > m_ref + kLazy || (m_ref == -INFINITY && mc > m_ref)) {
-            alpha = tc::ex2_approx(m_ref - mc);
-            rescale = j > 0;
-            m_ref = mc;
-          }
-          if (__any_sync(0xffffffffu, rescale)) {
-            ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort));
-            if (!ok) break;
-            tc::tc_fence_after();
+          float mc = fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]) * f, mo;
+          if (!(ok = exchange(mc, mo))) break;
+          mc = fmaxf(mc, mo);
+          const float m_new = mc > m_ref + kLazy || m_ref == -INFINITY ? fmaxf(mc, m_ref) : m_ref;
+          if (__any_sync(0xffffffffu, m_new != m_ref)) {
+            const float alpha = m_new == m_ref ? 1.f : tc::ex2_approx(m_ref - m_new);
+            if (j > 0) {
+              if (!(ok = wait_all(&ax->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort))) break;
+              tc::tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t o[32];
-              tc::tmem_ld32(tm + lane_base + c0, o);
-              tc::tmem_wait_ld();
+              for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
+                uint32_t o[32];
+                tc::tmem_ld32(tm + lane_base + c0, o);
+                tc::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tc::tmem_st32(tm + lane_base + c0, o);
+                for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tc::tmem_st32(tm + lane_base + c0, o);
+              }
             }
-            l *= alpha;
+            l = m_ref == -INFINITY ? 0.f : l * alpha;
+            m_ref = m_new;
           }
           const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t pk[KT / 2];
+          const F2 ff = f2(f, f), mm = f2(-m_use, -m_use);
+          F2 ls[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < KT; i += 2) {
-            float p0 = tc::ex2_approx(fmaf(x[i], f, -m_use)), p1 = tc::ex2_approx(fmaf(x[i + 1], f, -m_use));
-            if (INT8) {
-              ls[(i >> 1) & 3] += p0 + p1;
-              float v0 = p0 * a8->vs[sc][i], v1 = p1 * a8->vs[sc][i + 1];
-              if (masked) {  // a scale that this row does not see may be anything
-                v0 = x[i] == -INFINITY ? 0.f : v0;
-                v1 = x[i + 1] == -INFINITY ? 0.f : v1;
+          for (int c = 0; c < HC / 32; c++) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int y = 0; y < 16; y += 2) {
+              const int i = 16 * c + y;
+              float2 e[2];
+#pragma unroll
+              for (int z = 0; z < 2; z++) {
+                e[z] = f2_out(INT8 ? f2_add(x[i + z], mm) : f2_fma(x[i + z], ff, mm));
+                e[z].x = tc::ex2_approx(e[z].x);
+                e[z].y = tc::ex2_approx(e[z].y);
               }
-              pk[i >> 1] = pack_bf16(v0, v1);
-            } else {
-              const uint32_t w = pack_bf16(p0, p1);
-              pk[i >> 1] = w;
-              ls[(i >> 1) & 3] += __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
-            }
-          }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+              if (INT8) {
+                ls[0] = f2_add(ls[0], f2(e[0].x, e[0].y));
+                ls[1] = f2_add(ls[1], f2(e[1].x, e[1].y));
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&a8->vs[sc][wg * HC + 2 * i]);
+                float2 w0 = f2_out(f2_mul(f2(e[0].x, e[0].y), F2{v.x}));
+                float2 w1 = f2_out(f2_mul(f2(e[1].x, e[1].y), F2{v.y}));
+                if (masked) {  // a scale that this row does not see may be anything
+                  const float2 x0 = f2_out(x[i]), x1 = f2_out(x[i + 1]);
+                  w0 = make_float2(x0.x == -INFINITY ? 0.f : w0.x, x0.y == -INFINITY ? 0.f : w0.y);
+                  w1 = make_float2(x1.x == -INFINITY ? 0.f : w1.x, x1.y == -INFINITY ? 0.f : w1.y);
+                }
+                pk[y] = pack_bf16(w0.x, w0.y);
+                pk[y + 1] = pack_bf16(w1.x, w1.y);
+              } else {  // the sum takes the weights as they are rounded
 #pragma unroll
-          for (int c0 = 0; c0 < KT / 2; c0 += 32) tc::tmem_st32(scol + c0, reinterpret_cast<uint32_t(&)[32]>(pk[c0]));
+                for (int z = 0; z < 2; z++) {
+                  const uint32_t w = pack_bf16(e[z].x, e[z].y);
+                  pk[y + z] = w;
+                  ls[z] = f2_add(ls[z], f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
+                }
+              }
+            }
+            tmem_st16(scol + 16 * c, pk);
+          }
+          const float2 l0 = f2_out(f2_add(ls[0], ls[1]));
+          l += l0.x + l0.y;
           tc::tmem_wait_st();
         }  // a warp without rows leaves S as its weights: rows are independent, and its are not used
         if (!INT8 && masked) {
-          // Zero weights do not stop a NaN: rows of V without a token become
-          // zero, and so does every value that is not finite (put back for
-          // the queries that see it by the non-finite pass below).
+          // Zero weights do not stop a NaN: rows of V that no query of the tile
+          // sees become zero, and so does every value that is not finite (put
+          // back for the queries that see it when the output is written).
           const uint32_t fv = fills + fill_v(j, pc.n);
           const uint32_t vs = fv % a.stages;
-          ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->kv_full[vs], (fv / a.stages) & 1, abort, CTAS == 2));
-          if (!ok) break;
+          if (!(ok = wait_all(&ax->kv_full[vs], (fv / a.stages) & 1, abort))) break;
           unsigned char* V = sKV + vs * STAGE;
           bool found = false;
-          for (int i = r; i < STAGE / 16; i += 128) {
+          for (int i = tid - 128; i < STAGE / 16; i += 256) {
             const int grp = i / (VSUB * 64), row = grp * 8 + ((i >> 3) & 7);  // 64 16-byte pieces per 1024 B block
             uint4* at = reinterpret_cast<uint4*>(V + i * 16);
             const int key = t0 + row;  // seen by no query of the tile: its page may not have been read
@@ -895,34 +1071,37 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
                       tc::smem_addr(&ax->dirty)),
                   "r"(rank ^ 1u), "r"(1)
                   : "memory");
+            __threadfence();  // the peer reads it after this tile's products
           }
           tc::fence_async_smem();
         }
-        if (INT8) {
-          __syncwarp();
-          if (lane == 0) tc::bar_arrive(&a8->sc_empty[sc]);
-        }
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader<CTAS>(&ax->p_full[t & 1]);
+        if (lane == 0) {
+          if (INT8) tc::bar_arrive(&a8->sc_empty[sc]);
+          arrive_leader<CTAS>(&ax->p_full[t & 1]);
+        }
       }
       if (!ok) break;
-      // The last logits have been read, so the query tile is free: fetch the next one under the last product.
-      ok = get(k + 1, next);
-      if (!ok) break;
-      have_next = !next.last && next.n > 0 && pc.n > 0;
-      if (have_next) load_q(next);
+      // Once the last logits are there the query tile is free: fetch the next one under the last product.
+      const uint32_t t_last = g + pc.n - 1;
+      if (!(ok = get(k + 1, next))) break;
+      const bool have_next = !next.last && next.n > 0 && pc.n > 0;
       if (pc.n > 0) {
-        const uint32_t t = g + pc.n - 1;
-        ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->pv_done[t & 1], (t >> 1) & 1, abort));
-        if (!ok) break;
+        if (have_next) load_q(next);
+        if (warp_live) {
+          float lo;
+          if (!(ok = exchange(l, lo))) break;
+          l += lo;  // a sum of two: the same in both
+        }
+        if (!(ok = wait_all(&ax->pv_done[t_last & 1], (t_last >> 1) & 1, abort))) break;
         tc::tc_fence_after();
       }
       if (have_next) {
         q_ready();
         q_loaded = true;
       }
-      // ---- output ----
+      // ---- output: this group's half of the columns ----
       if (warp_live) {
         const bool whole = pc.slot < 0;
         const float inv = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
@@ -931,7 +1110,7 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
         uint16_t* orow = a.out + (tok * (a.Hkv * a.G) + pc.h * a.G + rt % a.G) * D;
         const int64_t prow = static_cast<int64_t>(pc.slot) * a.part_rows + rt;
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
           uint32_t o[32];
           __syncwarp();
           if (pc.n > 0) {
@@ -942,32 +1121,11 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
             for (int i = 0; i < 32; i++) o[i] = 0u;
           }
           if (dirty && live) {
-            for (int j = 0; j < pc.n; j++) {
-              const int tl = pc.j0 + j < pc.nsink ? pc.j0 + j : pc.lo + pc.j0 + j - pc.nsink;
-              const int t0 = tl * KT;
-              if (!(t0 + KT - 1 > pc.pos0 || (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S))) {
-                // unmasked: its values went through the products as they are, unless a page of it is bad
-                bool gap = false;
-                for (int x = 0; x < KT; x += 8) {
-                  const int64_t pg = (static_cast<int64_t>(t0) + x) / a.page;
-                  const int blk = pg < a.n_pages ? a.block_table[pc.b * a.n_pages + pg] : -1;
-                  gap |= blk < 0 || blk >= a.n_blocks;
-                }
-                if (!gap) continue;
-              }
-              for (int x = 0; x < KT; x++) {
-                const int key = t0 + x;
-                if (key > p || !(a.W == 0 || key > p - a.W || key < a.S)) continue;
-                const int64_t pg = key / a.page;
-                const int blk = pg < a.n_pages ? a.block_table[pc.b * a.n_pages + pg] : -1;
-                if (blk < 0 || blk >= a.n_blocks) continue;
-                const uint16_t* v = a.v_pool + ((static_cast<int64_t>(blk) * a.page + key % a.page) * a.Hkv + pc.h) * D + c0;
+            float y[32];
+            for (int i = 0; i < 32; i++) y[i] = 0.f;
+            add_nonfinite<D, KT>(a, pc, p, p_last, c0, y);
 #pragma unroll
-                for (int i = 0; i < 32; i++)
-                  if ((v[i] & 0x7f80u) == 0x7f80u)
-                    o[i] = __float_as_uint(__uint_as_float(o[i]) + bf16_bits_to_f32(v[i]));
-              }
-            }
+            for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) + y[i]);
           }
           if (!live) continue;
           if (whole) {
@@ -986,7 +1144,7 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
               *reinterpret_cast<uint4*>(a.ws_o + prow * D + c0 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
-        if (!whole && live) a.ws_ml[prow] = make_float2(m_ref, l);
+        if (!whole && live && wg == 0) a.ws_ml[prow] = make_float2(m_ref, l);
       }
       if (pc.n > 0) {
         tc::tc_fence_before();
@@ -1000,16 +1158,18 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
     if (!ok) {
       if (lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
       asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      tc::tmem_wait_ld();
     }
   } else if (INT8) {
-    // ---------------- int8 -> bf16 (warps 8-11) ----------------
-    const int ct = tid - 256;
+    // ---------------- int8 -> bf16 (warps 12-15) ----------------
+    const int ct = tid - 384;
     Ring st, sg;
     uint32_t uses = 0;
     bool ok = true;
     for (int k = 0; ok; k++) {
       const int slot = k % kPieces;
-      ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->pc_full[slot], (k / kPieces) & 1, abort));
+      ok = wait_all(&ax->pc_full[slot], (k / kPieces) & 1, abort);
       if (!ok) break;
       const int n = ax->pc[slot].n, last = ax->pc[slot].last;
       __syncwarp();
@@ -1017,9 +1177,9 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
       if (last) break;
       for (int f = 0; f < 2 * n; f++) {
         const bool is_v = !(f == 0 || ((f & 1) && f != 2 * n - 1));
-        ok = __all_sync(0xffffffffu, tc::bar_wait(&a8->st_full[sg.s], sg.ph, abort));
+        ok = wait_all(&a8->st_full[sg.s], sg.ph, abort);
         if (ok && uses >= static_cast<uint32_t>(a.stages))
-          ok = __all_sync(0xffffffffu, tc::bar_wait(&ax->kv_empty[st.s], st.ph ^ 1, abort));
+          ok = wait_all(&ax->kv_empty[st.s], st.ph ^ 1, abort);
         if (!ok) break;
         const unsigned char* src = sI8 + sg.s * (STAGE / 2);
         unsigned char* dst = sKV + st.s * STAGE;
@@ -1029,22 +1189,28 @@ __global__ void __launch_bounds__(INT8 ? 384 : 256, 1)
         auto widen = [&](int row_bytes_log) {
           const int pcs = 1 << (row_bytes_log - 4);  // 16-code pieces per row
           const int nsub = row_bytes_log == 6 ? 1 : (1 << row_bytes_log) / 64;
-#pragma unroll 4
-          for (int i = ct; i < STAGE / 32; i += 128) {
-            const int row = (i & 7) + 8 * ((i >> 3) / pcs), pce = (i >> 3) % pcs;
+          constexpr int N = STAGE / 32 / 128;  // pieces per thread
+          uint4 w[N];
+#pragma unroll
+          for (int y = 0; y < N; y++) {
+            const int i = ct + 128 * y, row = (i & 7) + 8 * ((i >> 3) / pcs), pce = (i >> 3) % pcs;
             const unsigned char* s;
             if (row_bytes_log == 6)  // 64-byte rows, 64-byte swizzle
               s = src + row * 64 + ((pce ^ ((row >> 1) & 3)) << 4);
             else  // [8-row group][128-byte block][8 rows], 128-byte swizzle
               s = src + (((row >> 3) << (row_bytes_log - 7)) + (pce >> 3)) * 1024 + (row & 7) * 128 +
                   (((pce & 7) ^ (row & 7)) << 4);
-            const uint4 w = *reinterpret_cast<const uint4*>(s);
+            w[y] = *reinterpret_cast<const uint4*>(s);
+          }
+#pragma unroll
+          for (int y = 0; y < N; y++) {
+            const int i = ct + 128 * y, row = (i & 7) + 8 * ((i >> 3) / pcs), pce = (i >> 3) % pcs;
             unsigned char* d = dst + ((row >> 3) * nsub + (pce >> 2)) * 1024 + (row & 7) * 128;
             const int ch = (pce & 3) * 2;
-            *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) =
-                make_uint4(int8_to_bf16x2<0>(w.x), int8_to_bf16x2<1>(w.x), int8_to_bf16x2<0>(w.y), int8_to_bf16x2<1>(w.y));
-            *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) << 4)) =
-                make_uint4(int8_to_bf16x2<0>(w.z), int8_to_bf16x2<1>(w.z), int8_to_bf16x2<0>(w.w), int8_to_bf16x2<1>(w.w));
+            *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) = make_uint4(
+                int8_to_bf16x2<0>(w[y].x), int8_to_bf16x2<1>(w[y].x), int8_to_bf16x2<0>(w[y].y), int8_to_bf16x2<1>(w[y].y));
+            *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(
+                int8_to_bf16x2<0>(w[y].z), int8_to_bf16x2<1>(w[y].z), int8_to_bf16x2<0>(w[y].w), int8_to_bf16x2<1>(w[y].w));
           }
         };
         constexpr int LD = D == 256 ? 8 : 7;
@@ -1201,7 +1367,7 @@ int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int
   if (smem_limit_once(configured, kernel, kMaxSmem) != SKV_OK) return SKV_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms / CTAS * CTAS, 1, 1);
-  cfg.blockDim = dim3(INT8 ? 384 : 256, 1, 1);
+  cfg.blockDim = dim3(kThreads<INT8>, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1302,6 +1468,8 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
   a.page = page;
   a.rb = 8;  // rows per box: the largest power of two up to 64 that divides the page
   while (a.rb < 64 && page % (2 * a.rb) == 0) a.rb *= 2;
+  while ((1u << a.page_shift) < static_cast<uint32_t>(page)) a.page_shift++;
+  a.page_mul = static_cast<uint32_t>(((((static_cast<uint64_t>(1) << a.page_shift) - page) << 32) / page) + 1);
   a.block_table = block_table;
   a.n_pages = n_pages;
   a.q_start = q_start;
@@ -1326,7 +1494,7 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
   const int q_rows = q_start ? tile_rows(n_tok, G, ctas) : G;
   a.q_bytes = ((q_rows < kRows ? q_rows : kRows) + 7) / 8 * 8 * d * 2;
   const int aux = static_cast<int>(sizeof(Aux)) + (int8 ? static_cast<int>(sizeof(Aux8)) : 0);
-  const int room = kMaxSmem - 1024 - aux - a.q_bytes;
+  const int room = kMaxSmem - aux - a.q_bytes;
   if (int8) {
     a.stages = ctas == 2 ? 3 : 4;
     if (d == 128) a.stages *= 2;
@@ -1336,7 +1504,7 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
     a.stages = room / stage;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
   }
-  const int smem = 1024 + a.q_bytes + a.stages * stage + a.staging * (stage / 2) + aux;
+  const int smem = a.q_bytes + a.stages * stage + a.staging * (stage / 2) + aux;
 
   CUtensorMap km, vm;
   const int block = int8 ? 128 : 64;                         // columns of a 128-byte block
