@@ -54,14 +54,19 @@ constexpr float kLazy = 8.f;       // log2 units a maximum may grow before O is 
 constexpr int kSplitPerUnit = 8;   // pieces that write partials, per CTA or pair (at most 4 per SM)
 constexpr uint32_t kSCol = 256;    // tensor memory: O in [0, D), S/P buffers from here
 constexpr int kMaxSmem = 227 * 1024;
+constexpr int kOutBytes = 8 * 2048;
 
 // Warp 0 copies, warp 1 issues products, warps 2 and 3 read int8 scales, two
 // groups of four warps take the softmax of the two halves of a tile's keys,
 // and for int8 rows four warps widen them.
 template <bool INT8>
 constexpr int kThreads = INT8 ? 512 : 384;
+// Keys per tile.  Pairs: 128, what two logit buffers beside O leave room for at
+// D = 256.  Single CTAs are bound by reading the cache, with 32 KB stages.
+__host__ __device__ constexpr int keys_per_tile(int d, int ctas) { return ctas == 2 ? 128 : 64 * (256 / d); }
+
 struct Piece {
-  int tok0, rows;     // first token, valid rows of the whole tile (tokens * G)
+  int tok0, toks;     // first token, tokens of the whole tile
   int pos0;           // position of the first token
   int b, h;
   int lo, nsink;      // first window tile, sink tiles before it
@@ -71,9 +76,7 @@ struct Piece {
 };
 
 struct PagedArgs {
-  int B, n_tok, Hkv, G, tpt;  // tpt: tokens per query tile
-  const uint16_t* q;
-  int64_t q_stride;
+  int B, n_tok, Hkv, G, tpc, tpt;  // tokens per CTA's 128 rows, and per query tile
   const uint16_t* v_pool;     // bf16 rows, for the non-finite pass only
   const __half *k_scale, *v_scale;
   int64_t n_blocks;
@@ -87,7 +90,9 @@ struct PagedArgs {
   uint16_t* out;
   int32_t* status;
   int stages, staging;        // ring depths
-  int q_bytes;                // shared memory of the query tile
+  int thin;                   // int8: query tiles of at most 32 rows; the other rows' softmax warps widen instead
+  int q_bytes;                // shared memory of the query tile: D / 64 column blocks of q_sub bytes
+  int q_sub, q_box;           // (128 per row, rounded up to 1024; pairs: 128 rows); bytes a copy of one brings
   int part_rows;              // rows of a partial slot
   int max_split;              // partial slots
   float part_cost;            // tiles' worth of writing and joining a partial
@@ -101,18 +106,16 @@ struct alignas(16) Aux {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   // Two barriers where a waiter may skip tiles: when S(t + 1) is there, O of
   // t - 1 is done and of t may not be, and one parity could not tell them apart.
-  uint64_t s_full[2], p_full[2], pv_done[2], q_full, o_free, mma_idle;
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_free, o_free, mma_idle;
   uint64_t x_full[2][4];  // per 32 rows: both softmax warps' values are in `x`
   uint64_t pc_full[kPieces], pc_empty[kPieces];
   Piece pc[kPieces];
   uint32_t tile_bad[kTileInfo];  // bit i: rows [8 i, 8 i + 8) of the tile have no page
   union {
-    struct {
-      int cand_p[2][kCand], cand_s[2][kCand], cand_u[2];  // while planning: pieces, those of split items, tiles
-    };
+    float2 cand[16];       // while planning: each warp's best cost and candidate
     float x[2][2][kRows];  // [exchange parity][group][row]: maxima of a tile, at a piece's end sums
   };
-  int nmax, units, items, split_c, split_from;
+  int nmax, items;
   uint32_t tmem_base;
   int dirty;  // a value that only some queries of a tile see was not finite
   int abort;
@@ -124,7 +127,7 @@ struct alignas(16) Aux8 {  // int8 rows only
   alignas(16) float ks[kScaleRing][kRows], vs[kScaleRing][kRows];
 };
 
-static_assert(sizeof(Aux) <= 3072, "what the bf16 pair kernel's query tile and five stages leave");
+static_assert(sizeof(Aux) <= 3072, "room beside the query tile, the stages and the output rows");
 
 // ---- work list -------------------------------------------------------------------
 
@@ -248,6 +251,16 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
 __device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t sbo) {
   return (static_cast<uint64_t>((sbo >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
+}
+
+// One 64-column block of a query tile: rows (token, head of the group).
+__device__ __forceinline__ void tma_query(uint32_t dst, const CUtensorMap* map, int head, int tok, int sub,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(head), "r"(tok), "r"(sub), "r"(tc::smem_addr(bar))
+      : "memory");
 }
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int b_mn) {
@@ -378,6 +391,27 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
+// A warp writes 64 bytes of each lane's row: through shared memory, so that a
+// store covers eight rows of 64 consecutive bytes (32 rows of 16 bytes take
+// the store unit 32 lines each, and ran 3 to 7 K clocks per piece).  Row
+// `id` (-1: none) starts at base + id * pitch.
+__device__ __forceinline__ void put_rows(unsigned char* buf, int lane, const uint32_t (&w)[16], int id, char* base,
+                                         int pitch) {
+#pragma unroll
+  for (int c = 0; c < 4; c++)
+    *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const int row = 8 * k + (lane >> 2), c = lane & 3;
+    const uint4 v = *reinterpret_cast<const uint4*>(buf + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+    const int to = __shfl_sync(0xffffffffu, id, row);
+    if (to >= 0) *reinterpret_cast<uint4*>(base + static_cast<int64_t>(to) * pitch + 16 * c) = v;
+  }
+  __syncwarp();
+}
+
 // Key tile j of a piece.
 __device__ __forceinline__ int tile_of(const Piece& pc, int j) {
   j += pc.j0;
@@ -446,21 +480,30 @@ __device__ __noinline__ void add_nonfinite(const PagedArgs& a, const Piece& pc, 
 template <int D, int CTAS, bool INT8>
 __global__ void __launch_bounds__(kThreads<INT8>, 1)
     paged_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                 const PagedArgs a) {
-  constexpr int KT = 64 * CTAS;          // keys per tile
+                 const __grid_constant__ CUtensorMap q_map, const PagedArgs a) {
+  constexpr int KT = keys_per_tile(D, CTAS);
+  constexpr int KR = KT / CTAS;          // of them, this CTA's rows of K
   constexpr int NSUB = D / 64;           // 64-column blocks of a row
   constexpr int VSUB = NSUB / CTAS;      // those of this CTA's part of V
-  constexpr int STAGE = 64 * D * 2;      // bytes of a K or V stage (either part)
+  constexpr int STAGE = KR * D * 2;      // bytes of a K or V stage (this CTA's part)
   constexpr int THREADS = kThreads<INT8>;
   constexpr uint32_t SBO_K = NSUB * 1024, SBO_V = VSUB * 1024;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sQ = smem_raw;  // 1024-byte aligned, as the swizzled tiles need (checked below)
   unsigned char* sKV = sQ + a.q_bytes;
   unsigned char* sI8 = sKV + a.stages * STAGE;
-  Aux* ax = reinterpret_cast<Aux*>(sI8 + (INT8 ? a.staging * (STAGE / 2) : 0));
+  unsigned char* sOut = sI8 + (INT8 ? a.staging * (STAGE / 2) : 0);  // 2 KB per softmax warp
+  Aux* ax = reinterpret_cast<Aux*>(sOut + kOutBytes);
   Aux8* a8 = reinterpret_cast<Aux8*>(ax + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CTAS == 1 ? 0u : tc::cluster_rank();
+  // Softmax warps and widening warps: with at most 32 rows a tile, as single
+  // tokens have, warps 4 and 8 do the softmax and 5, 6, 9, 10 join the widening
+  // (7 and 11 rest).  One row of work for six warps, two for four: a 64-key
+  // tile took 3.3K clocks, all in the widening.
+  const bool thin = INT8 && CTAS == 1 && a.thin;
+  const uint32_t n_soft = thin ? 2 : 8, n_wide = thin ? 8 : 4;
+  const bool softer = warp >= 4 && warp < 12 && (!thin || (warp & 3) == 0);
   const int unit = blockIdx.x / CTAS, n_units = gridDim.x / CTAS;
   volatile int* abort = &ax->abort;
 
@@ -469,12 +512,12 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
 #pragma unroll 1
     for (int s = 0; s < kMaxStages; s++) {
       // int8: the widening warps of both CTAs; bf16: the copies, and on the leader a note from the peer's
-      tc::bar_init(&ax->kv_full[s], INT8 ? 4 * CTAS : (rank == 0 ? CTAS : 1));
+      tc::bar_init(&ax->kv_full[s], INT8 ? n_wide * CTAS : (rank == 0 ? CTAS : 1));
       tc::bar_init(&ax->kv_empty[s], 1);
     }
     for (int s = 0; s < 2; s++) {
       tc::bar_init(&ax->s_full[s], 1);
-      tc::bar_init(&ax->p_full[s], 8 * CTAS);
+      tc::bar_init(&ax->p_full[s], n_soft * CTAS);
       tc::bar_init(&ax->pv_done[s], 1);
     }
 #pragma unroll 1
@@ -482,35 +525,33 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       tc::bar_init(&ax->x_full[0][s], 2);
       tc::bar_init(&ax->x_full[1][s], 2);
     }
-    tc::bar_init(&ax->q_full, 8 * CTAS);
-    tc::bar_init(&ax->o_free, 8 * CTAS);
+    tc::bar_init(&ax->q_full, rank == 0 ? CTAS : 1);  // the copy, and on the leader a note from the peer's
+    tc::bar_init(&ax->q_free, 1);
+    tc::bar_init(&ax->o_free, n_soft * CTAS);
     tc::bar_init(&ax->mma_idle, 1);
 #pragma unroll 1
     for (int s = 0; s < kPieces; s++) {
       tc::bar_init(&ax->pc_full[s], 1);
-      tc::bar_init(&ax->pc_empty[s], INT8 ? 15 : 9);  // MMA thread, softmax warps, (scale and widening warps)
+      tc::bar_init(&ax->pc_empty[s], 1 + n_soft + (INT8 ? 2 + n_wide : 0));  // products, softmax, scales, widening
     }
     if (INT8) {
 #pragma unroll 1
       for (int s = 0; s < kMaxStaging; s++) {
         tc::bar_init(&a8->st_full[s], 1);
-        tc::bar_init(&a8->st_empty[s], 4);
+        tc::bar_init(&a8->st_empty[s], n_wide);
       }
 #pragma unroll 1
       for (int s = 0; s < kScaleRing; s++) {
         tc::bar_init(&a8->sc_full[s], 1);
-        tc::bar_init(&a8->sc_empty[s], 8);
+        tc::bar_init(&a8->sc_empty[s], n_soft);
       }
     }
     ax->abort = (tc::smem_addr(smem_raw) & 1023u) != 0;  // every wait would give up at once
     ax->dirty = 0;
     ax->nmax = 0;
-    ax->units = 0;
     ax->items = 0;
-    ax->cand_u[0] = ax->cand_u[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid < 2 * kCand) (&ax->cand_p[0][0])[tid] = (&ax->cand_s[0][0])[tid] = 0;
   if (warp == 1) {
     if (CTAS == 1) {
       tc::tmem_alloc<512>(&ax->tmem_base);
@@ -524,110 +565,113 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   __syncthreads();
   tc::tc_fence_after();
 
+  int split_c, split_from;
   // ---- plan: tiles per piece -----------------------------------------------------
   // Candidate k cuts the longest item into k pieces of c = ceil(nmax / k)
   // tiles and every other one into ceil(tiles / c): all items, or those past
   // the last full round over the CTAs.  Its cost is the number of rounds times
   // a piece (the last at full length); a piece pays kOvh tiles for filling and
   // draining its pipeline, a split kJoin tiles once and part_cost per piece
-  // for its partials.
+  // for its partials.  Each warp weighs every NW-th candidate, a lane per
+  // request; the batch waits in shared memory that the ring will take over.
   {
     constexpr float kOvh = 3.f, kJoin = CTAS == 1 ? 4.f : 3.f;
-    int nmax = 0, units = 0, items = 0;
+    constexpr int NW = THREADS / 32;
+    int2* req = reinterpret_cast<int2*>(sKV);  // (query tiles, key tiles of the longest)
+    int nmax = 0, items = 0;
 #pragma unroll 1
     for (int b = tid; b < a.B; b += THREADS) {
       const Req r = request<KT>(a, b, unit == 0 && rank == 0);
+      req[b] = make_int2(r.nqt, r.ntmax);
       nmax = max(nmax, r.ntmax);
-      units += r.nqt * r.ntmax;
       items += r.nqt;
     }
-    nmax = __reduce_max_sync(0xffffffffu, nmax);
-    units = __reduce_add_sync(0xffffffffu, units);
-    items = __reduce_add_sync(0xffffffffu, items);
-    if (lane == 0 && nmax > 0) {
-      atomicMax(&ax->nmax, nmax);
-      atomicAdd(&ax->units, units);
-      atomicAdd(&ax->items, items);
+    if (warp * 32 < a.B) {
+      nmax = __reduce_max_sync(0xffffffffu, nmax);
+      items = __reduce_add_sync(0xffffffffu, items);
+      if (lane == 0 && items > 0) {
+        atomicMax(&ax->nmax, nmax);
+        atomicAdd(&ax->items, items);
+      }
     }
     __syncthreads();
     nmax = ax->nmax;
     items = ax->items * a.Hkv;
-    // Items kept whole in the second set of candidates: the full rounds.  The
-    // requests' order is the work list's; only a batch that one warp holds is
-    // looked at this way.
+    // Items kept whole in the second half of the candidates: the full rounds,
+    // in the work list's order; only a batch that one warp holds is looked at
+    // this way.
     const int x1 = a.B <= 32 && items > n_units ? items / n_units * n_units : 0;
-    const int c0 = (nmax + lane) / (lane + 1), c1 = (nmax + lane + 32) / (lane + 33);
+    const int nk = min(nmax, a.B > 512 ? 8 : kCand);
+    float best = 3e38f;
+    int pick = 0;
 #pragma unroll 1
-    for (int set = 0; set < (x1 > 0 ? 2 : 1); set++) {
-      int p0 = 0, p1 = 0, s0 = 0, s1 = 0, u = 0, seen = 0;
+    for (int i = warp; i < nk * (x1 > 0 ? 2 : 1); i += NW) {
+      const bool rest = i >= nk;
+      const int k = rest ? i - nk + 1 : i + 1;
+      const int c = (nmax + k - 1) / k;
+      const float rc = 1.f / c;
+      int P = 0, S = 0;
+      float u = 0.f, main_u = 0.f;
 #pragma unroll 1
-      for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-        const int m = min(32, a.B - b0 - warp * 32);
-        if (m <= 0 || nmax <= 1) break;
-        const Req r = request<KT>(a, b0 + tid, false);
-#pragma unroll 1
-        for (int i = 0; i < m; i++) {
-          const int all = __shfl_sync(0xffffffffu, r.nqt, i) * a.Hkv, nt = __shfl_sync(0xffffffffu, r.ntmax, i);
-          const int n = set == 0 ? all : max(0, seen + all - max(seen, x1));  // items that may be cut
-          seen += all;
-          u += n * nt;
-          const int k0 = pieces_of(nt, c0), k1 = pieces_of(nt, c1);
-          p0 += n * k0;
-          p1 += n * k1;
-          s0 += k0 > 1 ? n * k0 : 0;
-          s1 += k1 > 1 ? n * k1 : 0;
-        }
-      }
-      if (p0) {
-        atomicAdd(&ax->cand_p[set][lane], p0);
-        atomicAdd(&ax->cand_p[set][lane + 32], p1);
-        if (s0) atomicAdd(&ax->cand_s[set][lane], s0);
-        if (s1) atomicAdd(&ax->cand_s[set][lane + 32], s1);
-        if (lane == 0) atomicAdd(&ax->cand_u[set], u);
-      }
-    }
-    __syncthreads();
-    if (warp == 0) {
-      float best = 3e38f;
-      int pick = 0;
-      const float main_u = static_cast<float>(ax->cand_u[0] - ax->cand_u[1]);  // tiles of the items kept whole
-#pragma unroll 1
-      for (int i = lane; i < 2 * kCand; i += 32) {
-        const int set = i / kCand, k = i % kCand;
-        const float P = static_cast<float>(ax->cand_p[set][k]), Sp = static_cast<float>(ax->cand_s[set][k]);
-        const int c = (k & 32) ? c1 : c0;
-        if (nmax > 1 && k < nmax && Sp <= static_cast<float>(a.max_split) && (set == 0 || x1 > 0)) {
-          const float u = static_cast<float>(ax->cand_u[set]);
-          float cost = set ? main_u / n_units + x1 / n_units * kOvh : 0.f;
-          if (P > 0.f)
-            cost += (ceilf(P / n_units) - 1.f) * (u / P + kOvh) + c + kOvh + (Sp > 0.f ? kJoin + Sp * a.part_cost : 0.f);
-          if (cost < best) {
-            best = cost;
-            pick = i;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int2 r = b0 + lane < a.B ? req[b0 + lane] : make_int2(0, 0);
+        const int all = r.x * a.Hkv;
+        int n = all;  // items that may be cut
+        if (rest) {
+          int sum = all;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
           }
+          n = max(0, sum - max(sum - all, x1));
         }
+        // ceil(tiles / c): the quotient is half a c-th away from every integer, its error below 65 * 2^-23
+        const int ps = nmax < (1 << 15) ? max(1, static_cast<int>((r.y + c - 0.5f) * rc)) : pieces_of(r.y, c);
+        P += n * ps;
+        S += ps > 1 ? n * ps : 0;
+        u += static_cast<float>(n) * r.y;
+        main_u += static_cast<float>(all - n) * r.y;
       }
+      P = __reduce_add_sync(0xffffffffu, P);
+      S = __reduce_add_sync(0xffffffffu, S);
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
-        const float ob = __shfl_xor_sync(0xffffffffu, best, o);
-        const int oi = __shfl_xor_sync(0xffffffffu, pick, o);
-        if (ob < best || (ob == best && oi < pick)) {
-          best = ob;
-          pick = oi;
+        u += __shfl_xor_sync(0xffffffffu, u, o);
+        if (rest) main_u += __shfl_xor_sync(0xffffffffu, main_u, o);
+      }
+      if (S <= a.max_split) {
+        float cost = rest ? main_u / n_units + x1 / n_units * kOvh : 0.f;
+        if (P > 0)
+          cost += (ceilf(static_cast<float>(P) / n_units) - 1.f) * (u / P + kOvh) + c + kOvh +
+                  (S > 0 ? kJoin + S * a.part_cost : 0.f);
+        if (cost < best) {
+          best = cost;
+          pick = i;
         }
       }
-      if (lane == 0) {
-        const int k = pick % kCand;
-        ax->split_c = max(1, (nmax + k) / (k + 1));
-        ax->split_from = pick >= kCand ? x1 : 0;
+    }
+    if (lane == 0) ax->cand[warp] = make_float2(best, __int_as_float(pick));
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < NW; w++) {
+      const float2 o = ax->cand[w];
+      const int oi = __float_as_int(o.y);
+      if (w == 0 || o.x < best || (o.x == best && oi < pick)) {
+        best = o.x;
+        pick = oi;
       }
     }
+    tc::fence_async_smem();  // the copies write where the batch was
+    split_from = pick >= nk && nk > 0 ? x1 : 0;
+    const int k = pick >= nk && nk > 0 ? pick - nk + 1 : pick + 1;
+    split_c = max(1, (nmax + k - 1) / k);
     if (CTAS == 2)
       tc::cluster_sync();  // also: the peer's barriers exist before any remote access
     else
       __syncthreads();
   }
-  const int c = ax->split_c, whole = ax->split_from;  // tiles per piece; items before this one are not cut
+  const int c = split_c, whole = split_from;  // tiles per piece; items before this one are not cut
   if (tid == 0 && ax->tmem_base != 0) *abort = 1;
   // All 512 columns are this CTA's, so they start at 0: a constant keeps the
   // products' addresses out of registers.
@@ -668,7 +712,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     scan();
     const uint32_t full = 0xffffffffu;
     // boxes of a tile: this CTA copies boxes_k of them for K, all for V
-    const int boxes_k = 64 / a.rb, rb_log = 31 - __clz(a.rb);
+    const int boxes_k = KR / a.rb, rb_log = 31 - __clz(a.rb);
     const uint32_t box_k = static_cast<uint32_t>(a.rb) * D * (INT8 ? 1 : 2), box_v = box_k / CTAS;
     Ring st;  // K/V stage (bf16) or staging slot (int8)
     const int depth = INT8 ? a.staging : a.stages;
@@ -676,7 +720,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     uint64_t* empties = INT8 ? a8->st_empty : ax->kv_empty;
     const uint32_t ring0 = tc::smem_addr(INT8 ? sI8 : sKV);
     constexpr int SLOT = INT8 ? STAGE / 2 : STAGE;
-    uint32_t uses = 0, tile_no = 0;
+    uint32_t uses = 0, tile_no = 0, qn = 0;  // copies, tiles, query tiles so far
     bool ok = true;
 #pragma unroll 1
     for (int k = 0; ok; k++) {
@@ -720,7 +764,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         tile_range<KT>(a, q, qt, pc.lo, pc.nsink, nt);
         pc.b = b32 + w;
         pc.tok0 = q.start + qt * a.tpt;
-        pc.rows = min(a.tpt, q.nq - qt * a.tpt) * a.G;
+        pc.toks = min(a.tpt, q.nq - qt * a.tpt);
         pc.pos0 = q.T - q.nq + qt * a.tpt;
         const int each = nt / n_seg, more = nt % n_seg;  // the first `more` pieces take a tile more
         pc.j0 = seg * each + min(seg, more);
@@ -728,13 +772,13 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         pc.slot = split ? sb + (item - kept) * nsw + seg : -1;
         if (split && seg == 0 && rank == 0 && lane == 0) {
           const int at = ib + item - kept;
-          a.ws_item[2 * at] = make_int4(pc.tok0, pc.rows, pc.h, pc.slot);
+          a.ws_item[2 * at] = make_int4(pc.tok0, pc.toks * a.G, pc.h, pc.slot);
           a.ws_item[2 * at + 1] = make_int4(nsw, 0, 0, 0);
         }
       } else {
         pc.last = 1;
         pc.n = 0;
-        pc.rows = 0;
+        pc.toks = 0;
         pc.slot = -1;
       }
       const int slot = k % kPieces;
@@ -746,7 +790,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       if (pc.last) break;
       // Copies, in the order the products take them.  Lane i holds the box of
       // rows [i rb, i rb + rb) of a tile; table entries are read two tiles ahead.
-      const int p_hi = pc.pos0 + pc.rows / a.G - 1;  // keys past it are not copied
+      const int p_hi = pc.pos0 + pc.toks - 1;  // keys past it are not copied
       BoxLoad l0 = box_load<KT>(a, pc, 0, lane), l1 = box_load<KT>(a, pc, 1, lane);
       Box cur{-1, false}, prev;
 #pragma unroll 1
@@ -785,6 +829,15 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
           uses++;
           st.next(depth);
         }
+        if (ok && j == 0) {  // the query tile, behind the first keys: it is free once the last piece's logits are done
+          if (qn > 0 && !(ok = wait_all(&ax->q_free, (qn - 1) & 1, abort))) break;
+          qn++;
+          if (lane == 0) tc::bar_arrive_expect_tx(&ax->q_full, NSUB * a.q_box);
+          __syncwarp();
+          if (lane < NSUB)
+            tma_query(tc::smem_addr(sQ) + lane * a.q_sub, &q_map, pc.h * a.G, pc.tok0 + static_cast<int>(rank) * a.tpc,
+                      lane, &ax->q_full);
+        }
       }
     }
     if (!ok) {  // gave up: let the copies in flight land before the CTA leaves
@@ -817,6 +870,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       constexpr uint32_t id_qk = idesc_bf16(kRows * CTAS, KT, 0), id_pv = idesc_bf16(kRows * CTAS, D, 1);
       const uint32_t dQ = desc_lo(tc::smem_addr(sQ), 16), dK = desc_lo(tc::smem_addr(sKV), 16),
                      dV = desc_lo(tc::smem_addr(sKV), 1024);
+      const uint32_t q_step = CTAS == 2 ? kRows * 128 >> 4 : a.q_sub >> 4;
       Ring st;
       uint32_t g = 0, np = 0;  // tiles, pieces with work so far
       bool ok = true;
@@ -828,7 +882,9 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         const int n = ax->pc[slot].n, last = ax->pc[slot].last;
         tc::bar_arrive(&ax->pc_empty[slot]);
         if (last) break;
-        if (rank != 0) {  // the peer passes on to the leader that its stages are full
+        if (rank != 0) {  // the peer passes on to the leader that its query tile and its stages are full
+          if (n > 0 && (ok = wait(&ax->q_full, np & 1, abort))) arrive_leader<CTAS>(&ax->q_full);
+          np += n > 0;
 #pragma unroll 1
           for (int f = 0; !INT8 && ok && f < 2 * n; f++) {
             ok = wait(&ax->kv_full[st.s], st.ph, abort);
@@ -851,10 +907,11 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
 #pragma unroll
               for (int x = 0; x < D / 16; x++) {
                 const uint32_t off = ((x >> 2) * 1024 + (x & 3) * 32) >> 4;
-                mma_ss<CTAS>(d, desc(dQ + off, SBO_K), desc(kv + off, SBO_K), id_qk, x > 0);
+                mma_ss<CTAS>(d, desc(dQ + (x >> 2) * q_step + (x & 3) * 2, 1024), desc(kv + off, SBO_K), id_qk, x > 0);
               }
               commit<CTAS>(&ax->kv_empty[st.s]);
               commit<CTAS>(&ax->s_full[(g + j) & 1]);
+              if (j == n - 1) commit<CTAS>(&ax->q_free);
             }
             st.next(a.stages);
           }
@@ -900,7 +957,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&ax->pc_empty[slot]);
         if (pc.last) break;
-        const int p_hi = pc.pos0 + pc.rows / a.G - 1;
+        const int p_hi = pc.pos0 + pc.toks - 1;
         const int rb_log = 31 - __clz(a.rb);
         int j = static_cast<int>((g ^ (warp & 1)) & 1);  // first tile of this warp's parity
         BoxLoad l0 = box_load<KT>(a, pc, j, lane);
@@ -931,7 +988,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         g += pc.n;
       }
     }
-  } else if (warp < 12) {
+  } else if (softer) {
     // ---------------- softmax and output: thread = row, two groups ----------------
     // Group `wg` takes half of every tile's keys and half of the output's
     // columns: the logits-to-weights time stands between two products of the
@@ -941,9 +998,8 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     // maximum, and add up their sums at a piece's end.
     const int wg = (warp - 4) >> 2, quad = warp & 3;
     const int r = 32 * quad + lane;                     // row within this CTA
-    const int rt = static_cast<int>(rank) * kRows + r;  // row within the tile
+    const int tok_r = r / a.G, head_r = r % a.G;        // its token within the CTA's part of the tile, its head
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
-    const int warp_row = static_cast<int>(rank) * kRows + 32 * quad;
     uint32_t g = 0, fills = 0, xc = 0;  // tiles, ring fills, exchanges so far
     bool ok = true;
 
@@ -958,27 +1014,6 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       return true;
     };
 
-    // Query rows of a piece: 16-byte copies into the swizzled tile.
-    auto load_q = [&](const Piece& pc) {
-      constexpr int CH = D / 8;
-      const int rows = min(kRows, pc.rows - static_cast<int>(rank) * kRows);
-#pragma unroll 1
-      for (int i = tid - 128; i < rows * CH; i += 256) {
-        const int row = i / CH, ch = i % CH, rr = static_cast<int>(rank) * kRows + row;
-        const int tok = pc.tok0 + rr / a.G;
-        const uint16_t* src = a.q + tok * a.q_stride + static_cast<int64_t>(pc.h * a.G + rr % a.G) * D + ch * 8;
-        const uint32_t dst = tc::smem_addr(sQ) + (row >> 3) * SBO_K + (ch >> 3) * 1024 + (row & 7) * 128 +
-                             (((ch & 7) ^ (row & 7)) << 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    auto q_ready = [&]() {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_leader<CTAS>(&ax->q_full);
-    };
     auto get = [&](int k, Piece& pc) -> bool {  // descriptor k
       const int slot = k % kPieces;
       if (!wait_all(&ax->pc_full[slot], (k / kPieces) & 1, abort)) return false;
@@ -990,22 +1025,15 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
 
     Piece pc;
     ok = get(0, pc);
-    bool q_loaded = false;
 #pragma unroll 1
     for (int k = 0; ok && !pc.last; k++) {
-      Piece next;
-      next.last = 1;
-      const int tok_i = rt / a.G;
-      const bool live = rt < pc.rows;
+      const int tok_i = static_cast<int>(rank) * a.tpc + tok_r;  // this row's token within the tile
+      const bool live = tok_r < a.tpc && tok_i < pc.toks;
       const int p = live ? pc.pos0 + tok_i : -1;  // this row's position: keys 0 .. p
-      const bool warp_live = warp_row < pc.rows;
+      // some row of the warp is used
+      const bool warp_live = 32 * quad < min(a.tpc, pc.toks - static_cast<int>(rank) * a.tpc) * a.G;
       float m_ref = -INFINITY, l = 0.f;           // the maximum that l is relative to
-      if (pc.n > 0 && !q_loaded) {
-        load_q(pc);
-        q_ready();
-      }
-      q_loaded = false;
-      const int p_last = pc.pos0 + pc.rows / a.G - 1;
+      const int p_last = pc.pos0 + pc.toks - 1;
 #pragma unroll 1
       for (int j = 0; j < pc.n; j++) {
         const uint32_t t = g + j;
@@ -1066,6 +1094,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
           }
           const float f = INT8 ? 1.f : a.scale_log2;
           float mc = fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]) * f, mo;
+          if (!live) mc = -INFINITY;  // a row without a query holds anything: it must not call for a rescale
           if (!(ok = exchange(mc, mo))) break;
           mc = fmaxf(mc, mo);
           const float m_new = mc > m_ref + kLazy || m_ref == -INFINITY ? fmaxf(mc, m_ref) : m_ref;
@@ -1182,12 +1211,8 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         }
       }
       if (!ok) break;
-      // Once the last logits are there the query tile is free: fetch the next one under the last product.
       const uint32_t t_last = g + pc.n - 1;
-      if (!(ok = get(k + 1, next))) break;
-      const bool have_next = !next.last && next.n > 0 && pc.n > 0;
       if (pc.n > 0) {
-        if (have_next) load_q(next);
         if (warp_live) {
           float lo;
           if (!(ok = exchange(l, lo))) break;
@@ -1196,18 +1221,16 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         if (!(ok = wait_all(&ax->pv_done[t_last & 1], (t_last >> 1) & 1, abort))) break;
         tc::tc_fence_after();
       }
-      if (have_next) {
-        q_ready();
-        q_loaded = true;
-      }
       // ---- output: this group's half of the columns ----
       if (warp_live) {
         const bool whole = pc.slot < 0;
         const float inv = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
         const bool dirty = !INT8 && *reinterpret_cast<volatile int*>(&ax->dirty) != 0;
         const int64_t tok = static_cast<int64_t>(pc.tok0) + tok_i;
-        uint16_t* orow = a.out + (tok * (a.Hkv * a.G) + pc.h * a.G + rt % a.G) * D;
-        const int64_t prow = static_cast<int64_t>(pc.slot) * a.part_rows + rt;
+        const int64_t prow = static_cast<int64_t>(pc.slot) * a.part_rows + tok_i * a.G + head_r;
+        unsigned char* buf = sOut + (warp - 4) * 2048;
+        const int id = !live ? -1 : whole ? static_cast<int>(tok * (a.Hkv * a.G)) + pc.h * a.G + head_r : static_cast<int>(prow);
+        char* base = whole ? reinterpret_cast<char*>(a.out) : reinterpret_cast<char*>(a.ws_o);
 #pragma unroll 1
         for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
           uint32_t o[32];
@@ -1227,21 +1250,15 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
 #pragma unroll
             for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) + y[i]);
           }
-          if (!live) continue;
-          if (whole) {
+          __syncwarp();
+#pragma unroll 1
+          for (int y = 0; y < (whole ? 1 : pc.n > 0 ? 2 : 0); y++) {  // 32 columns of bf16, or twice 16 of fp32
+            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint4 w;
-              w.x = pack_bf16(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-              w.y = pack_bf16(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-              w.z = pack_bf16(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-              w.w = pack_bf16(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
-              *reinterpret_cast<uint4*>(orow + c0 + i) = w;
-            }
-          } else if (pc.n > 0) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(a.ws_o + prow * D + c0 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 16; i++)
+              w[i] = whole ? pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv)
+                           : y ? o[16 + i] : o[i];
+            put_rows(buf, lane, w, id, base + (whole ? 2 * c0 : 4 * (c0 + 16 * y)), whole ? 2 * D : 4 * D);
           }
         }
         if (!whole && live && wg == 0) a.ws_ml[prow] = make_float2(m_ref, l);
@@ -1253,23 +1270,23 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       }
       g += pc.n;
       fills += 2 * pc.n;
-      pc = next;
+      ok = get(k + 1, pc);
     }
     if (!ok) {
       if (lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
-      asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
       tc::tmem_wait_ld();
     }
-  } else if (INT8) {
-    // ---------------- int8 -> bf16 (warps 12-15) ----------------
-    const int ct = tid - 384;
-    // Thread -> 16 codes of one row, D / 32 times a stage: ct % 8 is the row
+  } else if (INT8 && (warp >= 12 || (warp & 3) != 3)) {
+    // ---------------- int8 -> bf16 (warps 12-15, and where they are free 5, 6, 9, 10) ----------------
+    const int ct = warp >= 12 ? tid - 384 : 128 + 32 * ((warp & 3) - 1 + (warp >= 8 ? 2 : 0)) + lane;
+    // Thread -> 16 codes of one row, a few times a stage: ct % 8 is the row
     // of its 8-row group, so eight lanes read eight rows' swizzled pieces
     // (distinct banks) and write them the same way.  Piece `pce` of a row is
     // bytes 16 pce of the staged row and the 32 bytes at 32 pce of the wide
-    // one; a step further is 2048 staged bytes, 4096 wide ones.
-    constexpr int kSteps = D / 32;
+    // one; a step of 128 threads is 2048 staged bytes, 4096 wide ones.
+    constexpr int kSteps = STAGE / 4096;
+    const int jump = thin ? 2 : 1;
     auto offsets = [&](int row_bytes, uint32_t& s, uint32_t& d) {
       const int pcs = row_bytes / 16, row = ct & 7, grp = (ct >> 3) / pcs, pce = (ct >> 3) % pcs;
       if (row_bytes == 64)  // 64-byte rows, 64-byte swizzle
@@ -1304,13 +1321,13 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         unsigned char* dst = sKV + st.s * STAGE;
         const uint32_t s0 = is_v ? sv : sk, d0 = is_v ? dv : dk;
 #pragma unroll 1
-        for (int y0 = 0; y0 < kSteps; y0 += 4) {
+        for (int y0 = 0; y0 < kSteps; y0 += 4 * jump) {
           uint4 w[4];
 #pragma unroll
-          for (int y = 0; y < 4; y++) w[y] = *reinterpret_cast<const uint4*>(src + s0 + (y0 + y) * 2048);
+          for (int y = 0; y < 4; y++) w[y] = *reinterpret_cast<const uint4*>(src + s0 + (y0 + y * jump) * 2048);
 #pragma unroll
           for (int y = 0; y < 4; y++) {
-            unsigned char* d = dst + (y0 + y) * 4096;
+            unsigned char* d = dst + (y0 + y * jump) * 4096;
             *reinterpret_cast<uint4*>(d + d0) = make_uint4(int8_to_bf16x2<0>(w[y].x), int8_to_bf16x2<1>(w[y].x),
                                                            int8_to_bf16x2<0>(w[y].y), int8_to_bf16x2<1>(w[y].y));
             *reinterpret_cast<uint4*>(d + (d0 ^ 16)) = make_uint4(int8_to_bf16x2<0>(w[y].z), int8_to_bf16x2<1>(w[y].z),
@@ -1347,41 +1364,52 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   if (CTAS == 2) tc::cluster_sync();
 }
 
-// Joins the pieces of split items, one warp per row, in piece order.
+// Joins the pieces of split items in piece order, at most 64 of them (kCand).
+// With few rows a block takes a row, its warps every eighth piece; with many a
+// warp takes a row.  Lane l holds the weights of pieces l and l + 32.
 template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head, const int4* __restrict__ item,
                                                     const float2* __restrict__ ml, const float* __restrict__ o,
                                                     int part_rows, int G, int Hq, uint16_t* __restrict__ out) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32;  // columns per lane: float4 f at 4 (lane + 32 f)
+  __shared__ float red[8][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();  // launched early: the partials are complete from here on
-  const int lane = threadIdx.x & 31;
-  const int64_t tasks = static_cast<int64_t>(head[0]) * part_rows;
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); w < tasks;
-       w += static_cast<int64_t>(gridDim.x) * 8) {
-    const int64_t it = w / part_rows;
-    const int row = static_cast<int>(w - it * part_rows);
+  const int tasks = head[0] * part_rows;
+  const bool wide = tasks <= 2 * static_cast<int>(gridDim.x);  // a block per row
+  const int step = wide ? gridDim.x : gridDim.x * 8, first = wide ? blockIdx.x : blockIdx.x * 8 + warp;
+  const int s0 = wide ? warp : 0, ds = wide ? 8 : 1;
+#pragma unroll 1
+  for (int w = first; w < tasks; w += step) {
+    const int it = w / part_rows, row = w - it * part_rows;
     const int4 x = item[2 * it];
     const int n = item[2 * it + 1].x;
-    if (row >= x.y) continue;
-    const int64_t first = static_cast<int64_t>(x.w) * part_rows + row;
-    float m = -INFINITY;
-    for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[first + static_cast<int64_t>(s) * part_rows].x);
+    if (row >= x.y) continue;  // the same for the whole block where it takes a row
+    const int64_t at = static_cast<int64_t>(x.w) * part_rows + row;
+    float2 v0 = make_float2(-INFINITY, 0.f), v1 = v0;
+    if (lane < n) v0 = ml[at + static_cast<int64_t>(lane) * part_rows];
+    if (lane + 32 < n) v1 = ml[at + static_cast<int64_t>(lane + 32) * part_rows];
+    float m = fmaxf(v0.x, v1.x);
 #pragma unroll
     for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    float den = 0.f, acc[E];
+    // A piece without a visible key has weight 0, and its O may be unwritten; NaN sums keep theirs.
+    const bool none0 = v0.x == -INFINITY && v0.y == 0.f, none1 = v1.x == -INFINITY && v1.y == 0.f;
+    const float f0 = none0 ? 0.f : exp2f(v0.x - m), f1 = none1 ? 0.f : exp2f(v1.x - m);
+    float den = (none0 ? 0.f : f0 * v0.y) + (none1 ? 0.f : f1 * v1.y);
+#pragma unroll
+    for (int i = 16; i; i >>= 1) den += __shfl_xor_sync(0xffffffffu, den, i);
+    const uint32_t has0 = __ballot_sync(0xffffffffu, !none0), has1 = __ballot_sync(0xffffffffu, !none1);
+    float acc[E];
 #pragma unroll
     for (int e = 0; e < E; e++) acc[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < n; s++) {
-      const int64_t at = first + static_cast<int64_t>(s) * part_rows;
-      const float2 v = ml[at];
-      if (v.x == -INFINITY && v.y == 0.f) continue;  // no visible key in this piece (its O may be unwritten)
-      const float f = exp2f(v.x - m);
-      den += f * v.y;
-      const float* src = o + at * D + lane * E;
+#pragma unroll 8
+    for (int s = s0; s < n; s += ds) {
+      const float f = __shfl_sync(0xffffffffu, s < 32 ? f0 : f1, s & 31);
+      if (!(((s < 32 ? has0 : has1) >> (s & 31)) & 1u)) continue;
+      const float* src = o + (at + static_cast<int64_t>(s) * part_rows) * D + 4 * lane;
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
-        const float4 y = *reinterpret_cast<const float4*>(src + e);
+        const float4 y = *reinterpret_cast<const float4*>(src + 32 * e);
         acc[e] += f * y.x;
         acc[e + 1] += f * y.y;
         acc[e + 2] += f * y.z;
@@ -1389,10 +1417,29 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head
       }
     }
     const float inv = den != 0.f ? 1.f / den : 0.f;
-    uint16_t* dst = out + (static_cast<int64_t>(x.x + row / G) * Hq + x.z * G + row % G) * D + lane * E;
+    uint16_t* dst = out + (static_cast<int64_t>(x.x + row / G) * Hq + x.z * G + row % G) * D;
+    if (wide) {
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+      for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<float4*>(&red[warp][4 * lane + 32 * e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+      __syncthreads();
+      if (threadIdx.x < D / 2) {
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const float2 y = *reinterpret_cast<const float2*>(&red[i][2 * threadIdx.x]);
+          sum.x += y.x;
+          sum.y += y.y;
+        }
+        *reinterpret_cast<uint32_t*>(dst + 2 * threadIdx.x) = pack_bf16(sum.x * inv, sum.y * inv);
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<uint2*>(dst + 4 * lane + 32 * e) =
+            make_uint2(pack_bf16(acc[e] * inv, acc[e + 1] * inv), pack_bf16(acc[e + 2] * inv, acc[e + 3] * inv));
+    }
   }
 }
 
@@ -1437,6 +1484,19 @@ bool encode_rows(CUtensorMap* map, const void* pool, bool int8, int Hkv, int d, 
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries as [column block][token][head][64]: a box holds a group's heads of
+// `toks` tokens; tokens past the last read as zeros.
+bool encode_query(CUtensorMap* map, const uint16_t* q, int64_t q_stride, int n_tok, int Hq, int G, int d, int toks) {
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(n_tok),
+                              static_cast<cuuint64_t>(d / 64)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(q_stride) * 2, 128};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(toks), 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(q), dims, strides, box, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Layout {  // workspace
   int max_split, part_rows;
   size_t item, ml, o, total;
@@ -1444,7 +1504,7 @@ struct Layout {  // workspace
 
 // Rows of a query tile that can hold a token: the tile's tokens, or all there are.
 int tile_rows(int n_tok, int G, int ctas) {
-  const int tpt = ctas * kRows / G;
+  const int tpt = ctas * (kRows / G);
   return (n_tok < tpt ? n_tok : tpt) * G;
 }
 
@@ -1460,7 +1520,7 @@ Layout layout(int n_tok, int G, int d, int ctas, int sms) {
 }
 
 template <int D, int CTAS, bool INT8>
-int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int smem, int sms, cudaStream_t st) {
+int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, int smem, int sms, cudaStream_t st) {
   static std::atomic<int> configured[kMaxDevices];
   auto kernel = paged_kernel<D, CTAS, INT8>;
   if (smem_limit_once(configured, kernel, kMaxSmem) != SKV_OK) return SKV_ECUDA;
@@ -1476,7 +1536,7 @@ int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, km, vm, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, km, vm, qm, a) != cudaSuccess) {
     cudaGetLastError();
     return SKV_ECUDA;
   }
@@ -1498,9 +1558,9 @@ int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int
 }
 
 template <int D, int CTAS>
-int launch_kind(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, bool int8, int smem, int sms,
+int launch_kind(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, bool int8, int smem, int sms,
                 cudaStream_t st) {
-  return int8 ? launch<D, CTAS, true>(a, km, vm, smem, sms, st) : launch<D, CTAS, false>(a, km, vm, smem, sms, st);
+  return int8 ? launch<D, CTAS, true>(a, km, vm, qm, smem, sms, st) : launch<D, CTAS, false>(a, km, vm, qm, smem, sms, st);
 }
 
 // CTA pairs from about two query tiles of rows per request on.
@@ -1542,7 +1602,7 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
     return SKV_EINVAL;
   if (!(softmax_scale > 0.f) || softmax_scale > 3.0e38f) return SKV_EINVAL;
   // 32-bit positions, tile coordinates and work-list counts
-  if (n_pages * page > INT32_MAX - 1024 || n_pool_rows > (static_cast<int64_t>(1) << 33)) return SKV_EINVAL;
+  if (n_pages * page > INT32_MAX - 1024 || static_cast<int64_t>(n_tok) * Hq > INT32_MAX || n_pool_rows > (static_cast<int64_t>(1) << 33)) return SKV_EINVAL;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < skv_paged_attend_workspace_size(B, n_tok, Hq, Hkv, d))
     return SKV_ENOMEM;
@@ -1550,16 +1610,15 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
   if (sms <= 1 || !encode_fn()) return SKV_ECUDA;
   const int G = Hq / Hkv;
   const int ctas = ctas_for(B, n_tok, G, !q_start);
-  const int stage = 64 * d * 2;
+  const int stage = keys_per_tile(d, ctas) / ctas * d * 2;
 
   PagedArgs a{};
   a.B = B;
   a.n_tok = n_tok;
   a.Hkv = Hkv;
   a.G = G;
-  a.tpt = ctas * kRows / G;
-  a.q = q;
-  a.q_stride = q_stride;
+  a.tpc = kRows / G;
+  a.tpt = ctas * a.tpc;
   a.v_pool = int8 ? nullptr : static_cast<const uint16_t*>(v_pool);
   a.k_scale = reinterpret_cast<const __half*>(k_scale);
   a.v_scale = reinterpret_cast<const __half*>(v_scale);
@@ -1591,36 +1650,40 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
   a.ws_o = reinterpret_cast<float*>(ws + w.o);
 
   // Shared memory: the query rows that can hold a token (the products read
-  // 128 rows from there on; what they read past these is never used), then as
-  // many stages as fit.
-  const int q_rows = q_start ? tile_rows(n_tok, G, ctas) : G;
-  a.q_bytes = ((q_rows < kRows ? q_rows : kRows) + 7) / 8 * 8 * d * 2;
+  // 128 rows of each column block; what they read past these is never used),
+  // then as many stages as fit.
+  const int q_toks = !q_start ? 1 : n_tok < a.tpc ? n_tok : a.tpc;  // per CTA
+  a.q_box = q_toks * G * 128;
+  a.thin = int8 && ctas == 1 && q_toks * G <= 32;
+  a.q_sub = ctas == 2 ? kRows * 128 : (a.q_box + 1023) / 1024 * 1024;
+  a.q_bytes = a.q_sub * (d / 64);
   const int aux = static_cast<int>(sizeof(Aux)) + (int8 ? static_cast<int>(sizeof(Aux8)) : 0);
-  const int room = kMaxSmem - aux - a.q_bytes;
+  const int room = kMaxSmem - kOutBytes - aux - a.q_bytes;
   if (int8) {
     a.stages = ctas == 2 ? 3 : 4;
-    if (d == 128) a.stages *= 2;
+    if (d == 128 && ctas == 2) a.stages *= 2;
     a.staging = (room - a.stages * stage) / (stage / 2);
     if (a.staging > kMaxStaging) a.staging = kMaxStaging;
   } else {
     a.stages = room / stage;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
   }
-  const int smem = a.q_bytes + a.stages * stage + a.staging * (stage / 2) + aux;
+  const int smem = a.q_bytes + a.stages * stage + a.staging * (stage / 2) + kOutBytes + aux;
 
-  CUtensorMap km, vm;
+  CUtensorMap km, vm, qm;
   const int block = int8 ? 128 : 64;                         // columns of a 128-byte block
   const int vcols = d / ctas, vblock = vcols < block ? vcols : block;
   if (!encode_rows(&km, k_pool, int8, Hkv, d, n_pool_rows, block, d / block, a.rb) ||
-      !encode_rows(&vm, v_pool, int8, Hkv, d, n_pool_rows, vblock, vcols / vblock, a.rb))
+      !encode_rows(&vm, v_pool, int8, Hkv, d, n_pool_rows, vblock, vcols / vblock, a.rb) ||
+      !encode_query(&qm, q, q_stride, n_tok, Hq, G, d, q_toks))
     return SKV_ECUDA;
   cudaStream_t st = as_stream(stream);
   int e;
   if (d == 128)
-    e = ctas == 2 ? launch_kind<128, 2>(a, km, vm, int8, smem, sms, st)
-                  : launch_kind<128, 1>(a, km, vm, int8, smem, sms, st);
+    e = ctas == 2 ? launch_kind<128, 2>(a, km, vm, qm, int8, smem, sms, st)
+                  : launch_kind<128, 1>(a, km, vm, qm, int8, smem, sms, st);
   else
-    e = ctas == 2 ? launch_kind<256, 2>(a, km, vm, int8, smem, sms, st)
-                  : launch_kind<256, 1>(a, km, vm, int8, smem, sms, st);
+    e = ctas == 2 ? launch_kind<256, 2>(a, km, vm, qm, int8, smem, sms, st)
+                  : launch_kind<256, 1>(a, km, vm, qm, int8, smem, sms, st);
   return e;
 }
