@@ -457,15 +457,29 @@ def prefill_attend(q, k_src, v_src, n_tokens, k_stage, v_stage, idx, count, soft
 
 
 # ---- dense layers: projections to rows, new tokens over a paged cache ---------------
+# These two run once per layer and step on small tensors too, so they pass plain
+# addresses (ctypes converts an int or None as fast as it can) and the handle of
+# the current stream.
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    if stream is None:  # as torch.cuda.current_stream().cuda_stream, without making the object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
 
 def _heads(t):
     """(heads, d, token stride) of a [n][heads][d] tensor whose tokens' heads are consecutive."""
     if t is None:
         return 0, 0, 0
     n, H, d = t.shape
-    if (H > 1 and t.stride(1) != d) or (d > 1 and t.stride(2) != 1):
+    s = t.stride()
+    if (H > 1 and s[1] != d) or (d > 1 and s[2] != 1):
         raise ValueError("a token's heads must be consecutive")
-    return H, d, t.stride(0) if n > 1 else H * d
+    return H, d, s[0] if n > 1 else H * d
 
 
 def norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pool, v_pool, q_weight=None, k_weight=None, eps=1e-6,
@@ -474,24 +488,25 @@ def norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pool, v_pool, q_weig
     """q bf16 [n][Hq][d], k, v bf16 [n][Hkv][d] (views with any token stride; each may be None): q and k normed per
     head (weights fp32 [d] or None) and rotated over 2 * len(inv_freq) dims by positions int32 [n]; q -> q_out,
     k and v -> rows out_rows (int64 [n], negative: none; None: row i) of the pools [rows][Hkv][d]."""
-    some = next(t for t in (q, k, v) if t is not None)
-    n, d = some.shape[0], some.shape[2]
-    Hq, _, qs = _heads(q)
-    kh, _, ks = _heads(k)
-    vh, _, vs = _heads(v)
-    if any(t is not None and (t.shape[0] != n or t.shape[2] != d) for t in (q, k, v)) or (kh and vh and kh != vh):
+    some = q if q is not None else k if k is not None else v
+    n, _, d = some.shape
+    Hq, qd, qs = _heads(q)
+    kh, kd, ks = _heads(k)
+    vh, vd, vs = _heads(v)
+    if (k is not None and (k.shape[0] != n or kd != d)) or (v is not None and (v.shape[0] != n or vd != d)) or \
+            (kh and vh and kh != vh):
         raise ValueError("q, k and v differ in tokens, head dimension or KV heads")
     pool = k_pool if k_pool is not None else v_pool
-    _check("skv_norm_rope_append", _load().skv_norm_rope_append(
-        n, Hq, kh or vh, d, 0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), _ptr(q), qs, _ptr(k),
-        ks, _ptr(v), vs, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), _ptr(q_out),
-        kv_kind, _ptr(out_rows), 0 if pool is None else pool.shape[0], _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
-        _ptr(v_scale), _ptr(status), _stream(stream)))
+    _check("skv_norm_rope_append", (_lib or _load()).skv_norm_rope_append(
+        n, Hq, kh or vh, d, 0 if inv_freq is None else 2 * inv_freq.shape[0], 1 if interleaved else 0, _at(q), qs,
+        _at(k), ks, _at(v), vs, _at(q_weight), _at(k_weight), eps, _at(positions), _at(inv_freq), _at(q_out), kv_kind,
+        _at(out_rows), 0 if pool is None else pool.shape[0], _at(k_pool), _at(v_pool), _at(k_scale), _at(v_scale),
+        _at(status), _raw_stream(stream)))
     return q_out
 
 
 def paged_attend_workspace_size(B, n_tok, Hq, Hkv, d) -> int:
-    return int(_load().skv_paged_attend_workspace_size(B, n_tok, Hq, Hkv, d))
+    return (_lib or _load()).skv_paged_attend_workspace_size(B, n_tok, Hq, Hkv, d)
 
 
 def paged_attend(kv_kind, q, k_pool, v_pool, block_table, page, lengths, softmax_scale, out, workspace, q_start=None,
@@ -500,11 +515,12 @@ def paged_attend(kv_kind, q, k_pool, v_pool, block_table, page, lengths, softmax
     q_start[b+1] (None: one each); pools [rows][Hkv][d]; block_table int32 [B][n_pages] -> out bf16 [n][Hq][d]."""
     Hq, d, qs = _heads(q)
     B, n_pages = block_table.shape
-    _check("skv_paged_attend", _load().skv_paged_attend(
-        kv_kind, B, q.shape[0], Hq, k_pool.shape[1], d, _ptr(q), qs, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
-        _ptr(v_scale), k_pool.shape[0], page, _ptr(block_table), n_pages, _ptr(q_start), _ptr(lengths), S, W,
-        float(softmax_scale), _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
-        _stream(stream)))
+    rows, Hkv, _ = k_pool.shape
+    _check("skv_paged_attend", (_lib or _load()).skv_paged_attend(
+        kv_kind, B, q.shape[0], Hq, Hkv, d, q.data_ptr(), qs, k_pool.data_ptr(), v_pool.data_ptr(), _at(k_scale),
+        _at(v_scale), rows, page, block_table.data_ptr(), n_pages, _at(q_start), lengths.data_ptr(), S, W,
+        softmax_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _at(status), _raw_stream(stream)))
     return out
 
 

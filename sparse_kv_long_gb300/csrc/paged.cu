@@ -498,9 +498,9 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CTAS == 1 ? 0u : tc::cluster_rank();
   // Softmax warps and widening warps: with at most 32 rows a tile, as single
-  // tokens have, warps 4 and 8 do the softmax and 5, 6, 9, 10 join the widening
-  // (7 and 11 rest).  One row of work for six warps, two for four: a 64-key
-  // tile took 3.3K clocks, all in the widening.
+  // tokens have, warps 4 and 8 do the softmax and 5, 6, 7, 11 join the widening (9 and
+  // 10 rest: at most two widen per scheduler that has other work).  64 ragged
+  // requests took 190 us with four widening warps, 166 with these eight.
   const bool thin = INT8 && CTAS == 1 && a.thin;
   const uint32_t n_soft = thin ? 2 : 8, n_wide = thin ? 8 : 4;
   const bool softer = warp >= 4 && warp < 12 && (!thin || (warp & 3) == 0);
@@ -1277,9 +1277,9 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       __syncwarp();
       tc::tmem_wait_ld();
     }
-  } else if (INT8 && (warp >= 12 || (warp & 3) != 3)) {
-    // ---------------- int8 -> bf16 (warps 12-15, and where they are free 5, 6, 9, 10) ----------------
-    const int ct = warp >= 12 ? tid - 384 : 128 + 32 * ((warp & 3) - 1 + (warp >= 8 ? 2 : 0)) + lane;
+  } else if (INT8 && (warp >= 12 || warp < 8 || warp == 11)) {
+    // ---------------- int8 -> bf16 (warps 12-15, and where they are free 5, 6, 7, 11) ----------------
+    const int ct = warp >= 12 ? tid - 384 : 128 + 32 * (warp == 11 ? 3 : warp - 5) + lane;
     // Thread -> 16 codes of one row, a few times a stage: ct % 8 is the row
     // of its 8-row group, so eight lanes read eight rows' swizzled pieces
     // (distinct banks) and write them the same way.  Piece `pce` of a row is
