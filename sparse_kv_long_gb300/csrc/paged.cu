@@ -52,6 +52,7 @@ constexpr int kScaleRing = 4;      // tiles whose int8 scales are kept
 constexpr int kCand = 64;          // split candidates
 constexpr float kLazy = 8.f;       // log2 units a maximum may grow before O is rescaled
 constexpr int kSplitPerUnit = 8;   // pieces that write partials, per CTA or pair (at most 4 per SM)
+constexpr uint32_t kGone = 0x7fc0dead;  // a NaN that no arithmetic gives
 constexpr uint32_t kSCol = 256;    // tensor memory: O in [0, D), S/P buffers from here
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kOutBytes = 8 * 2048;
@@ -107,7 +108,6 @@ struct alignas(16) Aux {
   // Two barriers where a waiter may skip tiles: when S(t + 1) is there, O of
   // t - 1 is done and of t may not be, and one parity could not tell them apart.
   uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_free, o_free, mma_idle;
-  uint64_t x_full[2][4];  // per 32 rows: both softmax warps' values are in `x`
   uint64_t pc_full[kPieces], pc_empty[kPieces];
   Piece pc[kPieces];
   uint32_t tile_bad[kTileInfo];  // bit i: rows [8 i, 8 i + 8) of the tile have no page
@@ -124,9 +124,10 @@ struct alignas(16) Aux {
 struct alignas(16) Aux8 {  // int8 rows only
   uint64_t st_full[kMaxStaging], st_empty[kMaxStaging];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
-  alignas(16) float ks[kScaleRing][kRows], vs[kScaleRing][kRows];
+  alignas(16) float ks[kScaleRing][kRows], vs[kScaleRing][kRows], rs[kScaleRing][kRows];  // rs: 1 / vs
 };
 
+static_assert(kMaxStages == kMaxStaging && kScaleRing <= kPieces, "one thread sets up a barrier of each");
 static_assert(sizeof(Aux) <= 3072, "room beside the query tile, the stages and the output rows");
 
 // ---- work list -------------------------------------------------------------------
@@ -508,50 +509,36 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   volatile int* abort = &ax->abort;
 
   allow_dependent_launch();  // the merge may be scheduled as SMs come free; it waits for this grid
-  if (tid == 0) {
-#pragma unroll 1
-    for (int s = 0; s < kMaxStages; s++) {
-      // int8: the widening warps of both CTAs; bf16: the copies, and on the leader a note from the peer's
-      tc::bar_init(&ax->kv_full[s], INT8 ? n_wide * CTAS : (rank == 0 ? CTAS : 1));
-      tc::bar_init(&ax->kv_empty[s], 1);
+  if (tid < kMaxStages) {  // a thread per barrier: one after the other they took a microsecond
+    // int8: the widening warps of both CTAs; bf16: the copies, and on the leader a note from the peer's
+    tc::bar_init(&ax->kv_full[tid], INT8 ? n_wide * CTAS : (rank == 0 ? CTAS : 1));
+    tc::bar_init(&ax->kv_empty[tid], 1);
+    if (INT8) {
+      tc::bar_init(&a8->st_full[tid], 1);
+      tc::bar_init(&a8->st_empty[tid], n_wide);
     }
-    for (int s = 0; s < 2; s++) {
-      tc::bar_init(&ax->s_full[s], 1);
-      tc::bar_init(&ax->p_full[s], n_soft * CTAS);
-      tc::bar_init(&ax->pv_done[s], 1);
+  } else if (tid >= 32 && tid < 34) {
+    tc::bar_init(&ax->s_full[tid - 32], 1);
+    tc::bar_init(&ax->p_full[tid - 32], n_soft * CTAS);
+    tc::bar_init(&ax->pv_done[tid - 32], 1);
+  } else if (tid >= 64 && tid < 64 + kPieces) {
+    tc::bar_init(&ax->pc_full[tid - 64], 1);
+    tc::bar_init(&ax->pc_empty[tid - 64], 1 + n_soft + (INT8 ? 2 + n_wide : 0));  // products, softmax, scales, widening
+    if (INT8 && tid - 64 < kScaleRing) {
+      tc::bar_init(&a8->sc_full[tid - 64], 1);
+      tc::bar_init(&a8->sc_empty[tid - 64], n_soft);
     }
-#pragma unroll 1
-    for (int s = 0; s < 4; s++) {
-      tc::bar_init(&ax->x_full[0][s], 2);
-      tc::bar_init(&ax->x_full[1][s], 2);
-    }
+  } else if (tid == 96) {
     tc::bar_init(&ax->q_full, rank == 0 ? CTAS : 1);  // the copy, and on the leader a note from the peer's
     tc::bar_init(&ax->q_free, 1);
     tc::bar_init(&ax->o_free, n_soft * CTAS);
     tc::bar_init(&ax->mma_idle, 1);
-#pragma unroll 1
-    for (int s = 0; s < kPieces; s++) {
-      tc::bar_init(&ax->pc_full[s], 1);
-      tc::bar_init(&ax->pc_empty[s], 1 + n_soft + (INT8 ? 2 + n_wide : 0));  // products, softmax, scales, widening
-    }
-    if (INT8) {
-#pragma unroll 1
-      for (int s = 0; s < kMaxStaging; s++) {
-        tc::bar_init(&a8->st_full[s], 1);
-        tc::bar_init(&a8->st_empty[s], n_wide);
-      }
-#pragma unroll 1
-      for (int s = 0; s < kScaleRing; s++) {
-        tc::bar_init(&a8->sc_full[s], 1);
-        tc::bar_init(&a8->sc_empty[s], n_soft);
-      }
-    }
     ax->abort = (tc::smem_addr(smem_raw) & 1023u) != 0;  // every wait would give up at once
     ax->dirty = 0;
     ax->nmax = 0;
     ax->items = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid < 128) asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   if (warp == 1) {
     if (CTAS == 1) {
       tc::tmem_alloc<512>(&ax->tmem_base);
@@ -610,8 +597,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       const int k = rest ? i - nk + 1 : i + 1;
       const int c = (nmax + k - 1) / k;
       const float rc = 1.f / c;
-      int P = 0, S = 0;
-      float u = 0.f, main_u = 0.f;
+      int P = 0, S = 0, u = 0, main_u = 0;  // pieces, those of cut items, tiles of the items looked at, of the others
 #pragma unroll 1
       for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int2 r = b0 + lane < a.B ? req[b0 + lane] : make_int2(0, 0);
@@ -630,20 +616,17 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         const int ps = nmax < (1 << 15) ? max(1, static_cast<int>((r.y + c - 0.5f) * rc)) : pieces_of(r.y, c);
         P += n * ps;
         S += ps > 1 ? n * ps : 0;
-        u += static_cast<float>(n) * r.y;
-        main_u += static_cast<float>(all - n) * r.y;
+        u += n * r.y;
+        main_u += (all - n) * r.y;
       }
       P = __reduce_add_sync(0xffffffffu, P);
       S = __reduce_add_sync(0xffffffffu, S);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        u += __shfl_xor_sync(0xffffffffu, u, o);
-        if (rest) main_u += __shfl_xor_sync(0xffffffffu, main_u, o);
-      }
+      u = __reduce_add_sync(0xffffffffu, u);
+      if (rest) main_u = __reduce_add_sync(0xffffffffu, main_u);
       if (S <= a.max_split) {
-        float cost = rest ? main_u / n_units + x1 / n_units * kOvh : 0.f;
+        float cost = rest ? static_cast<float>(main_u) / n_units + x1 / n_units * kOvh : 0.f;
         if (P > 0)
-          cost += (ceilf(static_cast<float>(P) / n_units) - 1.f) * (u / P + kOvh) + c + kOvh +
+          cost += static_cast<float>((P - 1) / n_units) * (static_cast<float>(u) / P + kOvh) + c + kOvh +
                   (S > 0 ? kJoin + S * a.part_cost : 0.f);
         if (cost < best) {
           best = cost;
@@ -980,7 +963,11 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
 #pragma unroll
           for (int e = 0; e < KT / 32; e++) {
             a8->ks[s][lane + 32 * e] = ks[e];
-            a8->vs[s][lane + 32 * e] = vs[e];
+            // A zero scale would leave the sum without the row's weight: 2^-100 keeps
+            // it, and the values at zero.  A scale that is not finite has no reciprocal.
+            const float v = vs[e] == 0.f ? 7.888609e-31f : vs[e];
+            a8->vs[s][lane + 32 * e] = v;
+            a8->rs[s][lane + 32 * e] = fabsf(v) <= 65504.f ? 1.f / v : 0.f;
           }
           __syncwarp();
           if (lane == 0) tc::bar_arrive(&a8->sc_full[s]);
@@ -1003,15 +990,15 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     uint32_t g = 0, fills = 0, xc = 0;  // tiles, ring fills, exchanges so far
     bool ok = true;
 
-    // This thread's value and its partner's (the other group's, same row).
-    auto exchange = [&](float v, float& other) -> bool {
+    // This thread's value and its partner's (the other group's, same row), over
+    // a named barrier of the two warps (an mbarrier took 100 clocks more).  Such
+    // a barrier has no bound of its own: each warp, done or given up, goes on
+    // exchanging kGone until it gets kGone back, so neither is left waiting.
+    auto exchange = [&](float v, float& other) {
       ax->x[xc & 1][wg][r] = v;
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&ax->x_full[xc & 1][quad]);
-      if (!wait_all(&ax->x_full[xc & 1][quad], (xc >> 1) & 1, abort)) return false;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
       other = ax->x[xc & 1][wg ^ 1][r];
       xc++;
-      return true;
     };
 
     auto get = [&](int k, Piece& pc) -> bool {  // descriptor k
@@ -1038,16 +1025,16 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       for (int j = 0; j < pc.n; j++) {
         const uint32_t t = g + j;
         const int t0 = tile_of(pc, j) * KT;
-        if (!(ok = wait_all(&ax->s_full[t & 1], (t >> 1) & 1, abort))) break;
-        tc::tc_fence_after();
-        const uint32_t bad = ax->tile_bad[t % kTileInfo];
-        // every row of the tile sees every key unless one of these holds
-        const bool masked = t0 + KT - 1 > pc.pos0 || bad != 0 ||
-                            (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S);
+        // every row of the tile sees every key unless one of these holds, or a page is missing
+        const bool edge = t0 + KT - 1 > pc.pos0 || (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S);
         constexpr int HC = KT / 2;  // this group's keys of the tile
         const uint32_t scol = tm + lane_base + kSCol + (t & 1) * 128 + wg * HC;
         const uint32_t sc = t % kScaleRing;
         if (INT8 && !(ok = wait_all(&a8->sc_full[sc], (t / kScaleRing) & 1, abort))) break;
+        if (!(ok = wait_all(&ax->s_full[t & 1], (t >> 1) & 1, abort))) break;
+        tc::tc_fence_after();
+        const uint32_t bad = ax->tile_bad[t % kTileInfo];
+        const bool masked = edge || bad != 0;
         if (warp_live) {
           uint32_t s[HC / 32][32];
 #pragma unroll
@@ -1095,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
           const float f = INT8 ? 1.f : a.scale_log2;
           float mc = fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]) * f, mo;
           if (!live) mc = -INFINITY;  // a row without a query holds anything: it must not call for a rescale
-          if (!(ok = exchange(mc, mo))) break;
+          exchange(mc, mo);
           mc = fmaxf(mc, mo);
           const float m_new = mc > m_ref + kLazy || m_ref == -INFINITY ? fmaxf(mc, m_ref) : m_ref;
           if (__any_sync(0xffffffffu, m_new != m_ref)) {
@@ -1132,10 +1119,11 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
                 e[z].x = tc::ex2_approx(e[z].x);
                 e[z].y = tc::ex2_approx(e[z].y);
               }
+              // The sum takes the weights as they are rounded, so that the weights
+              // applied add up to one: with few keys their errors cancel.
               if (INT8) {
-                ls[0] = f2_add(ls[0], f2(e[0].x, e[0].y));
-                ls[1] = f2_add(ls[1], f2(e[1].x, e[1].y));
                 const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&a8->vs[sc][wg * HC + 2 * i]);
+                const ulonglong2 rv = *reinterpret_cast<const ulonglong2*>(&a8->rs[sc][wg * HC + 2 * i]);
                 float2 w0 = f2_out(f2_mul(f2(e[0].x, e[0].y), F2{v.x}));
                 float2 w1 = f2_out(f2_mul(f2(e[1].x, e[1].y), F2{v.y}));
                 if (masked) {  // a scale that this row does not see may be anything
@@ -1143,9 +1131,12 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
                   w0 = make_float2(m & 1u ? w0.x : 0.f, m & 2u ? w0.y : 0.f);
                   w1 = make_float2(m & 4u ? w1.x : 0.f, m & 8u ? w1.y : 0.f);
                 }
-                pk[y] = pack_bf16(w0.x, w0.y);
-                pk[y + 1] = pack_bf16(w1.x, w1.y);
-              } else {  // the sum takes the weights as they are rounded
+                const uint32_t p0 = pack_bf16(w0.x, w0.y), p1 = pack_bf16(w1.x, w1.y);
+                pk[y] = p0;
+                pk[y + 1] = p1;
+                ls[0] = f2_fma(f2(__uint_as_float(p0 << 16), __uint_as_float(p0 & 0xffff0000u)), F2{rv.x}, ls[0]);
+                ls[1] = f2_fma(f2(__uint_as_float(p1 << 16), __uint_as_float(p1 & 0xffff0000u)), F2{rv.y}, ls[1]);
+              } else {
 #pragma unroll
                 for (int z = 0; z < 2; z++) {
                   const uint32_t w = pack_bf16(e[z].x, e[z].y);
@@ -1215,7 +1206,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       if (pc.n > 0) {
         if (warp_live) {
           float lo;
-          if (!(ok = exchange(l, lo))) break;
+          exchange(l, lo);
           l += lo;  // a sum of two: the same in both
         }
         if (!(ok = wait_all(&ax->pv_done[t_last & 1], (t_last >> 1) & 1, abort))) break;
@@ -1277,6 +1268,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       __syncwarp();
       tc::tmem_wait_ld();
     }
+    for (float other = 0.f; __float_as_uint(other) != kGone;) exchange(__uint_as_float(kGone), other);
   } else if (INT8 && (warp >= 12 || warp < 8 || warp == 11)) {
     // ---------------- int8 -> bf16 (warps 12-15, and where they are free 5, 6, 7, 11) ----------------
     const int ct = warp >= 12 ? tid - 384 : 128 + 32 * (warp == 11 ? 3 : warp - 5) + lane;
