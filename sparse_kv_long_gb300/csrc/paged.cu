@@ -97,7 +97,7 @@ struct PagedArgs {
   int part_rows;              // rows of a partial slot
   int max_split;              // partial slots
   float part_cost;            // tiles' worth of writing and joining a partial
-  int* ws_head;               // [0]: split items of this call
+  int* ws_head;               // split items of this call, the most rows one has
   int4* ws_item;              // per split item: (tok0, rows, h, first slot), (pieces, 0, 0, 0)
   float2* ws_ml;              // [slot][row]: running max (log2 units), row sum
   float* ws_o;                // [slot][row][D]
@@ -553,6 +553,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   tc::tc_fence_after();
 
   int split_c, split_from;
+  Req mine{0, 0, 0, 0, 0};  // warp 0: the first 32 requests
   // ---- plan: tiles per piece -----------------------------------------------------
   // Candidate k cuts the longest item into k pieces of c = ceil(nmax / k)
   // tiles and every other one into ceil(tiles / c): all items, or those past
@@ -569,6 +570,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
 #pragma unroll 1
     for (int b = tid; b < a.B; b += THREADS) {
       const Req r = request<KT>(a, b, unit == 0 && rank == 0);
+      if (b < 32) mine = r;
       req[b] = make_int2(r.nqt, r.ntmax);
       nmax = max(nmax, r.ntmax);
       items += r.nqt;
@@ -636,12 +638,17 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     }
     if (lane == 0) ax->cand[warp] = make_float2(best, __int_as_float(pick));
     __syncthreads();
-#pragma unroll 1
-    for (int w = 0; w < NW; w++) {
-      const float2 o = ax->cand[w];
-      const int oi = __float_as_int(o.y);
-      if (w == 0 || o.x < best || (o.x == best && oi < pick)) {
-        best = o.x;
+    {
+      const float2 o = ax->cand[min(lane, NW - 1)];
+      best = o.x;
+      pick = __float_as_int(o.y);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float ob = __shfl_xor_sync(0xffffffffu, best, o);
+      const int oi = __shfl_xor_sync(0xffffffffu, pick, o);
+      if (ob < best || (ob == best && oi < pick)) {
+        best = ob;
         pick = oi;
       }
     }
@@ -665,13 +672,13 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     // Request b's pieces: first those of its items that are kept whole, then
     // the cut items', each item's pieces one after the other.
     int b32 = 0, base = 0, ibase = 0, sbase = 0, seen = 0;  // first request of the window; pieces, split items, slots, items before it
-    Req r = request<KT>(a, lane, false);
+    Req r = mine;
     int pp, ii, ss, tt, ns, nw;  // inclusive sums over the window's requests; pieces per cut item, items kept whole
     auto scan = [&]() {
       ns = pieces_of(r.ntmax, c);
       const int items = r.nqt * a.Hkv;
       tt = items;
-#pragma unroll 1
+#pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, tt, o);
         if (lane >= o) tt += x;
@@ -681,7 +688,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       pp = nw + (items - nw) * ns;
       ii = items - nw;
       ss = ii * ns;
-#pragma unroll 1
+#pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, pp, o), y = __shfl_up_sync(0xffffffffu, ii, o),
                   z = __shfl_up_sync(0xffffffffu, ss, o);
@@ -830,7 +837,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     }
     // split items of this call, for the merge
     if (unit == 0 && rank == 0) {
-      int cut = 0, before = 0;
+      int cut = 0, before = 0, rows = 0;
 #pragma unroll 1
       for (int b0 = 0; b0 < a.B; b0 += 32) {
         const Req x = request<KT>(a, b0 + lane, false);
@@ -841,11 +848,19 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
           const int y = __shfl_up_sync(full, sum, o);
           if (lane >= o) sum += y;
         }
-        if (pieces_of(x.ntmax, c) > 1) cut += items - min(items, max(0, whole - (before + sum - items)));
+        if (pieces_of(x.ntmax, c) > 1) {
+          const int n = items - min(items, max(0, whole - (before + sum - items)));
+          cut += n;
+          if (n > 0) rows = max(rows, min(a.tpt, x.nq) * a.G);
+        }
         before += __shfl_sync(full, sum, 31);
       }
       cut = __reduce_add_sync(full, cut);
-      if (lane == 0) a.ws_head[0] = cut;
+      rows = __reduce_max_sync(full, rows);
+      if (lane == 0) {
+        a.ws_head[0] = cut;
+        a.ws_head[1] = rows;
+      }
     }
   } else if (warp == 1) {
     // ---------------- products (one thread of the leader) ----------------
@@ -1222,6 +1237,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         unsigned char* buf = sOut + (warp - 4) * 2048;
         const int id = !live ? -1 : whole ? static_cast<int>(tok * (a.Hkv * a.G)) + pc.h * a.G + head_r : static_cast<int>(prow);
         char* base = whole ? reinterpret_cast<char*>(a.out) : reinterpret_cast<char*>(a.ws_o);
+        const bool few = __popc(__ballot_sync(0xffffffffu, live)) <= 8;  // each lane writes its own row
 #pragma unroll 1
         for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
           uint32_t o[32];
@@ -1249,7 +1265,16 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
             for (int i = 0; i < 16; i++)
               w[i] = whole ? pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv)
                            : y ? o[16 + i] : o[i];
-            put_rows(buf, lane, w, id, base + (whole ? 2 * c0 : 4 * (c0 + 16 * y)), whole ? 2 * D : 4 * D);
+            char* to = base + (whole ? 2 * c0 : 4 * (c0 + 16 * y));
+            const int pitch = whole ? 2 * D : 4 * D;
+            if (!few) {
+              put_rows(buf, lane, w, id, to, pitch);
+            } else if (live) {
+#pragma unroll
+              for (int i = 0; i < 4; i++)
+                *reinterpret_cast<uint4*>(to + static_cast<int64_t>(id) * pitch + 16 * i) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
           }
         }
         if (!whole && live && wg == 0) a.ws_ml[prow] = make_float2(m_ref, l);
@@ -1367,13 +1392,13 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head
   __shared__ float red[8][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();  // launched early: the partials are complete from here on
-  const int tasks = head[0] * part_rows;
+  const int rows = head[1], tasks = head[0] * rows;
   const bool wide = tasks <= 2 * static_cast<int>(gridDim.x);  // a block per row
   const int step = wide ? gridDim.x : gridDim.x * 8, first = wide ? blockIdx.x : blockIdx.x * 8 + warp;
   const int s0 = wide ? warp : 0, ds = wide ? 8 : 1;
 #pragma unroll 1
   for (int w = first; w < tasks; w += step) {
-    const int it = w / part_rows, row = w - it * part_rows;
+    const int it = w / rows, row = w - it * rows;
     const int4 x = item[2 * it];
     const int n = item[2 * it + 1].x;
     if (row >= x.y) continue;  // the same for the whole block where it takes a row
