@@ -49,9 +49,11 @@ constexpr int kMaxStaging = 12;    // int8 staging ring
 constexpr int kPieces = 4;         // piece descriptors in flight
 constexpr int kTileInfo = 16;      // tiles whose page validity is kept (more than the ring holds)
 constexpr int kScaleRing = 4;      // tiles whose int8 scales are kept
-constexpr int kCand = 64;          // split candidates
+constexpr int kCand = 64;          // split candidates (pairs)
+constexpr int kItem = 3;           // tiles that filling and draining a piece's pipeline is worth (single CTAs)
+constexpr int kMinStretch = 4;     // tiles a CTA gets at least
 constexpr float kLazy = 8.f;       // log2 units a maximum may grow before O is rescaled
-constexpr int kSplitPerUnit = 8;   // pieces that write partials, per CTA or pair (at most 4 per SM)
+constexpr int kSplitPerPair = 8;   // pieces that write partials, per pair (single CTAs: two each)
 constexpr uint32_t kGone = 0x7fc0dead;  // a NaN that no arithmetic gives
 constexpr uint32_t kSCol = 256;    // tensor memory: O in [0, D), S/P buffers from here
 constexpr int kMaxSmem = 227 * 1024;
@@ -97,7 +99,7 @@ struct PagedArgs {
   int part_rows;              // rows of a partial slot
   int max_split;              // partial slots
   float part_cost;            // tiles' worth of writing and joining a partial
-  int* ws_head;               // split items of this call, the most rows one has
+  int* ws_head;               // listed split items of this call, the most rows one has, whether the list has gaps
   int4* ws_item;              // per split item: (tok0, rows, h, first slot), (pieces, 0, 0, 0)
   float2* ws_ml;              // [slot][row]: running max (log2 units), row sum
   float* ws_o;                // [slot][row][D]
@@ -552,18 +554,54 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   __syncthreads();
   tc::tc_fence_after();
 
-  int split_c, split_from;
-  Req mine{0, 0, 0, 0, 0};  // warp 0: the first 32 requests
-  // ---- plan: tiles per piece -----------------------------------------------------
-  // Candidate k cuts the longest item into k pieces of c = ceil(nmax / k)
-  // tiles and every other one into ceil(tiles / c): all items, or those past
-  // the last full round over the CTAs.  Its cost is the number of rounds times
+  // ---- plan ------------------------------------------------------------------------
+  // Single CTAs: the items' key tiles, each item preceded by kItem tiles' worth
+  // of filling and draining its pipeline, lie in one row and every CTA takes an
+  // equal stretch of it, whatever the requests' lengths (64 ragged requests: the
+  // busiest CTA had 2.2 times the idlest's work when whole pieces were dealt
+  // out).  An item's stretches are its pieces; a CTA has at most two that are
+  // not whole, its first and its last.  Fewer CTAs when a stretch would be
+  // shorter than kMinStretch.
+  //
+  // Pairs: queries of one request read the same keys, and those that run at the
+  // same time should be at the same place, so pieces are equal cuts of items
+  // instead.  Candidate k cuts the longest item into k pieces of c = ceil(nmax /
+  // k) tiles and every other one into ceil(tiles / c): all items, or those past
+  // the last full round over the pairs.  Its cost is the number of rounds times
   // a piece (the last at full length); a piece pays kOvh tiles for filling and
   // draining its pipeline, a split kJoin tiles once and part_cost per piece
   // for its partials.  Each warp weighs every NW-th candidate, a lane per
   // request; the batch waits in shared memory that the ring will take over.
-  {
-    constexpr float kOvh = 3.f, kJoin = CTAS == 1 ? 4.f : 3.f;
+  int split_c = 1, split_from = 0;
+  int total = 0, n_used = n_units;  // single CTAs: the row's length, the CTAs that share it
+  Req mine{0, 0, 0, 0, 0};          // warp 0: the first 32 requests
+  if (CTAS == 1) {
+    int sum = 0, rows = 0;
+#pragma unroll 1
+    for (int b = tid; b < a.B; b += THREADS) {
+      const Req r = request<KT>(a, b, unit == 0);
+      if (b < 32) mine = r;
+      sum += r.nqt * a.Hkv * (r.ntmax + kItem);
+      rows = max(rows, min(a.tpt, r.nq) * a.G);
+    }
+    if (warp * 32 < a.B) {
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      rows = __reduce_max_sync(0xffffffffu, rows);
+      if (lane == 0 && sum > 0) {
+        atomicAdd(&ax->items, sum);
+        atomicMax(&ax->nmax, rows);
+      }
+    }
+    __syncthreads();
+    total = ax->items;
+    n_used = min(n_units, max(1, total / kMinStretch));
+    if (tid == 0 && unit == 0) {
+      a.ws_head[0] = n_units;
+      a.ws_head[1] = ax->nmax;
+      a.ws_head[2] = 1;
+    }
+  } else {
+    constexpr float kOvh = 3.f, kJoin = 3.f;
     constexpr int NW = THREADS / 32;
     int2* req = reinterpret_cast<int2*>(sKV);  // (query tiles, key tiles of the longest)
     int nmax = 0, items = 0;
@@ -656,10 +694,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     split_from = pick >= nk && nk > 0 ? x1 : 0;
     const int k = pick >= nk && nk > 0 ? pick - nk + 1 : pick + 1;
     split_c = max(1, (nmax + k - 1) / k);
-    if (CTAS == 2)
-      tc::cluster_sync();  // also: the peer's barriers exist before any remote access
-    else
-      __syncthreads();
+    tc::cluster_sync();  // also: the peer's barriers exist before any remote access
   }
   const int c = split_c, whole = split_from;  // tiles per piece; items before this one are not cut
   if (tid == 0 && ax->tmem_base != 0) *abort = 1;
@@ -669,29 +704,34 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
 
   if (warp == 0) {
     // ---------------- pieces and copies ----------------
-    // Request b's pieces: first those of its items that are kept whole, then
-    // the cut items', each item's pieces one after the other.
+    // The requests are walked 32 at a time, a lane each.  Pairs: request b's
+    // pieces are first those of its items that are kept whole, then the cut
+    // items'.  Single CTAs: `pp` is the requests' length in the row.
     int b32 = 0, base = 0, ibase = 0, sbase = 0, seen = 0;  // first request of the window; pieces, split items, slots, items before it
     Req r = mine;
-    int pp, ii, ss, tt, ns, nw;  // inclusive sums over the window's requests; pieces per cut item, items kept whole
+    int pp, ii = 0, ss = 0, tt = 0, ns = 1, nw = 0;  // inclusive sums over the window's requests; pieces per cut item, items kept whole
     auto scan = [&]() {
-      ns = pieces_of(r.ntmax, c);
       const int items = r.nqt * a.Hkv;
-      tt = items;
+      if (CTAS == 1) {
+        pp = items * (r.ntmax + kItem);
+      } else {
+        ns = pieces_of(r.ntmax, c);
+        tt = items;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, tt, o);
-        if (lane >= o) tt += x;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, tt, o);
+          if (lane >= o) tt += x;
+        }
+        nw = min(items, max(0, whole - (seen + tt - items)));
+        if (ns == 1) nw = items;
+        pp = nw + (items - nw) * ns;
+        ii = items - nw;
+        ss = ii * ns;
       }
-      nw = min(items, max(0, whole - (seen + tt - items)));
-      if (ns == 1) nw = items;
-      pp = nw + (items - nw) * ns;
-      ii = items - nw;
-      ss = ii * ns;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, pp, o), y = __shfl_up_sync(0xffffffffu, ii, o),
-                  z = __shfl_up_sync(0xffffffffu, ss, o);
+        const int x = __shfl_up_sync(0xffffffffu, pp, o), y = CTAS == 1 ? 0 : __shfl_up_sync(0xffffffffu, ii, o),
+                  z = CTAS == 1 ? 0 : __shfl_up_sync(0xffffffffu, ss, o);
         if (lane >= o) {
           pp += x;
           ii += y;
@@ -700,6 +740,17 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       }
     };
     scan();
+    // single CTAs: this one's stretch, and the CTA that has a place of the row
+    int x = 0, x_end = 0;
+    bool listed = false;  // a split item begins here
+    if (CTAS == 1 && unit < n_used) {
+      x = static_cast<int>(static_cast<int64_t>(total) * unit / n_used);
+      x_end = static_cast<int>(static_cast<int64_t>(total) * (unit + 1) / n_used);
+    }
+    const int x_begin = x;
+    auto owner = [&](int at) {
+      return static_cast<int>((static_cast<int64_t>(at + 1) * n_used - 1) / total);
+    };
     const uint32_t full = 0xffffffffu;
     // boxes of a tile: this CTA copies boxes_k of them for K, all for V
     const int boxes_k = KR / a.rb, rb_log = 31 - __clz(a.rb);
@@ -714,59 +765,100 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     bool ok = true;
 #pragma unroll 1
     for (int k = 0; ok; k++) {
-      // every other round backwards: pieces come longest first, so this evens the CTAs' shares
-      const int id = k * n_units + ((k & 1) ? n_units - 1 - unit : unit);
-#pragma unroll 1
-      while (b32 < a.B && id >= base + __shfl_sync(full, pp, 31)) {
-        base += __shfl_sync(full, pp, 31);
-        ibase += __shfl_sync(full, ii, 31);
-        sbase += __shfl_sync(full, ss, 31);
-        seen += __shfl_sync(full, tt, 31);
-        b32 += 32;
-        r = request<KT>(a, b32 + lane, false);
-        scan();
-      }
       Piece pc;
-      pc.last = 0;
-      const bool any = b32 < a.B;
-      if (any) {
-        const int w = __ffs(__ballot_sync(full, id < base + pp)) - 1;
+      pc.last = 1;
+      pc.n = 0;
+      pc.toks = 0;
+      pc.slot = -1;
+      // every other round backwards: pieces come longest first, so this evens the pairs' shares
+      const int id = CTAS == 1 ? 0 : k * n_units + ((k & 1) ? n_units - 1 - unit : unit);
+#pragma unroll 1
+      while (pc.last) {
+        const int at = CTAS == 1 ? x : id;
+        if (CTAS == 1 && x >= x_end) break;
+#pragma unroll 1
+        while (b32 < a.B && at >= base + __shfl_sync(full, pp, 31)) {
+          base += __shfl_sync(full, pp, 31);
+          ibase += __shfl_sync(full, ii, 31);
+          sbase += __shfl_sync(full, ss, 31);
+          seen += __shfl_sync(full, tt, 31);
+          b32 += 32;
+          r = request<KT>(a, b32 + lane, false);
+          scan();
+        }
+        if (b32 >= a.B) break;
+        const int w = __ffs(__ballot_sync(full, at < base + pp)) - 1;
         Req q;
         q.start = __shfl_sync(full, r.start, w);
         q.nq = __shfl_sync(full, r.nq, w);
         q.T = __shfl_sync(full, r.T, w);
         q.nqt = __shfl_sync(full, r.nqt, w);
-        const int nsw = __shfl_sync(full, ns, w), kept = __shfl_sync(full, nw, w);
-        const int cut = q.nqt * a.Hkv - kept;
-        int idx = id - base - (__shfl_sync(full, pp, w) - kept - cut * nsw);
-        const int ib = ibase + __shfl_sync(full, ii, w) - cut, sb = sbase + __shfl_sync(full, ss, w) - cut * nsw;
-        const bool split = idx >= kept;
-        int seg = 0, item = idx, n_seg = 1;
-        if (split) {  // piece-major, so that neighbours in time read the same part of the keys
-          idx -= kept;
-          seg = idx / cut;
-          item = kept + idx % cut;
-          n_seg = nsw;
+        q.ntmax = __shfl_sync(full, r.ntmax, w);
+        const int before = __shfl_sync(full, pp, w);
+        int item, nt, first = 0, n_seg = 1, seg = 0, list = 0;  // of a split item: pieces, this one's number, its place in the list
+        if (CTAS == 1) {
+          const int len = q.ntmax + kItem;
+          const int start = base + before - q.nqt * a.Hkv * len;
+          item = (x - start) / len;
+          first = start + item * len;  // the item's place in the row
+        } else {
+          const int nsw = __shfl_sync(full, ns, w), kept = __shfl_sync(full, nw, w);
+          const int cut = q.nqt * a.Hkv - kept;
+          item = id - base - (before - kept - cut * nsw);
+          if (item >= kept) {  // piece-major, so that neighbours in time read the same part of the keys
+            const int idx = item - kept;
+            seg = idx / cut;
+            item = kept + idx % cut;
+            n_seg = nsw;
+            list = ibase + __shfl_sync(full, ii, w) - cut + item - kept;
+            pc.slot = sbase + __shfl_sync(full, ss, w) - cut * nsw + (item - kept) * nsw + seg;
+          }
         }
         pc.h = item % a.Hkv;
         const int qt = q.nqt - 1 - item / a.Hkv;  // longest first
-        int nt;
         tile_range<KT>(a, q, qt, pc.lo, pc.nsink, nt);
         pc.b = b32 + w;
         pc.tok0 = q.start + qt * a.tpt;
         pc.toks = min(a.tpt, q.nq - qt * a.tpt);
         pc.pos0 = q.T - q.nq + qt * a.tpt;
-        const int each = nt / n_seg, more = nt % n_seg;  // the first `more` pieces take a tile more
-        pc.j0 = seg * each + min(seg, more);
-        pc.n = each + (seg < more ? 1 : 0);
-        pc.slot = split ? sb + (item - kept) * nsw + seg : -1;
-        if (split && seg == 0 && rank == 0 && lane == 0) {
-          const int at = ib + item - kept;
-          a.ws_item[2 * at] = make_int4(pc.tok0, pc.toks * a.G, pc.h, pc.slot);
-          a.ws_item[2 * at + 1] = make_int4(nsw, 0, 0, 0);
+        pc.last = 0;
+        if (CTAS == 1) {
+          // Tiles of the item lie at [first + kItem, first + len), fewer than
+          // ntmax of them spread evenly; the CTAs that share these have its pieces.
+          const int len = q.ntmax + kItem, lo = max(0, x - first - kItem), hi = max(0, min(len, x_end - first) - kItem);
+          int f = unit, l = unit;
+          if (q.ntmax == 0) {
+            f = l = owner(first);
+          } else if (first + kItem < x_begin || first + len > x_end) {
+            f = owner(first + kItem);
+            l = owner(first + len - 1);
+          }
+          x = min(x_end, first + len);
+          pc.j0 = 0;
+          pc.n = nt;
+          if (unit < f || unit > l) {
+            pc.last = 1;  // nothing of it but the part that stands for its pipeline
+          } else if (f < l) {
+            pc.j0 = nt == q.ntmax ? lo : static_cast<int>(static_cast<int64_t>(lo) * nt / q.ntmax);
+            pc.n = (nt == q.ntmax ? hi : static_cast<int>(static_cast<int64_t>(hi) * nt / q.ntmax)) - pc.j0;
+            n_seg = l - f + 1;
+            seg = unit - f;
+            list = unit;
+            pc.slot = seg == 0 ? 2 * unit + 1 : 2 * unit;
+            listed |= seg == 0;
+          }
+        } else {
+          const int each = nt / n_seg, more = nt % n_seg;  // the first `more` pieces take a tile more
+          pc.j0 = seg * each + min(seg, more);
+          pc.n = each + (seg < more ? 1 : 0);
         }
-      } else {
-        pc.last = 1;
+        if (!pc.last && n_seg > 1 && seg == 0 && rank == 0 && lane == 0) {
+          a.ws_item[2 * list] = make_int4(pc.tok0, pc.toks * a.G, pc.h, pc.slot);
+          // pieces; the slots of the second and of each further one
+          a.ws_item[2 * list + 1] = CTAS == 1 ? make_int4(n_seg, 2 * unit + 2, 2, 0) : make_int4(n_seg, pc.slot + 1, 1, 0);
+        }
+      }
+      if (pc.last) {
         pc.n = 0;
         pc.toks = 0;
         pc.slot = -1;
@@ -836,7 +928,9 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       for (int i = 0; i < 1000000 && tc::global_ns() - t0 < 20000000ull; i++) __nanosleep(1000);
     }
     // split items of this call, for the merge
-    if (unit == 0 && rank == 0) {
+    if (CTAS == 1) {
+      if (!listed && lane == 0) a.ws_item[2 * unit + 1] = make_int4(0, 0, 0, 0);
+    } else if (unit == 0 && rank == 0) {
       int cut = 0, before = 0, rows = 0;
 #pragma unroll 1
       for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -860,6 +954,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       if (lane == 0) {
         a.ws_head[0] = cut;
         a.ws_head[1] = rows;
+        a.ws_head[2] = 0;
       }
     }
   } else if (warp == 1) {
@@ -1381,56 +1476,88 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   if (CTAS == 2) tc::cluster_sync();
 }
 
-// Joins the pieces of split items in piece order, at most 64 of them (kCand).
-// With few rows a block takes a row, its warps every eighth piece; with many a
-// warp takes a row.  Lane l holds the weights of pieces l and l + 32.
+// Joins the pieces of split items in piece order.  With few rows a block takes
+// a row, its warps every eighth piece; with many a warp takes a row.
+constexpr int kMaxPieces = 160;                     // also the most CTAs of a launch
+constexpr int kMaxItems = kSplitPerPair * kMaxPieces / 4;  // a split item has two pieces at least
 template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head, const int4* __restrict__ item,
                                                     const float2* __restrict__ ml, const float* __restrict__ o,
                                                     int part_rows, int G, int Hq, uint16_t* __restrict__ out) {
   constexpr int E = D / 32;  // columns per lane: float4 f at 4 (lane + 32 f)
-  __shared__ float red[8][D];
+  constexpr int Q = kMaxPieces / 32;
+  __shared__ __align__(16) float red[8][D];
+  __shared__ float weight[8][kMaxPieces];
+  __shared__ int items[kMaxItems], n_items;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();  // launched early: the partials are complete from here on
-  const int rows = head[1], tasks = head[0] * rows;
-  const bool wide = tasks <= 2 * static_cast<int>(gridDim.x);  // a block per row
+  // Single CTAs list a split item at the CTA where it begins, so the list has gaps.
+  const int listed = min(head[0], kMaxItems), rows = head[1];
+  const bool gaps = head[2] != 0;
+  if (gaps)
+    for (int i = threadIdx.x; i < listed; i += 256) items[i] = item[2 * i + 1].x;
+  __syncthreads();
+  if (gaps && warp == 0) {  // closed up in order: every block has to see the same list
+    int n = 0;
+    for (int i = 0; i < listed; i += 32) {
+      const bool is = i + lane < listed && items[i + lane] > 0;
+      const uint32_t mask = __ballot_sync(0xffffffffu, is);
+      if (is) items[n + __popc(mask & ((1u << lane) - 1u))] = i + lane;
+      n += __popc(mask);
+      __syncwarp();
+    }
+    if (lane == 0) n_items = n;
+  }
+  __syncthreads();
+  const int tasks = (gaps ? n_items : listed) * rows;
+  const bool wide = tasks <= 8 * static_cast<int>(gridDim.x);  // a block per row
   const int step = wide ? gridDim.x : gridDim.x * 8, first = wide ? blockIdx.x : blockIdx.x * 8 + warp;
   const int s0 = wide ? warp : 0, ds = wide ? 8 : 1;
 #pragma unroll 1
   for (int w = first; w < tasks; w += step) {
-    const int it = w / rows, row = w - it * rows;
-    const int4 x = item[2 * it];
-    const int n = item[2 * it + 1].x;
+    const int at = w / rows, row = w - at * rows, it = gaps ? items[at] : at;
+    const int4 x = item[2 * it], y = item[2 * it + 1];
+    const int n = y.x;
     if (row >= x.y) continue;  // the same for the whole block where it takes a row
-    const int64_t at = static_cast<int64_t>(x.w) * part_rows + row;
-    float2 v0 = make_float2(-INFINITY, 0.f), v1 = v0;
-    if (lane < n) v0 = ml[at + static_cast<int64_t>(lane) * part_rows];
-    if (lane + 32 < n) v1 = ml[at + static_cast<int64_t>(lane + 32) * part_rows];
-    float m = fmaxf(v0.x, v1.x);
+    auto slot_row = [&](int s) { return static_cast<int64_t>(s == 0 ? x.w : y.y + (s - 1) * y.z) * part_rows + row; };
+    float2 v[Q];
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < Q; i++) {
+      v[i] = make_float2(-INFINITY, 0.f);
+      if (lane + 32 * i < n) v[i] = ml[slot_row(lane + 32 * i)];
+      m = fmaxf(m, v[i].x);
+    }
 #pragma unroll
     for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    // A piece without a visible key has weight 0, and its O may be unwritten; NaN sums keep theirs.
-    const bool none0 = v0.x == -INFINITY && v0.y == 0.f, none1 = v1.x == -INFINITY && v1.y == 0.f;
-    const float f0 = none0 ? 0.f : exp2f(v0.x - m), f1 = none1 ? 0.f : exp2f(v1.x - m);
-    float den = (none0 ? 0.f : f0 * v0.y) + (none1 ? 0.f : f1 * v1.y);
+    // A piece without a visible key has weight 0, and its O may be unwritten.
+    float den = 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < Q; i++) {
+      const bool none = v[i].x == -INFINITY && v[i].y == 0.f;
+      const float f = none ? 0.f : exp2f(v[i].x - m);
+      den += none ? 0.f : f * v[i].y;
+      weight[warp][lane + 32 * i] = f;
+    }
+    __syncwarp();
 #pragma unroll
     for (int i = 16; i; i >>= 1) den += __shfl_xor_sync(0xffffffffu, den, i);
-    const uint32_t has0 = __ballot_sync(0xffffffffu, !none0), has1 = __ballot_sync(0xffffffffu, !none1);
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; e++) acc[e] = 0.f;
-#pragma unroll 8
+#pragma unroll 4
     for (int s = s0; s < n; s += ds) {
-      const float f = __shfl_sync(0xffffffffu, s < 32 ? f0 : f1, s & 31);
-      if (!(((s < 32 ? has0 : has1) >> (s & 31)) & 1u)) continue;
-      const float* src = o + (at + static_cast<int64_t>(s) * part_rows) * D + 4 * lane;
+      const float f = weight[warp][s];
+      if (f == 0.f) continue;
+      const float* src = o + slot_row(s) * D + 4 * lane;
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
-        const float4 y = *reinterpret_cast<const float4*>(src + 32 * e);
-        acc[e] += f * y.x;
-        acc[e + 1] += f * y.y;
-        acc[e + 2] += f * y.z;
-        acc[e + 3] += f * y.w;
+        const float4 z = *reinterpret_cast<const float4*>(src + 32 * e);
+        acc[e] += f * z.x;
+        acc[e + 1] += f * z.y;
+        acc[e + 2] += f * z.z;
+        acc[e + 3] += f * z.w;
       }
     }
     const float inv = den != 0.f ? 1.f / den : 0.f;
@@ -1444,9 +1571,9 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          const float2 y = *reinterpret_cast<const float2*>(&red[i][2 * threadIdx.x]);
-          sum.x += y.x;
-          sum.y += y.y;
+          const float2 z = *reinterpret_cast<const float2*>(&red[i][2 * threadIdx.x]);
+          sum.x += z.x;
+          sum.y += z.y;
         }
         *reinterpret_cast<uint32_t*>(dst + 2 * threadIdx.x) = pack_bf16(sum.x * inv, sum.y * inv);
       }
@@ -1527,7 +1654,8 @@ int tile_rows(int n_tok, int G, int ctas) {
 
 Layout layout(int n_tok, int G, int d, int ctas, int sms) {
   Layout w;
-  w.max_split = kSplitPerUnit / (3 - ctas) * (sms / ctas);
+  if (sms > kMaxPieces) sms = kMaxPieces;
+  w.max_split = ctas == 1 ? 2 * sms : kSplitPerPair * (sms / 2);
   w.part_rows = tile_rows(n_tok, G, ctas);
   w.item = 256;
   w.ml = w.item + static_cast<size_t>(w.max_split) * 2 * sizeof(int4);
@@ -1542,7 +1670,7 @@ int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, con
   auto kernel = paged_kernel<D, CTAS, INT8>;
   if (smem_limit_once(configured, kernel, kMaxSmem) != SKV_OK) return SKV_ECUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms / CTAS * CTAS, 1, 1);
+  cfg.gridDim = dim3((sms < kMaxPieces ? sms : kMaxPieces) / CTAS * CTAS, 1, 1);  // an item has a piece per CTA at most
   cfg.blockDim = dim3(kThreads<INT8>, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

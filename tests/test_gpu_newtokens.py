@@ -290,6 +290,16 @@ def test_long_axis_split(skv, kind, d, lens, new, S, W):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,lo,hi,n", [(40, 300, 1500, 1), (24, 10, 4000, 1), (30, 200, 900, 3), (7, 1000, 5000, 1)])
+def test_ragged_batches_are_shared_out(skv, kind, B, lo, hi, n):
+    """Ragged requests whose keys the CTAs share evenly: most items are cut, anywhere."""
+    rng = np.random.default_rng(B + hi)
+    lens = [int(x) for x in np.exp(rng.uniform(math.log(lo), math.log(hi), B))]
+    c = Case(skv, kind_of(skv, kind), 256 if n == 1 else 128, 8, 2, 16, lens, [n] * B, seed=B)
+    c.check(single=n == 1)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_many_requests(skv, kind):
     rng = np.random.default_rng(3)
     lens = [int(x) for x in np.exp(rng.uniform(0, math.log(600), 150))]
