@@ -403,22 +403,24 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 
 // A warp writes 64 bytes of each lane's row: through shared memory, so that a
 // store covers eight rows of 64 consecutive bytes (32 rows of 16 bytes take
-// the store unit 32 lines each, and ran 3 to 7 K clocks per piece).  Row
-// `id` (-1: none) starts at base + id * pitch.
-__device__ __forceinline__ void put_rows(unsigned char* buf, int lane, const uint32_t (&w)[16], int id, char* base,
-                                         int pitch) {
+// the store unit 32 lines each, and ran 3 to 7 K clocks per piece).  Lane i
+// stores piece i % 4 of rows i / 4 + 8 k, at to[k] (null: no such row).
+__device__ __forceinline__ void put_rows(unsigned char* buf, int lane, const uint32_t (&w)[16], char* const (&to)[4],
+                                         int at) {
 #pragma unroll
   for (int c = 0; c < 4; c++)
     *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
         make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   __syncwarp();
+  uint4 v[4];
 #pragma unroll
   for (int k = 0; k < 4; k++) {
     const int row = 8 * k + (lane >> 2), c = lane & 3;
-    const uint4 v = *reinterpret_cast<const uint4*>(buf + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
-    const int to = __shfl_sync(0xffffffffu, id, row);
-    if (to >= 0) *reinterpret_cast<uint4*>(base + static_cast<int64_t>(to) * pitch + 16 * c) = v;
+    v[k] = *reinterpret_cast<const uint4*>(buf + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
   }
+#pragma unroll
+  for (int k = 0; k < 4; k++)
+    if (to[k]) *reinterpret_cast<uint4*>(to[k] + at) = v[k];
   __syncwarp();
 }
 
@@ -1340,11 +1342,26 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         unsigned char* buf = sOut + (warp - 4) * 2048;
         const int id = !live ? -1 : whole ? static_cast<int>(tok * (a.Hkv * a.G)) + pc.h * a.G + head_r : static_cast<int>(prow);
         char* base = whole ? reinterpret_cast<char*>(a.out) : reinterpret_cast<char*>(a.ws_o);
+        const int pitch = whole ? 2 * D : 4 * D;
         const bool few = __popc(__ballot_sync(0xffffffffu, live)) <= 8;  // each lane writes its own row
+        char* to[4];
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          const int row = few ? id : __shfl_sync(0xffffffffu, id, 8 * x + (lane >> 2));
+          to[x] = row < 0 ? nullptr : base + static_cast<int64_t>(row) * pitch + (few ? 0 : 16 * (lane & 3));
+        }
+        auto put = [&](const uint32_t (&w)[16], int at) {  // 64 bytes of each row
+          if (!few) {
+            put_rows(buf, lane, w, to, at);
+          } else if (live) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              *reinterpret_cast<uint4*>(to[0] + at + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        };
 #pragma unroll 1
         for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
           uint32_t o[32];
-          __syncwarp();
           if (pc.n > 0) {
             tc::tmem_ld32(tm + lane_base + c0, o);
             tc::tmem_wait_ld();
@@ -1352,31 +1369,27 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
 #pragma unroll
             for (int i = 0; i < 32; i++) o[i] = 0u;
           }
-          if (dirty && live) {
+          if (dirty) {
             float y[32];
 #pragma unroll 1
             for (int i = 0; i < 32; i++) y[i] = 0.f;
-            add_nonfinite<D, KT>(a, pc, p, p_last, c0, y);
+            if (live) add_nonfinite<D, KT>(a, pc, p, p_last, c0, y);
 #pragma unroll
             for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) + y[i]);
+            __syncwarp();
           }
-          __syncwarp();
-#pragma unroll 1
-          for (int y = 0; y < (whole ? 1 : pc.n > 0 ? 2 : 0); y++) {  // 32 columns of bf16, or twice 16 of fp32
-            uint32_t w[16];
+          uint32_t w[16];
+          if (whole) {
 #pragma unroll
             for (int i = 0; i < 16; i++)
-              w[i] = whole ? pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv)
-                           : y ? o[16 + i] : o[i];
-            char* to = base + (whole ? 2 * c0 : 4 * (c0 + 16 * y));
-            const int pitch = whole ? 2 * D : 4 * D;
-            if (!few) {
-              put_rows(buf, lane, w, id, to, pitch);
-            } else if (live) {
+              w[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+            put(w, 2 * c0);
+          } else if (pc.n > 0) {
 #pragma unroll
-              for (int i = 0; i < 4; i++)
-                *reinterpret_cast<uint4*>(to + static_cast<int64_t>(id) * pitch + 16 * i) =
-                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            for (int y = 0; y < 2; y++) {
+#pragma unroll
+              for (int i = 0; i < 16; i++) w[i] = o[16 * y + i];
+              put(w, 4 * (c0 + 16 * y));
             }
           }
         }
