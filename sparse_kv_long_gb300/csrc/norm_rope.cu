@@ -289,9 +289,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_kernel(const N
         // top half of the low 64 bits of pos * t (pos sign-extended)
         uint32_t top = static_cast<uint32_t>(pos) * hi + __umulhi(static_cast<uint32_t>(pos), lo);
         if (pos < 0) top -= lo;
+        // half turns: 31 bits, of which a float holds 24; the rest turns the result by a small angle
+        // (without it one more rounding to bf16 in 50000 falls to the other side)
+        const int32_t ht = static_cast<int32_t>(top);
+        const float x = static_cast<float>(ht);
+        const float rest = static_cast<float>(ht - static_cast<int32_t>(x)) * 1.4629180792671596e-9f;  // pi 2^-31
         float sn, cn;
-        sincospif(static_cast<float>(static_cast<int32_t>(top)) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
-        cs[warp][f] = make_float2(cn, sn);
+        sincospif(x * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
+        cs[warp][f] = make_float2(fmaf(-sn, rest, cn), fmaf(cn, rest, sn));
       }
       __syncwarp();
     }
