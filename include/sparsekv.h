@@ -739,8 +739,8 @@ int skv_prefill_attend(int nq, int Hq, int Hkv, int d, const uint16_t *q, const 
  * q_out[i] = bf16(z).  The row out_rows[i] of k_pool takes bf16(z) of the
  * keys and that of v_pool the values, in the kv_kind row encoding:
  * SKV_KV_BF16 as they are, SKV_KV_INT8 as skv_quantize_int8_rows encodes the
- * bf16 values.  The angle is reduced modulo one turn before it is rounded to
- * fp32, so far positions lose nothing (about 2e-7 rad up to 2^24).
+ * bf16 values.  The angle is reduced modulo one turn as a 64-bit integer, so
+ * far positions lose nothing (inv_freq is taken as exact, and is finite).
  *   q  bf16 [n_tok][Hq][d], k and v  bf16 [n_tok][Hkv][d]: a token's heads are
  *      consecutive, tokens q_stride / k_stride / v_stride elements apart (views
  *      of a fused projection).  Each of the three may be NULL: that part is
@@ -779,7 +779,8 @@ int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int rot, int int
  * (a sliding window of W tokens, itself included, and S sinks).  Query head g
  * reads KV head g / (Hq/Hkv):
  *   out[i][g] = sum_t softmax_t(softmax_scale q[i][g] . k[t]) v[t]
- * A token that sees nothing (p < 0) gets zeros.  Key t of request b is pool
+ * A token that sees nothing (p < 0) gets zeros.  What a row holds that a token
+ * does not see may be anything, NaN and infinities included.  Key t of request b is pool
  * row block_table[b][t / page] * page + t % page, rows in the kv_kind
  * encoding.  Only pages with visible keys are looked up (pages before a
  * window may be gone); a page beyond n_pages or the pool is skipped and sets
@@ -793,16 +794,23 @@ int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int rot, int int
  *            from q_start[B] on are padding: their output is left as it was.
  *            A q_start that descends or leaves [0, n_tok] sets SKV_DEV_RANGE
  *   out      bf16 [n_tok][Hq][d]
- *   workspace  skv_paged_attend_workspace_size(...) bytes, zero-filled before
- *            first use; a workspace of the largest size serves every smaller
- *            call, in any order
+ *   workspace  skv_paged_attend_workspace_size(...) bytes; nothing in it
+ *            outlasts a call, so calls of any sizes may follow one another on
+ *            one of the largest size, but two at once need one each.  It holds
+ *            the partial sums of cut requests: at d = 256 up to 160 MB for
+ *            chunks, 40 MB for drafts, 5 MB for single tokens of 16 heads
+ *            a KV head
  * Constraints: d in {128, 256}; Hq / Hkv <= 128; page a multiple of 8;
- * softmax_scale > 0; q_stride a multiple of 8; q, out, pools and workspace
- * 16-byte aligned; B <= 4096; n_pages * page < 2^31 - 1024.  Errors: SKV_EUNSUPPORTED outside the first three, SKV_ENOMEM for a
- * short workspace, SKV_EINVAL for the rest.
+ * 0 < softmax_scale <= 2e38; q_stride a multiple of 8; q, out, pools and
+ * workspace 16-byte aligned; B <= 4096; n_pages * page < 2^31 - 1024; W <= 2^30
+ * or at least n_pages * page; n_tok * Hq < 2^31; tiles of 128 / (Hq/Hkv)
+ * tokens by KV heads by 64 keys of the table's width fewer than 2^31.
+ * Errors: SKV_EUNSUPPORTED outside the first three, SKV_ENOMEM for a short
+ * workspace, SKV_EINVAL for the rest.
  * Accuracy: logits accumulate exact products in fp32, the probabilities
  * (times the value scale for int8 rows) are rounded to bf16 for the tensor
  * cores, and each row is divided by the sum of its rounded probabilities.
+ * A call's result does not change from run to run.
  */
 size_t skv_paged_attend_workspace_size(int B, int n_tok, int Hq, int Hkv, int d);
 int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, int d, const uint16_t *q,

@@ -477,9 +477,23 @@ def _heads(t):
         return 0, 0, 0
     n, H, d = t.shape
     s = t.stride()
-    if (H > 1 and s[1] != d) or (d > 1 and s[2] != 1):
-        raise ValueError("a token's heads must be consecutive")
+    if (H > 1 and s[1] != d) or (d > 1 and s[2] != 1) or t.dtype is not torch.bfloat16:
+        raise ValueError("expected bf16 with a token's heads consecutive")
     return H, d, s[0] if n > 1 else H * d
+
+
+def _want(dev, *wanted):
+    """Each (tensor or None, dtype, n) has to be contiguous, of that type, of n elements at least and on device dev,
+    which is the current one."""
+    for t, dtype, n in wanted:
+        if t is not None:
+            if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+                raise ValueError(f"expected {n} contiguous elements of {dtype}, not {t.dtype} {tuple(t.shape)} with "
+                                 f"strides {t.stride()}")
+            if t.get_device() != dev:
+                raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("expected tensors on the current CUDA device")
 
 
 def norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pool, v_pool, q_weight=None, k_weight=None, eps=1e-6,
@@ -496,12 +510,20 @@ def norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pool, v_pool, q_weig
     if (k is not None and (k.shape[0] != n or kd != d)) or (v is not None and (v.shape[0] != n or vd != d)) or \
             (kh and vh and kh != vh):
         raise ValueError("q, k and v differ in tokens, head dimension or KV heads")
+    kind = torch.int8 if kv_kind == KV_INT8 else torch.bfloat16
+    dev = some.get_device()
+    if (k is not None and k.get_device() != dev) or (v is not None and v.get_device() != dev):
+        raise ValueError("q, k and v on different devices")
     pool = k_pool if k_pool is not None else v_pool
+    rows, H = 0 if pool is None else pool.shape[0], kh or vh
+    _want(dev, (k_pool, kind, rows * H * d), (v_pool, kind, rows * H * d), (k_scale, torch.float16, rows * H),
+          (v_scale, torch.float16, rows * H), (q_out, torch.bfloat16, n * Hq * d), (q_weight, torch.float32, d),
+          (k_weight, torch.float32, d), (positions, torch.int32, n), (inv_freq, torch.float32, 0),
+          (out_rows, torch.int64, n), (status, torch.int32, 1))
     _check("skv_norm_rope_append", (_lib or _load()).skv_norm_rope_append(
-        n, Hq, kh or vh, d, 0 if inv_freq is None else 2 * inv_freq.shape[0], 1 if interleaved else 0, _at(q), qs,
+        n, Hq, H, d, 0 if inv_freq is None else 2 * inv_freq.shape[0], 1 if interleaved else 0, _at(q), qs,
         _at(k), ks, _at(v), vs, _at(q_weight), _at(k_weight), eps, _at(positions), _at(inv_freq), _at(q_out), kv_kind,
-        _at(out_rows), 0 if pool is None else pool.shape[0], _at(k_pool), _at(v_pool), _at(k_scale), _at(v_scale),
-        _at(status), _raw_stream(stream)))
+        _at(out_rows), rows, _at(k_pool), _at(v_pool), _at(k_scale), _at(v_scale), _at(status), _raw_stream(stream)))
     return q_out
 
 
@@ -515,9 +537,16 @@ def paged_attend(kv_kind, q, k_pool, v_pool, block_table, page, lengths, softmax
     q_start[b+1] (None: one each); pools [rows][Hkv][d]; block_table int32 [B][n_pages] -> out bf16 [n][Hq][d]."""
     Hq, d, qs = _heads(q)
     B, n_pages = block_table.shape
-    rows, Hkv, _ = k_pool.shape
+    rows, Hkv, kd = k_pool.shape
+    n, kind = q.shape[0], torch.int8 if kv_kind == KV_INT8 else torch.bfloat16
+    if kd != d:
+        raise ValueError(f"queries of {d} values, rows of {kd}")
+    _want(q.get_device(), (k_pool, kind, 0), (v_pool, kind, rows * Hkv * d), (k_scale, torch.float16, rows * Hkv),
+          (v_scale, torch.float16, rows * Hkv), (out, torch.bfloat16, n * Hq * d), (block_table, torch.int32, 0),
+          (lengths, torch.int32, B), (q_start, torch.int32, B + 1), (status, torch.int32, 1),
+          (workspace, workspace.dtype, 0))
     _check("skv_paged_attend", (_lib or _load()).skv_paged_attend(
-        kv_kind, B, q.shape[0], Hq, Hkv, d, q.data_ptr(), qs, k_pool.data_ptr(), v_pool.data_ptr(), _at(k_scale),
+        kv_kind, B, n, Hq, Hkv, d, q.data_ptr(), qs, k_pool.data_ptr(), v_pool.data_ptr(), _at(k_scale),
         _at(v_scale), rows, page, block_table.data_ptr(), n_pages, _at(q_start), lengths.data_ptr(), S, W,
         softmax_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _at(status), _raw_stream(stream)))

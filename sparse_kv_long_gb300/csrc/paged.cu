@@ -160,7 +160,7 @@ template <int KT>
 __device__ __noinline__ Req request(const PagedArgs& a, int b, bool report) {
   Req r;
   if (b >= a.B) return Req{0, 0, 0, 0, 0};
-  r.T = a.lengths[b];
+  r.T = max(0, a.lengths[b]);
   if (a.q_start) {
     const int s = a.q_start[b], e = a.q_start[b + 1];
     const bool bad = s < 0 || e < s || e > a.n_tok;
@@ -1762,16 +1762,23 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || q_stride % 8 ||
       q_stride < static_cast<int64_t>(Hq) * d)
     return SKV_EINVAL;
-  if (!(softmax_scale > 0.f) || softmax_scale > 3.0e38f) return SKV_EINVAL;
+  if (!(softmax_scale > 0.f) || softmax_scale > 2.0e38f) return SKV_EINVAL;  // in log2 units it is finite, too
   // 32-bit positions, tile coordinates and work-list counts
-  if (n_pages * page > INT32_MAX - 1024 || static_cast<int64_t>(n_tok) * Hq > INT32_MAX || n_pool_rows > (static_cast<int64_t>(1) << 33)) return SKV_EINVAL;
+  if (n_pages > INT32_MAX / page || n_pages * page > INT32_MAX - 1024 || static_cast<int64_t>(n_tok) * Hq > INT32_MAX ||
+      n_pool_rows > (static_cast<int64_t>(1) << 33))
+    return SKV_EINVAL;
+  if (W >= n_pages * page) W = 0;  // no window: a position does not reach it
+  if (W > 1 << 30) return SKV_EINVAL;
+  const int G = Hq / Hkv;
+  const int ctas = ctas_for(B, n_tok, G, !q_start);
+  const int tpt = ctas * (kRows / G);  // tokens per query tile
+  const int64_t key_tiles = n_pages * page / keys_per_tile(d, ctas) + 1 + kItem;
+  if (key_tiles > INT32_MAX / ((static_cast<int64_t>(B) + n_tok / tpt) * Hkv)) return SKV_EINVAL;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < skv_paged_attend_workspace_size(B, n_tok, Hq, Hkv, d))
     return SKV_ENOMEM;
   const int sms = sm_count();
   if (sms <= 1 || !encode_fn()) return SKV_ECUDA;
-  const int G = Hq / Hkv;
-  const int ctas = ctas_for(B, n_tok, G, !q_start);
   const int stage = keys_per_tile(d, ctas) / ctas * d * 2;
 
   PagedArgs a{};
@@ -1780,7 +1787,7 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
   a.Hkv = Hkv;
   a.G = G;
   a.tpc = kRows / G;
-  a.tpt = ctas * a.tpc;
+  a.tpt = tpt;
   a.v_pool = int8 ? nullptr : static_cast<const uint16_t*>(v_pool);
   a.k_scale = reinterpret_cast<const __half*>(k_scale);
   a.v_scale = reinterpret_cast<const __half*>(v_scale);

@@ -543,3 +543,93 @@ def test_prompt_then_decode(skv, kind):
     tol = 2.0 ** -8 * np.abs(z) + 2.0 ** -19 * mag + (0.51 * f64(scales[0])[rows][..., None] if k8 else 0.0)
     assert (np.abs(k[rows] - z) <= tol).all()
     res.close()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,Hq,Hkv,page,lens,new", [
+    (128, 128, 1, 8, [300, 5], [1, 3]), (256, 128, 1, 16, [40, 290], [40, 150]), (256, 100, 1, 2048, [3000], [7]),
+    (128, 70, 10, 1000, [2100, 999], [300, 1]), (256, 2, 2, 24, [520], [520]),
+])
+def test_head_groups_and_page_sizes(skv, kind, d, Hq, Hkv, page, lens, new):
+    Case(skv, kind_of(skv, kind), d, Hq, Hkv, page, lens, new, seed=30, pad=2).check()
+
+
+def test_most_requests(skv):
+    rng = np.random.default_rng(31)
+    lens = [int(x) for x in rng.integers(0, 30, 4096)]
+    Case(skv, skv.KV_BF16, 128, 2, 1, 8, lens, [min(t, 1) for t in lens], seed=31).check(S=1, W=9)
+    Case(skv, skv.KV_INT8, 128, 2, 1, 8, [max(t, 1) for t in lens], [1] * 4096, seed=32).check(single=True)
+
+
+def test_lengths_below_the_new_tokens(skv):
+    """Tokens that stand before the cache's first row see nothing: zeros; so do all of a negative length."""
+    c = Case(skv, skv.KV_BF16, 256, 8, 2, 16, [40, 3, 60, 0], [4, 9, 200, 5], seed=33)
+    c.check()
+    want = c.out.clone()
+    assert (want[4:10] == 0).all() and (want[13:153] == 0).all() and (want[213:] == 0).all()
+    c.lens = [40, 3, 60, -7]
+    assert torch.equal(c.run(), want)
+    c.lens = [40, -(1 << 31), 60, -7]
+    got = c.run()
+    assert torch.equal(got[:4], want[:4]) and (got[4:13] == 0).all() and torch.equal(got[13:], want[13:])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_window_as_long_as_the_table_is_none(skv, kind):
+    c = Case(skv, kind_of(skv, kind), 128, 8, 2, 16, [200, 33], [130, 1], seed=34)
+    want = c.run().clone()
+    for W in (c.n_pages * 16, (1 << 31) - 1):
+        assert torch.equal(c.run(W=W), want)
+
+
+def test_two_calls_at_once(skv):
+    """Two streams, a workspace each: chunks beside single tokens."""
+    a = Case(skv, skv.KV_BF16, 256, 16, 2, 64, [9000], [600], seed=35)
+    b = Case(skv, skv.KV_INT8, 256, 24, 4, 64, [4000, 17, 9000], [1, 1, 1], seed=36)
+    want = a.run().clone(), b.run().clone()
+    s = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        for x in s:
+            x.wait_stream(torch.cuda.current_stream())
+        out = a.run(stream=s[0]), b.run(stream=s[1])
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_captured_append(skv):
+    """A captured append, replayed with new rows and positions written in place."""
+    g, n, d = gen(37), 9, 128
+    q, k, v = randn(g, n, 8, d), randn(g, n, 2, d), randn(g, n, 2, d)
+    pos, rows = T.dev(np.arange(n, dtype=np.int32)), T.dev(np.arange(n, dtype=np.int64))
+    inv = torch.logspace(0, -4, d // 2, device="cuda")
+    out, kp, vp = torch.zeros_like(q), torch.zeros((64, 2, d), dtype=torch.bfloat16, device="cuda"), torch.zeros(
+        (64, 2, d), dtype=torch.bfloat16, device="cuda")
+    call = lambda: skv.norm_rope_append(q, k, v, pos, inv, out, kp, vp, out_rows=rows)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for shift in (5, 50):
+        pos += shift
+        rows += 1
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone(), kp.clone(), vp.clone()
+        call()
+        assert all(torch.equal(x, y) for x, y in zip(got, (out, kp, vp)))
+
+
+def test_host_tensors_are_refused(skv):
+    c = Case(skv, skv.KV_BF16, 128, 4, 2, 16, [20], [1], seed=38)
+    c.run()
+    for i in (0, 1):
+        kept, c.dev[i] = c.dev[i], c.dev[i].cpu()
+        with pytest.raises(ValueError):
+            c.call()
+        c.dev[i] = kept
+    q = torch.zeros((1, 4, 128), dtype=torch.bfloat16)
+    for at in ("q", "k"):
+        x = {"q": c.q, "k": c.k[:1], at: q[:, :2] if at == "k" else q}
+        with pytest.raises(ValueError):
+            skv.norm_rope_append(x["q"], x["k"], None, c.dev[1], None, c.out, c.k, None)

@@ -72,3 +72,35 @@ def test_binding_refuses_scattered_heads():
     q, k = torch.zeros((4, 8, 256), dtype=torch.bfloat16), torch.zeros((5, 2, 256), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         skv.norm_rope_append(q, k, None, None, None, None, None, None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(scale=2.5e38), EINVAL),  # finite, but not in units of log2
+    (dict(n_pages=(1 << 62) // 16), EINVAL), (dict(n_pages=(1 << 27) - 64), EINVAL),
+    (dict(n_pages=(1 << 27) - 100, W=(1 << 30) + 1), EINVAL),  # a window that is neither short nor everything
+    (dict(n_tok=1 << 28), EINVAL), (dict(B=4000, n_tok=4000, n_pages=1 << 22), EINVAL), (dict(n_rows=1 << 34), EINVAL),
+])
+def test_paged_attend_refuses_what_32_bits_do_not_hold(lib, change, want):
+    assert lib.skv_paged_attend(*{**ATT, **change}.values()) == want
+
+
+def test_bindings_refuse_other_types_strides_and_sizes():
+    import sparse_kv_long_gb300 as skv
+    q = torch.zeros((4, 8, 256), dtype=torch.bfloat16)
+    pool = torch.zeros((64, 2, 256), dtype=torch.bfloat16)
+    i32 = torch.zeros((4,), dtype=torch.int32)
+    good = dict(q=q, k_pool=pool, v_pool=pool, block_table=torch.zeros((4, 2), dtype=torch.int32), page=16, lengths=i32,
+                softmax_scale=1.0, out=q, workspace=q)
+    for bad in (dict(q=q.half()), dict(k_pool=pool.half()), dict(v_pool=torch.zeros((2, 64, 256)).bfloat16().transpose(0, 1)),
+                dict(block_table=torch.zeros((2, 4), dtype=torch.int32).T), dict(lengths=i32.long()),
+                dict(out=q.float()), dict(q_start=i32.long()), dict(status=i32.long()), dict(k_scale=i32),
+                dict(v_pool=pool[:63]), dict(out=q[:3]), dict(lengths=i32[:3]), dict(q_start=i32), dict(k_pool=pool[..., :128])):
+        with pytest.raises(ValueError, match="contiguous|consecutive|differ |queries of"):
+            skv.paged_attend(skv.KV_BF16, **{**good, **bad})
+    good = dict(q=q, k=q[:, :2], v=q[:, 2:4], positions=i32, inv_freq=torch.zeros((64,)), q_out=q, k_pool=pool, v_pool=pool)
+    for bad in (dict(k=q[:, :2].half()), dict(positions=i32.long()), dict(inv_freq=torch.zeros((64,)).double()),
+                dict(q_out=torch.zeros((8, 4, 256)).bfloat16().transpose(0, 1)), dict(k_pool=pool.to(torch.int8)),
+                dict(out_rows=i32), dict(q_weight=q), dict(k_weight=torch.zeros((256,)).half()),
+                dict(positions=i32[:3]), dict(q_out=q[:3]), dict(v_pool=pool[:63]), dict(q_weight=torch.zeros((255,)))):
+        with pytest.raises(ValueError, match="contiguous|consecutive|differ |queries of"):
+            skv.norm_rope_append(**{**good, **bad})
