@@ -56,6 +56,7 @@ constexpr float kLazy = 8.f;       // log2 units a maximum may grow before O is 
 constexpr int kSplitPerPair = 8;   // pieces that write partials, per pair (single CTAs: two each)
 constexpr uint32_t kGone = 0x7fc0dead;  // a NaN that no arithmetic gives
 constexpr uint32_t kSCol = 256;    // tensor memory: O in [0, D), S/P buffers from here
+constexpr uint32_t kLCol = 128;    // row sums, where the tensor cores make them
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kOutBytes = 8 * 2048;
 
@@ -67,6 +68,12 @@ constexpr int kThreads = INT8 ? 512 : 384;
 // Keys per tile.  Pairs: 128, what two logit buffers beside O leave room for at
 // D = 256.  Single CTAs are bound by reading the cache, with 32 KB stages.
 __host__ __device__ constexpr int keys_per_tile(int d, int ctas) { return ctas == 2 ? 128 : 64 * (256 / d); }
+
+// Whether the tensor cores add up the rows' weights, as a product with ones
+// beside O.  Where tensor memory has columns for it (D = 128): the additions and
+// the unpacking of the rounded weights were a third of the softmax warps'
+// exponential loop.  int8 rows' sums have the scales' reciprocals as factors.
+__host__ __device__ constexpr bool row_sums(int d, bool int8) { return d == 128 && !int8; }
 
 struct Piece {
   int tok0, toks;     // first token, tokens of the whole tile
@@ -119,6 +126,7 @@ struct alignas(16) Aux {
   };
   int nmax, items;
   uint32_t tmem_base;
+  alignas(16) uint16_t ones[256];  // 16 rows of 16 ones
   int dirty;  // a value that only some queries of a tile see was not finite
   int abort;
 };
@@ -130,7 +138,7 @@ struct alignas(16) Aux8 {  // int8 rows only
 };
 
 static_assert(kMaxStages == kMaxStaging && kScaleRing <= kPieces, "one thread sets up a barrier of each");
-static_assert(sizeof(Aux) <= 3 * 1024, "room beside the query tile, the stages and the output rows");
+static_assert(sizeof(Aux) <= 4 * 1024, "room beside the query tile, the stages and the output rows");
 
 // ---- work list -------------------------------------------------------------------
 
@@ -334,6 +342,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 
+// One column of the warp's 32 rows.
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
+  return r;
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+
 // Two fp32 values in one 64-bit register.
 struct F2 {
   uint64_t v;
@@ -499,6 +517,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   constexpr int VSUB = NSUB / CTAS;      // those of this CTA's part of V
   constexpr int STAGE = KR * D * 2;      // bytes of a K or V stage (this CTA's part)
   constexpr int THREADS = kThreads<INT8>;
+  constexpr bool SUM = row_sums(D, INT8);
   constexpr uint32_t SBO_K = NSUB * 1024, SBO_V = VSUB * 1024;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sQ = smem_raw;  // 1024-byte aligned, as the swizzled tiles need (checked below)
@@ -547,6 +566,10 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     ax->dirty = 0;
     ax->nmax = 0;
     ax->items = 0;
+  }
+  if (SUM) {
+    for (int i = tid; i < 256; i += THREADS) ax->ones[i] = 0x3f80u;  // 1
+    tc::fence_async_smem();
   }
   if (tid < 128) asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   if (warp == 1) {
@@ -971,7 +994,10 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     // left and issues the products with less around them (chunks of 2048 tokens
     // at 65536 keys: 1193 -> 1142 us).
     if (elect_one()) {
-      constexpr uint32_t id_qk = idesc_bf16(kRows * CTAS, KT, 0), id_pv = idesc_bf16(kRows * CTAS, D, 1);
+      constexpr uint32_t id_qk = idesc_bf16(kRows * CTAS, KT, 0), id_pv = idesc_bf16(kRows * CTAS, D, 1),
+                         id_sum = idesc_bf16(kRows * CTAS, 16 * CTAS, 0);
+      // eight rows of 16 bytes side by side, without a swizzle; the steps do not matter among equal values
+      const uint64_t ones = (static_cast<uint64_t>((256 >> 4) | (1u << 14)) << 32) | desc_lo(tc::smem_addr(ax->ones), 128);
       const uint32_t dQ = desc_lo(tc::smem_addr(sQ), 16), dK = desc_lo(tc::smem_addr(sKV), 16),
                      dV = desc_lo(tc::smem_addr(sKV), 1024);
       const uint32_t q_step = CTAS == 2 ? kRows * 128 >> 4 : a.q_sub >> 4;
@@ -1033,6 +1059,11 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
                 mma_ts<CTAS>(tm, p + 8 * x + (x >= KT / 32 ? KT / 4 : 0), desc(kv + x * (2 * SBO_V >> 4), SBO_V), id_pv,
                              j > 1 || x > 0);
               commit<CTAS>(&ax->kv_empty[st.s]);
+              if (SUM) {
+#pragma unroll
+                for (int x = 0; x < KT / 16; x++)
+                  mma_ts<CTAS>(tm + kLCol, p + 8 * x + (x >= KT / 32 ? KT / 4 : 0), ones, id_sum, j > 1 || x > 0);
+              }
               commit<CTAS>(&ax->pv_done[t & 1]);
             }
             st.next(a.stages);
@@ -1219,6 +1250,10 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
                 for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                 tc::tmem_st32(tm + lane_base + c0, o);
               }
+              if (SUM && wg == 0) {
+                const float s1 = __uint_as_float(tmem_ld1(tm + lane_base + kLCol));
+                tmem_st1(tm + lane_base + kLCol, __float_as_uint(s1 * alpha));
+              }
             }
             l = m_ref == -INFINITY ? 0.f : l * alpha;
             m_ref = m_new;
@@ -1261,7 +1296,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
                 for (int z = 0; z < 2; z++) {
                   const uint32_t w = pack_bf16(e[z].x, e[z].y);
                   pk[y + z] = w;
-                  ls[z] = f2_add(ls[z], f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
+                  if (!SUM) ls[z] = f2_add(ls[z], f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
                 }
               }
             }
@@ -1324,7 +1359,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       if (!ok) break;
       const uint32_t t_last = g + pc.n - 1;
       if (pc.n > 0) {
-        if (warp_live) {
+        if (!SUM && warp_live) {
           float lo;
           exchange(l, lo);
           l += lo;  // a sum of two: the same in both
@@ -1335,6 +1370,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       // ---- output: this group's half of the columns ----
       if (warp_live) {
         const bool whole = pc.slot < 0;
+        if (SUM && pc.n > 0) l = __uint_as_float(tmem_ld1(tm + lane_base + kLCol));
         const float inv = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
         const bool dirty = !INT8 && *reinterpret_cast<volatile int*>(&ax->dirty) != 0;
         const int64_t tok = static_cast<int64_t>(pc.tok0) + tok_i;
