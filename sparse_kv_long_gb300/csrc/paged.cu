@@ -584,6 +584,10 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  // Launched early, too: barriers and tensor memory are set up while the
+  // previous kernel ends (windowed single tokens, calls back to back: see the
+  // launch); from here on what it wrote is there.
+  grid_dependency_wait();
 
   // ---- plan ------------------------------------------------------------------------
   // Single CTAs: the items' key tiles, each item preceded by kItem tiles' worth
@@ -1543,6 +1547,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head
   __shared__ float weight[8][kMaxPieces];
   __shared__ int items[kMaxItems], n_items;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  allow_dependent_launch();
   grid_dependency_wait();  // launched early: the partials are complete from here on
   // Single CTAs list a split item at the CTA where it begins, so the list has gaps.
   const int listed = min(head[0], kMaxItems), rows = head[1];
@@ -1727,13 +1732,15 @@ int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, con
   cfg.blockDim = dim3(kThreads<INT8>, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CTAS;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CTAS;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kernel, km, vm, qm, a) != cudaSuccess) {
     cudaGetLastError();
     return SKV_ECUDA;
@@ -1741,8 +1748,7 @@ int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, con
   cfg.gridDim = dim3(2 * sms, 1, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
   const int* head = a.ws_head;
   const int4* item = a.ws_item;
   const float2* ml = a.ws_ml;
