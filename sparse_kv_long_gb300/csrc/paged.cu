@@ -56,7 +56,6 @@ constexpr float kLazy = 8.f;       // log2 units a maximum may grow before O is 
 constexpr int kSplitPerPair = 8;   // pieces that write partials, per pair (single CTAs: two each)
 constexpr uint32_t kGone = 0x7fc0dead;  // a NaN that no arithmetic gives
 constexpr uint32_t kSCol = 256;    // tensor memory: O in [0, D), S/P buffers from here
-constexpr uint32_t kLCol = 128;    // row sums, where the tensor cores make them
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kOutBytes = 8 * 2048;
 
@@ -70,10 +69,16 @@ constexpr int kThreads = INT8 ? 512 : 384;
 __host__ __device__ constexpr int keys_per_tile(int d, int ctas) { return ctas == 2 ? 128 : 64 * (256 / d); }
 
 // Whether the tensor cores add up the rows' weights, as a product with ones
-// beside O.  Where tensor memory has columns for it (D = 128): the additions and
+// beside O (int8 rows: with the reciprocals of the value scales, each as the
+// sum of two bf16), where tensor memory has columns for it.  The additions and
 // the unpacking of the rounded weights were a third of the softmax warps'
-// exponential loop.  int8 rows' sums have the scales' reciprocals as factors.
-__host__ __device__ constexpr bool row_sums(int d, bool int8) { return d == 128 && !int8; }
+// exponential loop: 2048 tokens at 65536 keys of 128 dims took 289 us, now 257;
+// int8 rows at 16384 keys 397, now 363, single tokens 129.7, now 127.2 (64
+// requests, 256 dims).  Single bf16 tokens of 256 dims wait for memory and
+// gained nothing (170.5 against 172), so theirs are added up by the warps.
+__host__ __device__ constexpr bool row_sums(int d, int ctas, bool int8) { return d == 128 || (ctas == 1 && int8); }
+// Their first column: beside O, or beside the 64 keys' logits of single CTAs.
+__host__ __device__ constexpr uint32_t sum_col(int d) { return d == 128 ? 128 : kSCol + 64; }
 
 struct Piece {
   int tok0, toks;     // first token, tokens of the whole tile
@@ -131,10 +136,17 @@ struct alignas(16) Aux {
   int abort;
 };
 
+template <int KT>
 struct alignas(16) Aux8 {  // int8 rows only
   uint64_t st_full[kMaxStaging], st_empty[kMaxStaging];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
-  alignas(16) float ks[kScaleRing][kRows], vs[kScaleRing][kRows], rs[kScaleRing][kRows];  // rs: 1 / vs
+  alignas(16) float ks[kScaleRing][KT], vs[kScaleRing][KT];
+  union {  // 1 / vs
+    float rs[kScaleRing][KT];
+    // for the sums' products: of every eight keys eight rows of 16 bytes, row 0
+    // the reciprocals as bf16, row 1 what is left of them, the others zero
+    alignas(16) uint16_t rsum[kScaleRing][KT * 8];
+  };
 };
 
 static_assert(kMaxStages == kMaxStaging && kScaleRing <= kPieces, "one thread sets up a barrier of each");
@@ -342,14 +354,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 
-// One column of the warp's 32 rows.
-__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
+// Two columns of the warp's 32 rows.
+__device__ __forceinline__ float2 tmem_ld2(uint32_t taddr) {
+  float2 r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\ntcgen05.wait::ld.sync.aligned;"
+               : "=f"(r.x), "=f"(r.y)
+               : "r"(taddr)
+               : "memory");
   return r;
 }
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, float2 r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "f"(r.x), "f"(r.y) : "memory");
 }
 
 // Two fp32 values in one 64-bit register.
@@ -517,7 +532,8 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   constexpr int VSUB = NSUB / CTAS;      // those of this CTA's part of V
   constexpr int STAGE = KR * D * 2;      // bytes of a K or V stage (this CTA's part)
   constexpr int THREADS = kThreads<INT8>;
-  constexpr bool SUM = row_sums(D, INT8);
+  constexpr bool SUM = row_sums(D, CTAS, INT8);
+  constexpr uint32_t LCOL = sum_col(D);
   constexpr uint32_t SBO_K = NSUB * 1024, SBO_V = VSUB * 1024;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sQ = smem_raw;  // 1024-byte aligned, as the swizzled tiles need (checked below)
@@ -525,7 +541,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   unsigned char* sI8 = sKV + a.stages * STAGE;
   unsigned char* sOut = sI8 + (INT8 ? a.staging * (STAGE / 2) : 0);  // 2 KB per softmax warp
   Aux* ax = reinterpret_cast<Aux*>(sOut + kOutBytes);
-  Aux8* a8 = reinterpret_cast<Aux8*>(ax + 1);
+  Aux8<KT>* a8 = reinterpret_cast<Aux8<KT>*>(ax + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CTAS == 1 ? 0u : tc::cluster_rank();
   // Softmax warps and widening warps: with at most 32 rows a tile, as single
@@ -556,7 +572,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     tc::bar_init(&ax->pc_empty[tid - 64], 1 + n_soft + (INT8 ? 2 + n_wide : 0));  // products, softmax, scales, widening
     if (INT8 && tid - 64 < kScaleRing) {
       tc::bar_init(&a8->sc_full[tid - 64], 1);
-      tc::bar_init(&a8->sc_empty[tid - 64], n_soft);
+      tc::bar_init(&a8->sc_empty[tid - 64], n_soft + (SUM ? 1 : 0));  // softmax, the sums' products
     }
   } else if (tid == 96) {
     tc::bar_init(&ax->q_full, rank == 0 ? CTAS : 1);  // the copy, and on the leader a note from the peer's
@@ -568,7 +584,12 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     ax->items = 0;
   }
   if (SUM) {
-    for (int i = tid; i < 256; i += THREADS) ax->ones[i] = 0x3f80u;  // 1
+    if (INT8) {
+      for (int i = tid; i < kScaleRing * KT; i += THREADS)
+        *reinterpret_cast<uint4*>(&a8->rsum[0][8 * i]) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      for (int i = tid; i < 256; i += THREADS) ax->ones[i] = 0x3f80u;  // 1
+    }
     tc::fence_async_smem();
   }
   if (tid < 128) asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1000,8 +1021,11 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     if (elect_one()) {
       constexpr uint32_t id_qk = idesc_bf16(kRows * CTAS, KT, 0), id_pv = idesc_bf16(kRows * CTAS, D, 1),
                          id_sum = idesc_bf16(kRows * CTAS, 16 * CTAS, 0);
-      // eight rows of 16 bytes side by side, without a swizzle; the steps do not matter among equal values
-      const uint64_t ones = (static_cast<uint64_t>((256 >> 4) | (1u << 14)) << 32) | desc_lo(tc::smem_addr(ax->ones), 128);
+      // K-major without a swizzle: eight rows of 16 bytes follow one another, 128
+      // bytes on come the next eight keys; int8: rows 8 on repeat the first eight
+      const uint64_t ones =
+          (static_cast<uint64_t>(((INT8 ? 0 : 256) >> 4) | (1u << 14)) << 32) |
+          desc_lo(INT8 ? tc::smem_addr(a8->rsum) : tc::smem_addr(ax->ones), 128);
       const uint32_t dQ = desc_lo(tc::smem_addr(sQ), 16), dK = desc_lo(tc::smem_addr(sKV), 16),
                      dV = desc_lo(tc::smem_addr(sKV), 1024);
       const uint32_t q_step = CTAS == 2 ? kRows * 128 >> 4 : a.q_sub >> 4;
@@ -1066,7 +1090,9 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
               if (SUM) {
 #pragma unroll
                 for (int x = 0; x < KT / 16; x++)
-                  mma_ts<CTAS>(tm + kLCol, p + 8 * x + (x >= KT / 32 ? KT / 4 : 0), ones, id_sum, j > 1 || x > 0);
+                  mma_ts<CTAS>(tm + LCOL, p + 8 * x + (x >= KT / 32 ? KT / 4 : 0),
+                               INT8 ? ones + ((t % kScaleRing * KT + x * 16) * 16 >> 4) : ones, id_sum, j > 1 || x > 0);
+                if (INT8) commit<CTAS>(&a8->sc_empty[t % kScaleRing]);
               }
               commit<CTAS>(&ax->pv_done[t & 1]);
             }
@@ -1122,8 +1148,18 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
             // it, and the values at zero.  A scale that is not finite has no reciprocal.
             const float v = vs[e] == 0.f ? 7.888609e-31f : vs[e];
             a8->vs[s][lane + 32 * e] = v;
-            a8->rs[s][lane + 32 * e] = fabsf(v) <= 65504.f ? 1.f / v : 0.f;
+            const float r = fabsf(v) <= 65504.f ? 1.f / v : 0.f;
+            if (SUM) {
+              const int key = lane + 32 * e;
+              uint16_t* to = &a8->rsum[s][(key >> 3) * 64 + (key & 7)];
+              const uint32_t hi = pack_bf16(r, 0.f) & 0xffffu;
+              to[0] = static_cast<uint16_t>(hi);
+              to[8] = static_cast<uint16_t>(pack_bf16(r - __uint_as_float(hi << 16), 0.f));
+            } else {
+              a8->rs[s][lane + 32 * e] = r;
+            }
           }
+          if (SUM) tc::fence_async_smem();
           __syncwarp();
           if (lane == 0) tc::bar_arrive(&a8->sc_full[s]);
         }
@@ -1255,8 +1291,8 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
                 tc::tmem_st32(tm + lane_base + c0, o);
               }
               if (SUM && wg == 0) {
-                const float s1 = __uint_as_float(tmem_ld1(tm + lane_base + kLCol));
-                tmem_st1(tm + lane_base + kLCol, __float_as_uint(s1 * alpha));
+                const float2 s2 = tmem_ld2(tm + lane_base + LCOL);
+                tmem_st2(tm + lane_base + LCOL, make_float2(s2.x * alpha, s2.y * alpha));
               }
             }
             l = m_ref == -INFINITY ? 0.f : l * alpha;
@@ -1282,7 +1318,6 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
               // applied add up to one: with few keys their errors cancel.
               if (INT8) {
                 const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&a8->vs[sc][wg * HC + 2 * i]);
-                const ulonglong2 rv = *reinterpret_cast<const ulonglong2*>(&a8->rs[sc][wg * HC + 2 * i]);
                 float2 w0 = f2_out(f2_mul(f2(e[0].x, e[0].y), F2{v.x}));
                 float2 w1 = f2_out(f2_mul(f2(e[1].x, e[1].y), F2{v.y}));
                 if (masked) {  // a scale that this row does not see may be anything
@@ -1293,8 +1328,11 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
                 const uint32_t p0 = pack_bf16(w0.x, w0.y), p1 = pack_bf16(w1.x, w1.y);
                 pk[y] = p0;
                 pk[y + 1] = p1;
-                ls[0] = f2_fma(f2(__uint_as_float(p0 << 16), __uint_as_float(p0 & 0xffff0000u)), F2{rv.x}, ls[0]);
-                ls[1] = f2_fma(f2(__uint_as_float(p1 << 16), __uint_as_float(p1 & 0xffff0000u)), F2{rv.y}, ls[1]);
+                if (!SUM) {
+                  const ulonglong2 rv = *reinterpret_cast<const ulonglong2*>(&a8->rs[sc][wg * HC + 2 * i]);
+                  ls[0] = f2_fma(f2(__uint_as_float(p0 << 16), __uint_as_float(p0 & 0xffff0000u)), F2{rv.x}, ls[0]);
+                  ls[1] = f2_fma(f2(__uint_as_float(p1 << 16), __uint_as_float(p1 & 0xffff0000u)), F2{rv.y}, ls[1]);
+                }
               } else {
 #pragma unroll
                 for (int z = 0; z < 2; z++) {
@@ -1374,7 +1412,10 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       // ---- output: this group's half of the columns ----
       if (warp_live) {
         const bool whole = pc.slot < 0;
-        if (SUM && pc.n > 0) l = __uint_as_float(tmem_ld1(tm + lane_base + kLCol));
+        if (SUM && pc.n > 0) {
+          const float2 s2 = tmem_ld2(tm + lane_base + LCOL);
+          l = INT8 ? s2.x + s2.y : s2.x;
+        }
         const float inv = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
         const bool dirty = !INT8 && *reinterpret_cast<volatile int*>(&ax->dirty) != 0;
         const int64_t tok = static_cast<int64_t>(pc.tok0) + tok_i;
@@ -1868,7 +1909,7 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
   a.thin = int8 && ctas == 1 && q_toks * G <= 32;
   a.q_sub = ctas == 2 ? kRows * 128 : (a.q_box + 1023) / 1024 * 1024;
   a.q_bytes = a.q_sub * (d / 64);
-  const int aux = static_cast<int>(sizeof(Aux)) + (int8 ? static_cast<int>(sizeof(Aux8)) : 0);
+  const int aux = static_cast<int>(sizeof(Aux)) + (!int8 ? 0 : static_cast<int>(keys_per_tile(d, ctas) == 64 ? sizeof(Aux8<64>) : sizeof(Aux8<128>)));
   const int room = kMaxSmem - kOutBytes - aux - a.q_bytes;
   if (int8) {
     a.stages = ctas == 2 ? 3 : 4;
