@@ -1763,6 +1763,44 @@ Layout layout(int n_tok, int G, int d, int ctas, int sms) {
   return w;
 }
 
+// Shared memory of a CTA: the query tile (q_sub bytes per 64 columns), then as
+// many stages as fit.  int8 rows: four wide stages (pairs three, six of half
+// the size at 128 dims), the rest staging; where that would leave fewer than
+// two staging slots, as beside a full query tile of 256 dims, a wide stage
+// makes room (64 ragged requests: 3 and 6 slots 130.2 us, 4 and 4 129.3, 5 and
+// 2 156).
+struct Shared {
+  int q_bytes, stages, staging, total;
+};
+constexpr Shared shared_layout(int d, int ctas, bool int8, int q_sub) {
+  Shared s{};
+  const int stage = keys_per_tile(d, ctas) / ctas * d * 2;
+  const int aux8 = static_cast<int>(keys_per_tile(d, ctas) == 64 ? sizeof(Aux8<64>) : sizeof(Aux8<128>));
+  const int aux = static_cast<int>(sizeof(Aux)) + (int8 ? aux8 : 0);
+  s.q_bytes = q_sub * (d / 64);
+  const int room = kMaxSmem - kOutBytes - aux - s.q_bytes;
+  if (int8) {
+    s.stages = ctas == 1 ? 4 : d == 128 ? 6 : 3;
+    while (s.stages > 1 && (room - s.stages * stage) / (stage / 2) < 2) s.stages--;
+    s.staging = (room - s.stages * stage) / (stage / 2);
+    if (s.staging > kMaxStaging) s.staging = kMaxStaging;
+  } else {
+    s.stages = room / stage;
+    if (s.stages > kMaxStages) s.stages = kMaxStages;
+  }
+  s.total = s.q_bytes + s.stages * stage + s.staging * (stage / 2) + kOutBytes + aux;
+  return s;
+}
+// A full query tile leaves the least room: two keys' tiles and the values
+// between them, and int8 rows two slots to arrive in.
+constexpr bool fits(int d, int ctas, bool int8) {
+  const Shared s = shared_layout(d, ctas, int8, kRows * 128);
+  return s.stages >= 3 && (!int8 || s.staging >= 2) && s.total <= kMaxSmem;
+}
+static_assert(fits(128, 1, false) && fits(128, 2, false) && fits(256, 1, false) && fits(256, 2, false) &&
+                  fits(128, 1, true) && fits(128, 2, true) && fits(256, 1, true) && fits(256, 2, true),
+              "every kind of call has its stages");
+
 template <int D, int CTAS, bool INT8>
 int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm, int smem, int sms, cudaStream_t st) {
   static std::atomic<int> configured[kMaxDevices];
@@ -1862,7 +1900,6 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
     return SKV_ENOMEM;
   const int sms = sm_count();
   if (sms <= 1 || !encode_fn()) return SKV_ECUDA;
-  const int stage = keys_per_tile(d, ctas) / ctas * d * 2;
 
   PagedArgs a{};
   a.B = B;
@@ -1901,26 +1938,17 @@ SKV_EXPORT int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, 
   a.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.ws_o = reinterpret_cast<float*>(ws + w.o);
 
-  // Shared memory: the query rows that can hold a token (the products read
-  // 128 rows of each column block; what they read past these is never used),
-  // then as many stages as fit.
+  // The query rows that can hold a token (the products read 128 rows of each
+  // column block; what they read past these is never used).
   const int q_toks = !q_start ? 1 : n_tok < a.tpc ? n_tok : a.tpc;  // per CTA
   a.q_box = q_toks * G * 128;
   a.thin = int8 && ctas == 1 && q_toks * G <= 32;
   a.q_sub = ctas == 2 ? kRows * 128 : (a.q_box + 1023) / 1024 * 1024;
-  a.q_bytes = a.q_sub * (d / 64);
-  const int aux = static_cast<int>(sizeof(Aux)) + (!int8 ? 0 : static_cast<int>(keys_per_tile(d, ctas) == 64 ? sizeof(Aux8<64>) : sizeof(Aux8<128>)));
-  const int room = kMaxSmem - kOutBytes - aux - a.q_bytes;
-  if (int8) {
-    a.stages = ctas == 2 ? 3 : 4;
-    if (d == 128 && ctas == 2) a.stages *= 2;
-    a.staging = (room - a.stages * stage) / (stage / 2);
-    if (a.staging > kMaxStaging) a.staging = kMaxStaging;
-  } else {
-    a.stages = room / stage;
-    if (a.stages > kMaxStages) a.stages = kMaxStages;
-  }
-  const int smem = a.q_bytes + a.stages * stage + a.staging * (stage / 2) + kOutBytes + aux;
+  const Shared sh = shared_layout(d, ctas, int8, a.q_sub);
+  a.q_bytes = sh.q_bytes;
+  a.stages = sh.stages;
+  a.staging = sh.staging;
+  const int smem = sh.total;
 
   CUtensorMap km, vm, qm;
   const int block = int8 ? 128 : 64;                         // columns of a 128-byte block

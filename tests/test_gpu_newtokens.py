@@ -633,3 +633,14 @@ def test_host_tensors_are_refused(skv):
         x = {"q": c.q, "k": c.k[:1], at: q[:, :2] if at == "k" else q}
         with pytest.raises(ValueError):
             skv.norm_rope_append(x["q"], x["k"], None, c.dev[1], None, c.out, c.k, None)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,Hq,Hkv,B,n", [
+    (256, 24, 4, 8, 8), (256, 24, 4, 3, 5), (256, 16, 1, 6, 8), (256, 128, 1, 4, 1), (256, 12, 2, 3, 4), (128, 24, 4, 8, 8),
+    (128, 16, 1, 6, 8), (256, 8, 8, 2, 64),
+])
+def test_drafts_of_every_query_tile(skv, kind, d, Hq, Hkv, B, n):
+    """From a few rows to the whole query tile of a single CTA: the more it takes, the fewer slots are left for keys."""
+    rng = np.random.default_rng(40)
+    Case(skv, kind_of(skv, kind), d, Hq, Hkv, 64, [int(x) for x in rng.integers(n, 1500, B)], [n] * B, seed=40).check()
