@@ -15,8 +15,26 @@
 //   O += P V    (P from tensor memory, V from shared memory, fp32 in TMEM),
 // with S double-buffered so that the softmax of one tile runs under the
 // products of its neighbours.  m moves only when a row's maximum grows by
-// more than 2^kLazy; then the row's O is rescaled.  The row sum adds the
-// rounded weights (bf16 rows), so the weights applied sum to one.
+// more than 2^kLazy; then the row's O is rescaled.  P is bf16 because V is (or
+// widens to it exactly) and a product takes one type; the row sum adds the
+// weights as rounded, so that the weights applied sum to one.  Logits, O, m
+// and the sums are fp32.
+//
+// What bounds it, and what it measured (bf16 product rate 1916 TFLOP/s, copy
+// rate 6.79 TB/s):
+//  - chunks of 256-dim bf16 rows: the products.  2048 tokens at 65536 keys, 16
+//    heads: 1.11 ms, 1.9 PFLOP/s; 256 tokens at 262144 keys 0.60 ms.
+//  - chunks of 128 dims: the softmax warps, whose chain per 128 keys (logits
+//    from tensor memory, maximum, exponentials, weights back) takes 2.1 K clocks
+//    against 1.0 K of products: 1.17 PFLOP/s; six prompts of up to 4096 tokens
+//    250 us, 0.8 PFLOP/s with their masked tiles.
+//  - int8 chunks: the same chain with scales and, beside it, the widening:
+//    the issue slots are 58 % used.  4001 tokens in a window: 147 us.
+//  - single tokens: reading the cache.  Four requests of 131072 tokens, bf16:
+//    168 us, 94 % of the copy rate; 64 ragged int8 requests 127 us, 46 %, bound
+//    by the widening and the softmax chain.  In a window of a thousand keys
+//    (20 us) by what follows one another: launch, lengths, plan, table,
+//    keys, two products, merge.
 //
 // Long prompts run as CTA pairs (cta_group::2, CTAS = 2): 256 query rows, 128
 // keys a tile, each CTA holding half of the tile's keys (K) and half of its
@@ -28,13 +46,14 @@
 // K and V tiles are 5-dimensional TMA boxes of whole pages (or the largest
 // power-of-two part of one), laid out as [8-row group][64-column block][8 x
 // 128 B], 128-byte swizzle: one box per page brings all dims.  int8 rows
-// arrive in a staging ring and four warps widen them to bf16 (exact); the K
+// arrive in a staging ring and four warps (eight for single tokens) widen them to bf16 (exact); the K
 // scales multiply the logits, the V scales the weights.
 //
-// Work list: items (request, query tile, KV head), each cut into pieces of
-// about c key tiles; c is chosen on the device from the lengths by the cost
-// of a few candidates (plan()).  Whole items write bf16 output, pieces write
-// fp32 partials that merge_kernel joins in piece order.
+// Work list: items (request, query tile, KV head), made on the device from the
+// lengths.  Single CTAs share the batch's key tiles evenly; pairs cut items
+// into pieces of about c tiles, c by the cost of a few candidates (see the
+// plan).  Whole items write bf16 output, pieces write fp32 partials that
+// merge_kernel joins in piece order.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -367,35 +386,6 @@ __device__ __forceinline__ void tmem_st2(uint32_t taddr, float2 r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "f"(r.x), "f"(r.y) : "memory");
 }
 
-// Two fp32 values in one 64-bit register.
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2_out(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
