@@ -644,3 +644,46 @@ def test_drafts_of_every_query_tile(skv, kind, d, Hq, Hkv, B, n):
     """From a few rows to the whole query tile of a single CTA: the more it takes, the fewer slots are left for keys."""
     rng = np.random.default_rng(40)
     Case(skv, kind_of(skv, kind), d, Hq, Hkv, 64, [int(x) for x in rng.integers(n, 1500, B)], [n] * B, seed=40).check()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,lens,new", [(256, [3000, 40], [1, 1]), (128, [2000, 900], [300, 5])])
+def test_calls_back_to_back_see_each_other(skv, kind, d, lens, new):
+    """Each call's queries are the last one's output, and its rows go over those the last one read: with the calls
+    one behind the other, captured or not, as with a wait between them."""
+    c = Case(skv, kind_of(skv, kind), d, 8, 2, 16, lens, new, seed=41)
+    n = c.q.shape[0]
+    pos, inv = torch.arange(n, device="cuda", dtype=torch.int32), torch.logspace(0, -3, 32, device="cuda")
+    rows = torch.from_numpy(np.concatenate([
+        c.table[b][np.arange(t - m, t) // 16].astype(np.int64) * 16 + np.arange(t - m, t) % 16
+        for b, (t, m) in enumerate(zip(lens, new))])).cuda()
+    c.run()
+    first, pools = c.q.clone(), [x.clone() for x in (c.k, c.v)] + [None if x is None else x.clone() for x in (c.ks, c.vs)]
+    x, y = torch.empty_like(c.q), torch.empty_like(c.q)
+
+    def chain(wait):
+        x.copy_(first)
+        for dst, src in zip((c.k, c.v, c.ks, c.vs), pools):
+            if dst is not None:
+                dst.copy_(src)
+        for _ in range(6):
+            skv.norm_rope_append(x, x[:, 2:4], x[:, 4:6], pos, inv, y, c.k, c.v, kv_kind=c.kind, k_scale=c.ks,
+                                 v_scale=c.vs, out_rows=rows, status=c.st)
+            for a, b in ((y, x), (x, y), (y, x)):
+                skv.paged_attend(c.kind, a, c.k, c.v, c.dev[0], 16, c.dev[1], 1.0, b, c.ws, q_start=c.dev[2],
+                                 k_scale=c.ks, v_scale=c.vs, status=c.st)
+                if wait:
+                    torch.cuda.synchronize()
+        return x.clone()
+
+    want = chain(True)
+    assert torch.isfinite(want).all() and torch.equal(chain(False), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(False)
+    for _ in range(3):
+        x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(x, want)
+    assert int(c.st.item()) == 0
