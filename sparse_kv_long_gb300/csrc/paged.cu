@@ -1567,44 +1567,57 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
 // Joins the pieces of split items in piece order.  With few rows a block takes
 // a row, its warps every eighth piece; with many a warp takes a row.
 constexpr int kMaxPieces = 160;                     // also the most CTAs of a launch
-constexpr int kMaxItems = kSplitPerPair * kMaxPieces / 4;  // a split item has two pieces at least
 template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head, const int4* __restrict__ item,
                                                     const float2* __restrict__ ml, const float* __restrict__ o,
-                                                    int part_rows, int G, int Hq, uint16_t* __restrict__ out) {
+                                                    int listable, int part_rows, int G, int Hq,
+                                                    uint16_t* __restrict__ out) {
   constexpr int E = D / 32;  // columns per lane: float4 f at 4 (lane + 32 f)
   constexpr int Q = kMaxPieces / 32;
   __shared__ __align__(16) float red[8][D];
   __shared__ float weight[8][kMaxPieces];
-  __shared__ int items[kMaxItems], n_items;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   allow_dependent_launch();
   grid_dependency_wait();  // launched early: the partials are complete from here on
-  // Single CTAs list a split item at the CTA where it begins, so the list has gaps.
-  const int listed = min(head[0], kMaxItems), rows = head[1];
-  const bool gaps = head[2] != 0;
-  if (gaps)
-    for (int i = threadIdx.x; i < listed; i += 256) items[i] = item[2 * i + 1].x;
-  __syncthreads();
-  if (gaps && warp == 0) {  // closed up in order: every block has to see the same list
-    int n = 0;
-    for (int i = 0; i < listed; i += 32) {
-      const bool is = i + lane < listed && items[i + lane] > 0;
-      const uint32_t mask = __ballot_sync(0xffffffffu, is);
-      if (is) items[n + __popc(mask & ((1u << lane) - 1u))] = i + lane;
-      n += __popc(mask);
-      __syncwarp();
-    }
-    if (lane == 0) n_items = n;
+  // Single CTAs list a split item at the CTA where it begins, so the list has
+  // gaps: every warp closes it up for itself, in order, as masks of the used
+  // entries (its loads go out with the head's).
+  uint32_t used[Q];
+  int pieces[Q];
+#pragma unroll
+  for (int i = 0; i < Q; i++) pieces[i] = lane + 32 * i < listable ? item[2 * (lane + 32 * i) + 1].x : 0;
+  const int4 hd = *reinterpret_cast<const int4*>(head);
+  const int listed = hd.x, rows = hd.y;
+  const bool gaps = hd.z != 0;
+  int n_items = gaps ? 0 : listed;
+#pragma unroll
+  for (int i = 0; i < Q; i++) {
+    used[i] = __ballot_sync(0xffffffffu, lane + 32 * i < listed && pieces[i] > 0);
+    n_items += gaps ? __popc(used[i]) : 0;
   }
-  __syncthreads();
-  const int tasks = (gaps ? n_items : listed) * rows;
+  const int tasks = n_items * rows;
   const bool wide = tasks <= 8 * static_cast<int>(gridDim.x);  // a block per row
   const int step = wide ? gridDim.x : gridDim.x * 8, first = wide ? blockIdx.x : blockIdx.x * 8 + warp;
   const int s0 = wide ? warp : 0, ds = wide ? 8 : 1;
 #pragma unroll 1
   for (int w = first; w < tasks; w += step) {
-    const int at = w / rows, row = w - at * rows, it = gaps ? items[at] : at;
+    const int at = w / rows, row = w - at * rows;
+    int it = at;
+    if (gaps) {
+      int left = at;
+      uint32_t mask = 0;
+#pragma unroll
+      for (int i = 0; i < Q; i++) {
+        const int n = __popc(used[i]);
+        if (left >= 0 && left < n) {
+          mask = used[i];
+          it = 32 * i;
+          const bool is = (mask >> lane & 1u) && __popc(mask & ((1u << lane) - 1u)) == left;
+          it += __ffs(__ballot_sync(0xffffffffu, is)) - 1;
+        }
+        left -= n;
+      }
+    }
     const int4 x = item[2 * it], y = item[2 * it + 1];
     const int n = y.x;
     if (row >= x.y) continue;  // the same for the whole block where it takes a row
@@ -1818,11 +1831,12 @@ int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, con
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
+  const int listable = a.max_split < kMaxPieces ? a.max_split : kMaxPieces;
   const int* head = a.ws_head;
   const int4* item = a.ws_item;
   const float2* ml = a.ws_ml;
   const float* o = a.ws_o;
-  if (cudaLaunchKernelEx(&cfg, merge_kernel<D>, head, item, ml, o, a.part_rows, a.G, a.Hkv * a.G, a.out) !=
+  if (cudaLaunchKernelEx(&cfg, merge_kernel<D>, head, item, ml, o, listable, a.part_rows, a.G, a.Hkv * a.G, a.out) !=
       cudaSuccess) {
     cudaGetLastError();
     return SKV_ECUDA;
