@@ -27,12 +27,12 @@
 // Bound: memory, then instruction issue (about 60 per head and warp): every
 // value is read once and written once; d / 8 lanes share a head, so a head's
 // sum is a shuffle reduction and no value passes through shared memory.  A
-// warp takes a token's heads one after the other, four in flight, and
+// warp takes a token's heads one after the other, a few in flight, and
 // computes the token's sines once; with few tokens a token's heads are spread
 // over several warps instead (launch rule below).  Measured (copy rate 6.79
-// TB/s): 2048 tokens of 16 + 2 + 2 heads, 256 dims, 10.3 us (4.1 TB/s); 5237 of
-// 32 + 8 + 8, 128 dims, pairs neighbours, 22.1 us (5.8 TB/s); 32768 of 24 + 4 + 4
-// int8, 256 dims, 209 us (4.8 TB/s, 59 % of the issue slots); 8 tokens 3.6 us.
+// TB/s): 2048 tokens of 16 + 2 + 2 heads, 256 dims, 9.9 us (4.2 TB/s); 5237 of
+// 32 + 8 + 8, 128 dims, pairs neighbours, 22.0 us (5.8 TB/s); 32768 of 24 + 4 + 4
+// int8, 256 dims, 205 us (4.9 TB/s, 59 % of the issue slots); 8 tokens 3.6 us.
 #include "common.cuh"
 
 namespace skv {
@@ -40,8 +40,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+// 64 registers a thread.  32768 int8 tokens of 256 dims / 5237 bf16 tokens of
+// 128 took 219 / 23.0 us with three CTAs, 208 / 22.0 with four, 284 / 26.2
+// (spills) with five.
 constexpr int kCtasPerSm = 4;
-constexpr int kBatch = 4;  // heads per lane group whose loads are in flight together
+// Heads per lane group whose loads are in flight together.  The same two: two
+// heads 205 / 25.1 us, four 208 / 22.0, six 225 / 23.7; 2048 bf16 tokens of 256
+// dims: two 9.9, four 10.4.
+template <int D>
+constexpr int kBatch = D == 256 ? 2 : 4;
 
 struct NormArgs {
   int64_t n_tok;
@@ -159,10 +166,10 @@ __device__ __forceinline__ void run_heads(const NormArgs& a, int64_t tok, int64_
   const uint16_t* src = KIND == kQ ? a.q + tok * a.q_stride
                                    : KIND == kK ? a.k + tok * a.k_stride : a.v + tok * a.v_stride;
   const bool normed = KIND == kQ ? a.q_weight != nullptr : a.k_weight != nullptr;
-  for (int s0 = lo; s0 < hi; s0 += kBatch) {
-    Vals raw[kBatch];
+  for (int s0 = lo; s0 < hi; s0 += kBatch<D>) {
+    Vals raw[kBatch<D>];
 #pragma unroll
-    for (int u = 0; u < kBatch; u++) {  // every load of the batch first
+    for (int u = 0; u < kBatch<D>; u++) {  // every load of the batch first
       const int h = (s0 + u) * HPW + grp;
       raw[u] = Vals{{0u, 0u, 0u, 0u}};
       if (s0 + u < hi && (HPW == 1 || h < H)) {
@@ -171,7 +178,7 @@ __device__ __forceinline__ void run_heads(const NormArgs& a, int64_t tok, int64_
       }
     }
 #pragma unroll
-    for (int u = 0; u < kBatch; u++) {
+    for (int u = 0; u < kBatch<D>; u++) {
       if (s0 + u >= hi) break;
       const int h = (s0 + u) * HPW + grp;
       const bool live = HPW == 1 || h < H;
