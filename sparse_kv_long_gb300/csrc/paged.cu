@@ -69,8 +69,12 @@ constexpr int kPieces = 4;         // piece descriptors in flight
 constexpr int kTileInfo = 16;      // tiles whose page validity is kept (more than the ring holds)
 constexpr int kScaleRing = 4;      // tiles whose int8 scales are kept
 constexpr int kCand = 64;          // split candidates (pairs)
-constexpr int kItem = 3;           // tiles that filling and draining a piece's pipeline is worth (single CTAs)
-constexpr int kMinStretch = 4;     // tiles a CTA gets at least
+// Single CTAs.  Tiles that filling and draining a piece's pipeline is worth: 16
+// drafts / 64 ragged requests took 64.8 / 133 us with 1, 52.5 / 128 with 3,
+// 52.5 / 133 with 5, 52.0 / 139 with 8.  Tiles a CTA gets at least: eight tokens
+// in a window of a thousand keys 19.5 us with 2 and 4, 22.7 with 8.
+constexpr int kItem = 3;
+constexpr int kMinStretch = 4;
 constexpr float kLazy = 8.f;       // log2 units a maximum may grow before O is rescaled
 constexpr int kSplitPerPair = 8;   // pieces that write partials, per pair (single CTAs: two each)
 constexpr uint32_t kGone = 0x7fc0dead;  // a NaN that no arithmetic gives
@@ -1414,7 +1418,9 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         const int id = !live ? -1 : whole ? static_cast<int>(tok * (a.Hkv * a.G)) + pc.h * a.G + head_r : static_cast<int>(prow);
         char* base = whole ? reinterpret_cast<char*>(a.out) : reinterpret_cast<char*>(a.ws_o);
         const int pitch = whole ? 2 * D : 4 * D;
-        const bool few = __popc(__ballot_sync(0xffffffffu, live)) <= 8;  // each lane writes its own row
+        // With a few rows each lane writes its own (a window's single tokens 19.7 ->
+        // 19.3 us; with 32 rows that took 4 to 7 % of a chunk).
+        const bool few = CTAS == 1 && __popc(__ballot_sync(0xffffffffu, live)) <= 8;
         char* to[4];
 #pragma unroll
         for (int x = 0; x < 4; x++) {
@@ -1850,7 +1856,11 @@ int launch_kind(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm
   return int8 ? launch<D, CTAS, true>(a, km, vm, qm, smem, sms, st) : launch<D, CTAS, false>(a, km, vm, qm, smem, sms, st);
 }
 
-// CTA pairs from about two query tiles of rows per request on.
+// CTA pairs where requests have more rows than a single CTA's query tile, which
+// would read the cache twice.  Eight requests of 30000 tokens, rows 128 / 192
+// each, single against pairs: bf16 of 256 dims 127 / 185 us against 126 / 119,
+// int8 136 / 205 against 165 / 157; of 128 dims 90 / 112 against 106 / 96, int8
+// 100 / 134 against 134 / 123.
 int ctas_for(int B, int n_tok, int G, bool single) {
   return !single && static_cast<int64_t>(n_tok) * G > static_cast<int64_t>(B) * kRows ? 2 : 1;
 }
