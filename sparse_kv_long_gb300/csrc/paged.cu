@@ -23,17 +23,17 @@
 // What bounds it, and what it measured (bf16 product rate 1916 TFLOP/s, copy
 // rate 6.79 TB/s):
 //  - chunks of 256-dim bf16 rows: the products.  2048 tokens at 65536 keys, 16
-//    heads: 1.11 ms, 1.9 PFLOP/s; 256 tokens at 262144 keys 0.60 ms.
+//    heads: 1.09 ms, 1.9 PFLOP/s and more; 256 tokens at 262144 keys 0.58 ms.
 //  - chunks of 128 dims: the softmax warps, whose chain per 128 keys (logits
 //    from tensor memory, maximum, exponentials, weights back) takes 2.1 K clocks
 //    against 1.0 K of products: 1.17 PFLOP/s; six prompts of up to 4096 tokens
-//    250 us, 0.8 PFLOP/s with their masked tiles.
+//    247 us, 0.8 PFLOP/s with their masked tiles.
 //  - int8 chunks: the same chain with scales and, beside it, the widening:
-//    the issue slots are 58 % used.  4001 tokens in a window: 147 us.
+//    the issue slots are 58 % used.  4001 tokens in a window: 140 us.
 //  - single tokens: reading the cache.  Four requests of 131072 tokens, bf16:
-//    168 us, 94 % of the copy rate; 64 ragged int8 requests 127 us, 46 %, bound
+//    168 us, 94 % of the copy rate; 64 ragged int8 requests 122 us, 48 %, bound
 //    by the widening and the softmax chain.  In a window of a thousand keys
-//    (20 us) by what follows one another: launch, lengths, plan, table,
+//    (19.4 us) by what follows one another: launch, lengths, plan, table,
 //    keys, two products, merge.
 //
 // Long prompts run as CTA pairs (cta_group::2, CTAS = 2): 256 query rows, 128
@@ -1657,7 +1657,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; e++) acc[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = s0; s < n; s += ds) {
       const float f = weight[warp][s];
       if (f == 0.f) continue;
@@ -1836,7 +1836,9 @@ int launch(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, con
     cudaGetLastError();
     return SKV_ECUDA;
   }
-  cfg.gridDim = dim3(2 * sms, 1, 1);
+  // Four blocks per SM: 64 ragged int8 requests 127.2 us with two, 122.4 with
+  // four, 124.0 with six; 256 tokens at 262144 keys 587, 576, 576.
+  cfg.gridDim = dim3(4 * sms, 1, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
