@@ -1583,7 +1583,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head
   __shared__ __align__(16) float red[8][D];
   __shared__ float weight[8][kMaxPieces];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  allow_dependent_launch();
+  // It lets nothing start early in its turn: kernels that read before they wait
+  // count on everything but the kernel just before them being complete.
   grid_dependency_wait();  // launched early: the partials are complete from here on
   // Single CTAs list a split item at the CTA where it begins, so the list has
   // gaps: every warp closes it up for itself, in order, as masks of the used
