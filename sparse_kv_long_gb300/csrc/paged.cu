@@ -31,7 +31,7 @@
 //  - int8 chunks: the same chain with scales and, beside it, the widening:
 //    the issue slots are 58 % used.  4001 tokens in a window: 140 us.
 //  - single tokens: reading the cache.  Four requests of 131072 tokens, bf16:
-//    168 us, 94 % of the copy rate; 64 ragged int8 requests 122 us, 48 %, bound
+//    168 us, 94 % of the copy rate; 64 ragged int8 requests 118 us, 50 %, bound
 //    by the widening and the softmax chain.  In a window of a thousand keys
 //    (19.4 us) by what follows one another: launch, lengths, plan, table,
 //    keys, two products, merge.

@@ -687,3 +687,41 @@ def test_calls_back_to_back_see_each_other(skv, kind, d, lens, new):
         torch.cuda.synchronize()
         assert torch.equal(x, want)
     assert int(c.st.item()) == 0
+
+
+def test_sparse_calls_behind_dense_ones(skv):
+    """A sparse layer's attention on queries that came two dense calls before it, over rows just appended: queued
+    without a wait between the calls as with one."""
+    B, Hq, Hkv, d, page, t = 4, 16, 2, 256, 64, 5000
+    c = Case(skv, skv.KV_BF16, d, Hq, Hkv, page, [t] * B, [1] * B, seed=42)
+    other = Case(skv, skv.KV_BF16, d, Hq, Hkv, page, [t], [200], seed=43)
+    c.run(), other.run()
+    r = np.stack([c.table[b][np.arange(t - 300, t) // page] * page + np.arange(t - 300, t) % page for b in range(B)])
+    rows, count = T.dev(r.astype(np.int32)), T.dev(np.full(B, 300, np.int32))
+    last = torch.from_numpy(r[:, -1].astype(np.int64)).cuda()
+    ws = torch.zeros((skv.attend_workspace_size(B, Hq, Hkv, d, 300),), dtype=torch.uint8, device="cuda")
+    x, y = c.q.clone(), torch.zeros_like(c.q)
+    out = torch.zeros((B, Hq, d), dtype=torch.float32, device="cuda")
+    pos, inv = torch.arange(B, device="cuda", dtype=torch.int32), torch.logspace(0, -3, 32, device="cuda")
+    pools = c.k.clone(), c.v.clone()
+
+    def steps(wait):
+        x.copy_(c.q), c.k.copy_(pools[0]), c.v.copy_(pools[1])
+        got = []
+        for _ in range(8):
+            for call in (
+                    lambda: skv.norm_rope_append(x, x[:, :2], x[:, 2:4], pos, inv, y, c.k, c.v, out_rows=last),
+                    lambda: skv.paged_attend(c.kind, y, c.k, c.v, c.dev[0], page, c.dev[1], 0.1, x, c.ws, status=c.st),
+                    lambda: other.call(),
+                    lambda: skv.sparse_attend_decode(c.kind, x, c.k, c.v, rows, count, 0.1, out, ws, Hkv, status=c.st),
+                    lambda: got.append(out.clone())):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        return torch.stack(got)
+
+    want = steps(True)
+    assert torch.isfinite(want).all()
+    for _ in range(5):
+        assert torch.equal(steps(False), want)
+    assert int(c.st.item()) == 0
