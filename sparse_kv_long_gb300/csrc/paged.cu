@@ -600,8 +600,8 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   __syncthreads();
   tc::tc_fence_after();
   // Launched early, too: barriers and tensor memory are set up while the
-  // previous kernel ends (windowed single tokens, calls back to back: see the
-  // launch); from here on what it wrote is there.
+  // previous kernel ends (eight tokens in a window 19.5 -> 19.2 us); from here on
+  // what it wrote is there.
   grid_dependency_wait();
 
   // ---- plan ------------------------------------------------------------------------
