@@ -252,12 +252,16 @@ __device__ __forceinline__ uint32_t leader_addr(uint64_t* bar) {
 // another role has; sets *abort and returns false.  Half a dozen waits
 // follow one another per tile, so this is as short as it can be: a clock in
 // the loop, a call, or one lane asking for the warp each cost 5 to 20 % of a
-// whole call.
-constexpr uint32_t kSpins = 4000000u;
+// whole call.  Built with another SKV_PAGED_LOOKS (0: waits give up at once),
+// the tests take the paths behind a wait that has given up.
+#ifndef SKV_PAGED_LOOKS
+#define SKV_PAGED_LOOKS 4000000
+#endif
+constexpr uint32_t kSpins = SKV_PAGED_LOOKS;
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   if (tc::bar_test(bar, parity, false)) return true;
 #pragma unroll 1
-  for (uint32_t it = 0; it < kSpins; it++) {
+  for (uint32_t it = 0; it != kSpins; it++) {
     if (tc::bar_test(bar, parity, false)) return true;
     if ((it & 255) == 255 && *abort) return false;
   }
@@ -972,11 +976,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         }
       }
     }
-    if (!ok) {  // gave up: let the copies in flight land before the CTA leaves
-      if (lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
-      const uint64_t t0 = tc::global_ns();
-      for (int i = 0; i < 1000000 && tc::global_ns() - t0 < 20000000ull; i++) __nanosleep(1000);
-    }
+    if (!ok && lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
     // split items of this call, for the merge
     if (CTAS == 1) {
       if (!listed && lane == 0) a.ws_item[2 * unit + 1] = make_int4(0, 0, 0, 0);
@@ -1560,6 +1560,15 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     tc::cluster_sync();  // no CTA leaves while its peer may still signal it
   else
     __syncthreads();
+  // Whichever role gave up, copies that none has waited for may be in flight,
+  // also where the copying warp had issued its last: they land before the CTA
+  // leaves.  (Where none gave up, each has been waited for by who used it: the
+  // products, the peer's notes to the leader or the widening warps.)
+  if (warp == 0 && *abort) {
+    const uint64_t t0 = tc::global_ns();
+    for (int i = 0; i < 1000000 && tc::global_ns() - t0 < 20000000ull; i++) __nanosleep(1000);
+    __syncwarp();
+  }
   if (warp == 1) {
     tc::tc_fence_after();
     if (CTAS == 1)
