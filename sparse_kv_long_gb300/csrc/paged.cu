@@ -817,8 +817,11 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     constexpr int SLOT = INT8 ? STAGE / 2 : STAGE;
     uint32_t uses = 0, tile_no = 0, qn = 0;  // copies, tiles, query tiles so far
     bool ok = true;
+    // A warp that has given up walks on without copies: the merge reads the
+    // descriptor of every split item, and one that this call did not write
+    // would be an earlier call's, or no descriptor at all.
 #pragma unroll 1
-    for (int k = 0; ok; k++) {
+    for (int k = 0;; k++) {
       Piece pc;
       pc.last = 1;
       pc.n = 0;
@@ -918,12 +921,13 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         pc.slot = -1;
       }
       const int slot = k % kPieces;
-      if (k >= kPieces && !(ok = wait_all(&ax->pc_empty[slot], ((k / kPieces) - 1) & 1, abort))) break;
-      if (lane == 0) {
+      if (ok && k >= kPieces) ok = wait_all(&ax->pc_empty[slot], ((k / kPieces) - 1) & 1, abort);
+      if (ok && lane == 0) {
         ax->pc[slot] = pc;
         tc::bar_arrive(&ax->pc_full[slot]);
       }
       if (pc.last) break;
+      if (!ok) continue;
       // Copies, in the order the products take them.  Lane i holds the box of
       // rows [i rb, i rb + rb) of a tile; table entries are read two tiles ahead.
       const int p_hi = pc.pos0 + pc.toks - 1;  // keys past it are not copied

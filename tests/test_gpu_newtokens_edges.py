@@ -58,3 +58,11 @@ def gives_up(skv, hasty, monkeypatch, c, single):  # noqa: F811
 def test_single_ctas_that_give_up(skv, hasty, monkeypatch, kind, d, lens, new, single):  # noqa: F811
     c = Case(skv, kind_of(skv, kind), d, 8, 2, 16, lens, new, seed=50, pad=0 if single else 3)
     gives_up(skv, hasty, monkeypatch, c, single)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,lens,new", [(256, [30000], [700]), (128, [9000, 12000], [300, 300]), (256, [5000, 300], [2000, 250])])
+def test_pairs_that_give_up(skv, hasty, monkeypatch, kind, d, lens, new):  # noqa: F811
+    """Requests cut into pieces whose descriptors other pairs write: given up on, they are this call's all the same."""
+    c = Case(skv, kind_of(skv, kind), d, 8, 2, 64, lens, new, seed=51, pad=3)
+    gives_up(skv, hasty, monkeypatch, c, False)
