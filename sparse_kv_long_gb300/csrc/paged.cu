@@ -1584,13 +1584,13 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
 }
 
 // Joins the pieces of split items in piece order.  With few rows a block takes
-// a row, its warps every eighth piece; with many a warp takes a row.
+// a row, its warps every eighth piece; with many a warp takes a row.  It is
+// launched while the attention still writes what it reads, so none of that is
+// declared read-only or unaliased: such loads could be moved ahead of the wait.
 constexpr int kMaxPieces = 160;                     // also the most CTAs of a launch
 template <int D>
-__global__ void __launch_bounds__(256) merge_kernel(const int* __restrict__ head, const int4* __restrict__ item,
-                                                    const float2* __restrict__ ml, const float* __restrict__ o,
-                                                    int listable, int part_rows, int G, int Hq,
-                                                    uint16_t* __restrict__ out) {
+__global__ void __launch_bounds__(256) merge_kernel(const int* head, const int4* item, const float2* ml, const float* o,
+                                                    int listable, int part_rows, int G, int Hq, uint16_t* out) {
   constexpr int E = D / 32;  // columns per lane: float4 f at 4 (lane + 32 f)
   constexpr int Q = kMaxPieces / 32;
   __shared__ __align__(16) float red[8][D];

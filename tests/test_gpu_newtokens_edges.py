@@ -66,3 +66,29 @@ def test_pairs_that_give_up(skv, hasty, monkeypatch, kind, d, lens, new):  # noq
     """Requests cut into pieces whose descriptors other pairs write: given up on, they are this call's all the same."""
     c = Case(skv, kind_of(skv, kind), d, 8, 2, 64, lens, new, seed=51, pad=3)
     gives_up(skv, hasty, monkeypatch, c, False)
+
+
+# ---------------------------------------------------------------------------
+# the merge
+# ---------------------------------------------------------------------------
+
+def test_changing_calls_queued_on_one_workspace(skv):  # noqa: F811
+    """Calls whose lists of split items and partials differ, one behind the other on a workspace without a wait: the
+    merge, launched while the attention runs, reads this call's."""
+    cases = [Case(skv, kind_of(skv, k), d, 8, 2, 16, lens, new, seed=60 + i) for i, (k, d, lens, new) in enumerate([
+        ("bf16", 256, [9000], [1]), ("int8", 256, [700, 5000, 3], [2, 3, 1]), ("bf16", 128, [6000], [400]),
+        ("bf16", 256, [4000, 100, 2500], [1, 1, 1]), ("int8", 128, [8000], [200])])]
+    need = max(skv.paged_attend_workspace_size(len(c.lens), c.q.shape[0], 8, 2, c.d) for c in cases)
+    ws = torch.zeros((need,), dtype=torch.uint8, device="cuda")
+    want = []
+    for c in cases:
+        want.append(c.run(ws=ws).clone())
+        torch.cuda.synchronize()
+    for _ in range(20):
+        for c in cases:
+            c.out.zero_()
+        for c in cases + cases[::-1]:
+            c.call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(c.out, w) for c, w in zip(cases, want))
+    assert all(int(c.st.item()) == 0 for c in cases)
