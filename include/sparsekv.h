@@ -792,7 +792,9 @@ int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int rot, int int
  *   q_start  int32 [B+1], ascending (a request may have no token), or NULL:
  *            one token per request (n_tok == B).  Tokens before q_start[0] and
  *            from q_start[B] on are padding: their output is left as it was.
- *            A q_start that descends or leaves [0, n_tok] sets SKV_DEV_RANGE
+ *            A request whose offsets descend or leave [0, n_tok], or that has a
+ *            token of an earlier request, is skipped (its output is left as it
+ *            was) and sets SKV_DEV_RANGE
  *   out      bf16 [n_tok][Hq][d]
  *   workspace  skv_paged_attend_workspace_size(...) bytes; nothing in it
  *            outlasts a call, so calls of any sizes may follow one another on

@@ -153,6 +153,7 @@ struct alignas(16) Aux {
     float x[2][2][kRows];  // [exchange parity][group][row]: maxima of a tile, at a piece's end sums
   };
   int nmax, items;
+  int disorder;  // some request's offsets descend or leave [0, n_tok]
   uint32_t tmem_base;
   alignas(16) uint16_t ones[256];  // 16 rows of 16 ones
   int dirty;  // a value that only some queries of a tile see was not finite
@@ -199,15 +200,35 @@ __device__ __forceinline__ void tile_range(const PagedArgs& a, const Req& r, int
   n = nsink + max(0, p_hi / KT - lo + 1);
 }
 
+// Whether an earlier request has tokens past the first of request b; only
+// possible where some request's offsets are not in order.
+__device__ __noinline__ bool taken(const int32_t* q_start, int n_tok, int b, int first) {
+  bool hit = false;
+#pragma unroll 1
+  for (int i = 0, s = q_start[0]; i < b; i++) {
+    const int e = q_start[i + 1];
+    hit |= s >= 0 && e > s && e <= n_tok && e > first;
+    s = e;
+  }
+  return hit;
+}
+
+// A request whose offsets are not in order, or (looked for once *disorder is
+// known) whose tokens an earlier one has, has none: the requests left are
+// disjoint, so none writes another's rows and 32 bits count their work.
 template <int KT>
-__device__ __noinline__ Req request(const PagedArgs& a, int b, bool report) {
+__device__ __noinline__ Req request(const PagedArgs& a, int b, bool report, int* disorder, bool known) {
   Req r;
   if (b >= a.B) return Req{0, 0, 0, 0, 0};
   r.T = max(0, a.lengths[b]);
   if (a.q_start) {
     const int s = a.q_start[b], e = a.q_start[b + 1];
-    const bool bad = s < 0 || e < s || e > a.n_tok;
-    if (bad && report) set_status(a.status, SKV_DEV_RANGE);
+    bool bad = s < 0 || e < s || e > a.n_tok;
+    if (bad) {
+      *disorder = 1;  // (every writer's value)
+      if (report) set_status(a.status, SKV_DEV_RANGE);
+    }
+    if (known && !bad && e > s && *disorder) bad = taken(a.q_start, a.n_tok, b, s);
     r.start = s;
     r.nq = bad ? 0 : e - s;
   } else {
@@ -578,6 +599,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     tc::bar_init(&ax->mma_idle, 1);
     ax->abort = (tc::smem_addr(smem_raw) & 1023u) != 0;  // every wait would give up at once
     ax->dirty = 0;
+    ax->disorder = 0;
     ax->nmax = 0;
     ax->items = 0;
   }
@@ -629,24 +651,34 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   int split_c = 1, split_from = 0;
   int total = 0, n_used = n_units;  // single CTAs: the row's length, the CTAs that share it
   Req mine{0, 0, 0, 0, 0};          // warp 0: the first 32 requests
-  if (CTAS == 1) {
-    int sum = 0, rows = 0;
-#pragma unroll 1
-    for (int b = tid; b < a.B; b += THREADS) {
-      const Req r = request<KT>(a, b, unit == 0);
-      if (b < 32) mine = r;
-      sum += r.nqt * a.Hkv * (r.ntmax + kItem);
-      rows = max(rows, min(a.tpt, r.nq) * a.G);
-    }
-    if (warp * 32 < a.B) {
-      sum = __reduce_add_sync(0xffffffffu, sum);
-      rows = __reduce_max_sync(0xffffffffu, rows);
-      if (lane == 0 && sum > 0) {
-        atomicAdd(&ax->items, sum);
-        atomicMax(&ax->nmax, rows);
-      }
-    }
+  auto again = [&]() {  // offsets out of order: the batch is gone through again, without the requests that overlap
     __syncthreads();
+    if (tid == 0) ax->nmax = ax->items = 0;
+    __syncthreads();
+  };
+  if (CTAS == 1) {
+#pragma unroll 1
+    for (bool known = false;; known = true) {
+      int sum = 0, rows = 0;
+#pragma unroll 1
+      for (int b = tid; b < a.B; b += THREADS) {
+        const Req r = request<KT>(a, b, unit == 0, &ax->disorder, known);
+        if (b < 32) mine = r;
+        sum += r.nqt * a.Hkv * (r.ntmax + kItem);
+        rows = max(rows, min(a.tpt, r.nq) * a.G);
+      }
+      if (warp * 32 < a.B) {
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        rows = __reduce_max_sync(0xffffffffu, rows);
+        if (lane == 0 && sum > 0) {
+          atomicAdd(&ax->items, sum);
+          atomicMax(&ax->nmax, rows);
+        }
+      }
+      __syncthreads();
+      if (known || !ax->disorder) break;
+      again();
+    }
     total = ax->items;
     n_used = min(n_units, max(1, total / kMinStretch));
     if (tid == 0 && unit == 0) {
@@ -658,26 +690,30 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     constexpr float kOvh = 3.f, kJoin = 3.f;
     constexpr int NW = THREADS / 32;
     int2* req = reinterpret_cast<int2*>(sKV);  // (query tiles, key tiles of the longest)
-    int nmax = 0, items = 0;
 #pragma unroll 1
-    for (int b = tid; b < a.B; b += THREADS) {
-      const Req r = request<KT>(a, b, unit == 0 && rank == 0);
-      if (b < 32) mine = r;
-      req[b] = make_int2(r.nqt, r.ntmax);
-      nmax = max(nmax, r.ntmax);
-      items += r.nqt;
-    }
-    if (warp * 32 < a.B) {
-      nmax = __reduce_max_sync(0xffffffffu, nmax);
-      items = __reduce_add_sync(0xffffffffu, items);
-      if (lane == 0 && items > 0) {
-        atomicMax(&ax->nmax, nmax);
-        atomicAdd(&ax->items, items);
+    for (bool known = false;; known = true) {
+      int longest = 0, tiles = 0;
+#pragma unroll 1
+      for (int b = tid; b < a.B; b += THREADS) {
+        const Req r = request<KT>(a, b, unit == 0 && rank == 0, &ax->disorder, known);
+        if (b < 32) mine = r;
+        req[b] = make_int2(r.nqt, r.ntmax);
+        longest = max(longest, r.ntmax);
+        tiles += r.nqt;
       }
+      if (warp * 32 < a.B) {
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        tiles = __reduce_add_sync(0xffffffffu, tiles);
+        if (lane == 0 && tiles > 0) {
+          atomicMax(&ax->nmax, longest);
+          atomicAdd(&ax->items, tiles);
+        }
+      }
+      __syncthreads();
+      if (known || !ax->disorder) break;
+      again();
     }
-    __syncthreads();
-    nmax = ax->nmax;
-    items = ax->items * a.Hkv;
+    const int nmax = ax->nmax, items = ax->items * a.Hkv;
     // Items kept whole in the second half of the candidates: the full rounds,
     // in the work list's order; only a batch that one warp holds is looked at
     // this way.
@@ -840,7 +876,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
           sbase += __shfl_sync(full, ss, 31);
           seen += __shfl_sync(full, tt, 31);
           b32 += 32;
-          r = request<KT>(a, b32 + lane, false);
+          r = request<KT>(a, b32 + lane, false, &ax->disorder, true);
           scan();
         }
         if (b32 >= a.B) break;
@@ -988,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       int cut = 0, before = 0, rows = 0;
 #pragma unroll 1
       for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const Req x = request<KT>(a, b0 + lane, false);
+        const Req x = request<KT>(a, b0 + lane, false, &ax->disorder, true);
         const int items = x.nqt * a.Hkv;
         int sum = items;
 #pragma unroll 1

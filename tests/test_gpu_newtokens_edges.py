@@ -6,10 +6,12 @@ import os
 import subprocess
 import types
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_newtokens import KINDS, Case, kind_of, skv  # noqa: F401  (skv is a fixture)
+from oracle import newtokens as plain
+from test_gpu_newtokens import KINDS, Case, f64, gen, kind_of, skv, status  # noqa: F401  (skv is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +94,69 @@ def test_changing_calls_queued_on_one_workspace(skv):  # noqa: F811
         torch.cuda.synchronize()
         assert all(torch.equal(c.out, w) for c, w in zip(cases, want))
     assert all(int(c.st.item()) == 0 for c in cases)
+
+
+# ---------------------------------------------------------------------------
+# offsets out of order
+# ---------------------------------------------------------------------------
+
+def kept(starts, n):
+    """Requests that remain: offsets in order and within [0, n], and no token that such a request before them has."""
+    good = [0 <= s <= e <= n for s, e in zip(starts, starts[1:])]
+    return [b for b in range(len(good)) if good[b] and not any(
+        good[i] and starts[i + 1] > starts[i] and starts[i + 1] > starts[b] for i in range(b))]
+
+
+def bad_offsets(skv, kind, d, page, lens, starts, n):  # noqa: F811
+    c = Case(skv, kind, d, 8, 2, page, lens, [0] * len(lens), seed=70, pad=n)
+    c.starts = np.array(starts, np.int32)
+    c.run()  # lays the device tensors out; once more into the middle of a larger output
+    wide = torch.full((n + 64, 8, d), 123.0, dtype=torch.bfloat16, device="cuda")
+    c.out = wide[32:32 + n]
+    c.st.zero_()
+    c.call()
+    keep, owned = kept(starts, n), torch.zeros(n + 64, dtype=torch.bool, device="cuda")
+    assert int(c.st.item()) == (0 if len(keep) == len(lens) else skv.DEV_RANGE)
+    k, v = c.values()
+    for b in keep:
+        s, e = starts[b], starts[b + 1]
+        owned[32 + s:32 + e] = True
+        ref, spread = plain.paged_attend(f64(c.q)[s:e], k, v, c.table[b:b + 1], page, [lens[b]], c.scale, [0, e - s], 0, 0)
+        tol = 2.0 ** -8 * np.abs(ref) + 2 * (2.0 ** -8 + 2.0 ** -10) * (spread + np.abs(ref))
+        assert (np.abs(f64(c.out[s:e]) - ref) <= tol).all()
+    assert (wide[~owned] == 123).all()  # nobody's rows, and those around the output
+
+
+@pytest.mark.parametrize("starts", [[0, 5, 3, 9], [0, 5, 9, 400], [-3, 2, 4, 9], [2, 4, 6, 9], [0, 9, 0, 9], [7, 7, 3, 9],
+                                    [0, 400, 5, 9], [4, 2, 6, 5], [9, 9, 9, 9], [10, 9, 0, 4]])
+@pytest.mark.parametrize("kind", KINDS)
+def test_offsets_out_of_order(skv, kind, starts):  # noqa: F811
+    """Single CTAs: only the requests that remain are written, and these are right."""
+    bad_offsets(skv, kind_of(skv, kind), 128, 16, [64, 700, 64], starts, 9)
+
+
+@pytest.mark.parametrize("starts", [[0, 300, 0, 300], [0, 250, 100, 300], [5, 2, 290, 280], [0, 1000, 120, 300], [30, 40, 40, 200]])
+@pytest.mark.parametrize("kind", KINDS)
+def test_offsets_out_of_order_in_chunks(skv, kind, starts):  # noqa: F811
+    """The same for CTA pairs."""
+    bad_offsets(skv, kind_of(skv, kind), 256, 16, [400, 300, 900], starts, 300)
+
+
+@pytest.mark.parametrize("d,n,T", [(128, 1 << 20, 40000), (256, 1 << 19, 20100)])
+def test_offsets_that_repeat_the_largest_request(skv, d, n, T):  # noqa: F811
+    """2048 times the same tokens: taken as they are, the work list's counts would pass 32 bits.  The first has them."""
+    B, page = 4096, 64
+    g = gen(71)
+    k = torch.randn((T // page + 1) * page, 1, d, generator=g, device="cuda").bfloat16()
+    q = torch.randn(n, 1, d, generator=g, device="cuda").bfloat16()
+    table = torch.arange(T // page + 1, device="cuda", dtype=torch.int32).repeat(B, 1)
+    lens = torch.full((B,), T, device="cuda", dtype=torch.int32)
+    ws = torch.zeros((skv.paged_attend_workspace_size(B, n, 1, 1, d),), dtype=torch.uint8, device="cuda")
+    out = []
+    for starts in ([0] + [n] * B, [0, n] * (B // 2) + [0]):
+        st, o = status(), torch.zeros_like(q)
+        skv.paged_attend(skv.KV_BF16, q, k, k, table, page, lens, d ** -0.5, o, ws,
+                         q_start=torch.tensor(starts, device="cuda", dtype=torch.int32), status=st)
+        out.append((o, int(st.item())))
+    assert torch.equal(out[0][0], out[1][0]) and (out[0][0] != 0).any()
+    assert [x[1] for x in out] == [0, skv.DEV_RANGE]
