@@ -1691,7 +1691,9 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* head, const int4*
     }
 #pragma unroll
     for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    // A piece without a visible key has weight 0, and its O may be unwritten.
+    // A piece without a visible key takes no part, and its O may be unwritten:
+    // marked with a weight of -1.  One whose weight vanishes beside another's
+    // does take part: what is not finite in it reaches the output.
     float den = 0.f;
     __syncwarp();
 #pragma unroll
@@ -1699,7 +1701,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* head, const int4*
       const bool none = v[i].x == -INFINITY && v[i].y == 0.f;
       const float f = none ? 0.f : exp2f(v[i].x - m);
       den += none ? 0.f : f * v[i].y;
-      weight[warp][lane + 32 * i] = f;
+      weight[warp][lane + 32 * i] = none ? -1.f : f;
     }
     __syncwarp();
 #pragma unroll
@@ -1710,7 +1712,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* head, const int4*
 #pragma unroll 8
     for (int s = s0; s < n; s += ds) {
       const float f = weight[warp][s];
-      if (f == 0.f) continue;
+      if (f < 0.f) continue;
       const float* src = o + slot_row(s) * D + 4 * lane;
 #pragma unroll
       for (int e = 0; e < E; e += 4) {

@@ -160,3 +160,28 @@ def test_offsets_that_repeat_the_largest_request(skv, d, n, T):  # noqa: F811
         out.append((o, int(st.item())))
     assert torch.equal(out[0][0], out[1][0]) and (out[0][0] != 0).any()
     assert [x[1] for x in out] == [0, skv.DEV_RANGE]
+
+
+# ---------------------------------------------------------------------------
+# values at the ends of their ranges
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("d,T,n", [(256, 20000, 1), (128, 20000, 3), (256, 20000, 200)])
+def test_a_value_under_a_vanishing_weight_reaches_the_output(skv, d, T, n, value):  # noqa: F811
+    """A value that is not finite, seen under a weight below fp32's range (another key's logit is hundreds larger):
+    whatever piece of the keys it falls into, its column is not finite, and the others are as without it."""
+    c = Case(skv, skv.KV_BF16, d, 2, 2, 64, [T], [n], seed=80)
+    row = lambda t: int(c.table[0][t // 64]) * 64 + t % 64  # noqa: E731
+    c.q[:] = c.q[:1]
+    c.k[row(T - 300)] = 8 * c.q[0]  # every token sees it, with a logit of 8 |q|^2 / sqrt(d)
+    clean, col = c.run().clone(), 77
+    for t in (0, 100, T // 2, T - 700):
+        kept = c.v[row(t), 0, col].clone()
+        c.v[row(t), 0, col] = value
+        got = c.run()
+        c.v[row(t), 0, col] = kept
+        assert not torch.isfinite(got[:, 0, col]).any(), t
+        same = torch.ones_like(got, dtype=torch.bool)
+        same[:, 0, col] = False
+        assert torch.equal(got[same], clean[same])
