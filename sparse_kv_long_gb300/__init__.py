@@ -496,12 +496,26 @@ def _want(dev, *wanted):
         raise ValueError("expected tensors on the current CUDA device")
 
 
+def _want_rows(dev, *wanted):
+    """Each (tensor or None, dtype, shape) has to be contiguous, of that type, on device dev and of that shape, or of
+    more rows: as many elements laid out otherwise (rows of other heads, blocks of pages) would be misread."""
+    for t, dtype, shape in wanted:
+        if t is not None:
+            s = t.shape
+            if (s != shape and (len(s) != len(shape) or s[1:] != shape[1:] or s[0] < shape[0])) or t.dtype is not dtype \
+                    or not t.is_contiguous():
+                raise ValueError(f"expected contiguous rows {shape} of {dtype}, not {t.dtype} {tuple(s)} with strides "
+                                 f"{t.stride()}")
+            if t.get_device() != dev:
+                raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+
+
 def norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pool, v_pool, q_weight=None, k_weight=None, eps=1e-6,
                      interleaved=False, kv_kind=KV_BF16, k_scale=None, v_scale=None, out_rows=None, status=None,
                      stream=None):
     """q bf16 [n][Hq][d], k, v bf16 [n][Hkv][d] (views with any token stride; each may be None): q and k normed per
     head (weights fp32 [d] or None) and rotated over 2 * len(inv_freq) dims by positions int32 [n]; q -> q_out,
-    k and v -> rows out_rows (int64 [n], negative: none; None: row i) of the pools [rows][Hkv][d]."""
+    k and v -> rows out_rows (int64 [n], negative: none; None: row i) of the pools [rows][Hkv][d], scales [rows][Hkv]."""
     some = q if q is not None else k if k is not None else v
     n, _, d = some.shape
     Hq, qd, qs = _heads(q)
@@ -516,10 +530,12 @@ def norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pool, v_pool, q_weig
         raise ValueError("q, k and v on different devices")
     pool = k_pool if k_pool is not None else v_pool
     rows, H = 0 if pool is None else pool.shape[0], kh or vh
-    _want(dev, (k_pool, kind, rows * H * d), (v_pool, kind, rows * H * d), (k_scale, torch.float16, rows * H),
-          (v_scale, torch.float16, rows * H), (q_out, torch.bfloat16, n * Hq * d), (q_weight, torch.float32, d),
-          (k_weight, torch.float32, d), (positions, torch.int32, n), (inv_freq, torch.float32, 0),
-          (out_rows, torch.int64, n), (status, torch.int32, 1))
+    if H:
+        row, scales = (rows, H, d), (rows, H)
+        _want_rows(dev, (k_pool, kind, row), (v_pool, kind, row), (k_scale, torch.float16, scales),
+                   (v_scale, torch.float16, scales))
+    _want(dev, (q_out, torch.bfloat16, n * Hq * d), (q_weight, torch.float32, d), (k_weight, torch.float32, d),
+          (positions, torch.int32, n), (inv_freq, torch.float32, 0), (out_rows, torch.int64, n), (status, torch.int32, 1))
     _check("skv_norm_rope_append", (_lib or _load()).skv_norm_rope_append(
         n, Hq, H, d, 0 if inv_freq is None else 2 * inv_freq.shape[0], 1 if interleaved else 0, _at(q), qs,
         _at(k), ks, _at(v), vs, _at(q_weight), _at(k_weight), eps, _at(positions), _at(inv_freq), _at(q_out), kv_kind,
@@ -534,17 +550,19 @@ def paged_attend_workspace_size(B, n_tok, Hq, Hkv, d) -> int:
 def paged_attend(kv_kind, q, k_pool, v_pool, block_table, page, lengths, softmax_scale, out, workspace, q_start=None,
                  S=0, W=0, k_scale=None, v_scale=None, status=None, stream=None):
     """q bf16 [n][Hq][d] (any token stride): the newest tokens of each request, request b's at q_start[b] ..
-    q_start[b+1] (None: one each); pools [rows][Hkv][d]; block_table int32 [B][n_pages] -> out bf16 [n][Hq][d]."""
+    q_start[b+1] (None: one each); pools [rows][Hkv][d], scales [rows][Hkv]; block_table int32 [B][n_pages] -> out
+    bf16 [n][Hq][d]."""
     Hq, d, qs = _heads(q)
     B, n_pages = block_table.shape
     rows, Hkv, kd = k_pool.shape
     n, kind = q.shape[0], torch.int8 if kv_kind == KV_INT8 else torch.bfloat16
     if kd != d:
         raise ValueError(f"queries of {d} values, rows of {kd}")
-    _want(q.get_device(), (k_pool, kind, 0), (v_pool, kind, rows * Hkv * d), (k_scale, torch.float16, rows * Hkv),
-          (v_scale, torch.float16, rows * Hkv), (out, torch.bfloat16, n * Hq * d), (block_table, torch.int32, 0),
-          (lengths, torch.int32, B), (q_start, torch.int32, B + 1), (status, torch.int32, 1),
-          (workspace, workspace.dtype, 0))
+    dev, row, scales = q.get_device(), (rows, Hkv, d), (rows, Hkv)
+    _want_rows(dev, (k_pool, kind, row), (v_pool, kind, row), (k_scale, torch.float16, scales),
+               (v_scale, torch.float16, scales))
+    _want(dev, (out, torch.bfloat16, n * Hq * d), (block_table, torch.int32, 0), (lengths, torch.int32, B),
+          (q_start, torch.int32, B + 1), (status, torch.int32, 1), (workspace, workspace.dtype, 0))
     _check("skv_paged_attend", (_lib or _load()).skv_paged_attend(
         kv_kind, B, n, Hq, Hkv, d, q.data_ptr(), qs, k_pool.data_ptr(), v_pool.data_ptr(), _at(k_scale),
         _at(v_scale), rows, page, block_table.data_ptr(), n_pages, _at(q_start), lengths.data_ptr(), S, W,

@@ -104,3 +104,29 @@ def test_bindings_refuse_other_types_strides_and_sizes():
                 dict(positions=i32[:3]), dict(q_out=q[:3]), dict(v_pool=pool[:63]), dict(q_weight=torch.zeros((255,)))):
         with pytest.raises(ValueError, match="contiguous|consecutive|differ |queries of"):
             skv.norm_rope_append(**{**good, **bad})
+
+
+def test_bindings_refuse_pools_and_scales_of_another_layout():
+    """Enough elements are not enough: rows of another length or heads, or pages where rows are expected, would be
+    misread."""
+    import sparse_kv_long_gb300 as skv
+    q, i32 = torch.zeros((4, 8, 256), dtype=torch.bfloat16), torch.zeros((4,), dtype=torch.int32)
+    pool, scale = torch.zeros((64, 2, 256), dtype=torch.int8), torch.zeros((64, 2), dtype=torch.float16)
+    other = [pool.new_zeros(s) for s in ((64, 4, 256), (8, 16, 2, 256), (128, 1, 256), (64, 2, 512), (64, 1024), (63, 2, 256))]
+    wide = [scale.new_zeros(s) for s in ((64, 4), (128, 1), (8, 16, 2), (256,), (63, 2))]
+    good = dict(kv_kind=skv.KV_INT8, q=q, k_pool=pool, v_pool=pool, block_table=torch.zeros((4, 2), dtype=torch.int32),
+                page=16, lengths=i32, softmax_scale=1.0, out=q, workspace=q, k_scale=scale, v_scale=scale)
+    bad = [dict(v_pool=t) for t in other] + [{s: t} for s in ("k_scale", "v_scale") for t in wide]
+    for b in bad:
+        with pytest.raises(ValueError, match="expected contiguous rows"):
+            skv.paged_attend(**{**good, **b})
+    with pytest.raises(ValueError):
+        skv.paged_attend(**{**good, "k_pool": other[1]})
+    good = dict(q=q, k=q[:, :2], v=q[:, 2:4], positions=i32, inv_freq=torch.zeros((64,)), q_out=q, k_pool=pool, v_pool=pool,
+                kv_kind=skv.KV_INT8, k_scale=scale, v_scale=scale)
+    for b in bad + [dict(k_pool=t) for t in other[:2]] + [dict(k_pool=other[0], v_pool=other[0])]:
+        with pytest.raises(ValueError, match="expected contiguous rows"):
+            skv.norm_rope_append(**{**good, **b})
+    for g in (good, {**good, "k": None}, {**good, "v": None}, {**good, "k": None, "k_pool": None, "k_scale": None}):
+        with pytest.raises(ValueError, match="on the current CUDA device"):  # nothing else is wrong with these
+            skv.norm_rope_append(**g)
