@@ -799,9 +799,12 @@ int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int rot, int int
  *   workspace  skv_paged_attend_workspace_size(...) bytes; nothing in it
  *            outlasts a call, so calls of any sizes may follow one another on
  *            one of the largest size, but two at once need one each.  It holds
- *            the partial sums of cut requests: at d = 256 up to 160 MB for
- *            chunks, 40 MB for drafts, 5 MB for single tokens of 16 heads
- *            a KV head
+ *            the partial sums of cut requests.  With r = n_tok * Hq/Hkv rows,
+ *            at d = 256 and 152 SMs: 0.32 MB a row up to r = 128 (5 MB for a
+ *            token of 16 heads a KV head), above that 0.63 MB a row up to 161
+ *            MB; half of it at d = 128.  The size does not depend on B: it is
+ *            enough for every batch of up to n_tok tokens, and a decode batch
+ *            of many requests takes as much as a chunk of as many tokens
  * Constraints: d in {128, 256}; Hq / Hkv <= 128; page a multiple of 8;
  * 0 < softmax_scale <= 2e38; q_stride a multiple of 8; q, out, pools and
  * workspace 16-byte aligned; B <= 4096; n_pages * page < 2^31 - 1024; W <= 2^30

@@ -1931,7 +1931,11 @@ SKV_EXPORT size_t skv_paged_attend_workspace_size(int B, int n_tok, int Hq, int 
   if (B < 1 || n_tok < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv || Hq / Hkv > 128 || (d != 128 && d != 256)) return 0;
   const int sms = sm_count() > 0 ? sm_count() : 152;
   const int G = Hq / Hkv;
-  const size_t one = layout(n_tok, G, d, 1, sms).total, two = layout(n_tok, G, d, 2, sms).total;
+  // Enough for every call of up to n_tok tokens: by the number of requests one
+  // runs as pairs or not, but never with so few rows (ctas_for).
+  const size_t one = layout(n_tok, G, d, 1, sms).total;
+  if (static_cast<int64_t>(n_tok) * G <= kRows) return one;
+  const size_t two = layout(n_tok, G, d, 2, sms).total;
   return one > two ? one : two;
 }
 

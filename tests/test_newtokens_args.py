@@ -130,3 +130,16 @@ def test_bindings_refuse_pools_and_scales_of_another_layout():
     for g in (good, {**good, "k": None}, {**good, "v": None}, {**good, "k": None, "k_pool": None, "k_scale": None}):
         with pytest.raises(ValueError, match="on the current CUDA device"):  # nothing else is wrong with these
             skv.norm_rope_append(**g)
+
+
+@pytest.mark.parametrize("d,G,n,mb", [  # megabytes of the documentation, at 152 SMs
+    (256, 16, 1, 5.1), (256, 1, 1, 0.33), (256, 4, 32, 41), (256, 6, 22, 84), (256, 6, 64, 161), (256, 24, 4000, 161),
+    (128, 16, 1, 2.6), (128, 4, 32, 20.5), (128, 4, 33, 42), (128, 4, 4000, 81),
+])
+def test_workspace_sizes_are_the_documented_ones(lib, d, G, n, mb):
+    sms = lib.skv_device_sm_count()
+    sizes = {lib.skv_paged_attend_workspace_size(B, n, 2 * G, 2, d) for B in (1, 7, n, 4096)}
+    assert len(sizes) == 1  # whatever the number of requests
+    assert mb * 0.9e6 < sizes.pop() / (sms if sms > 0 else 152) * 152 <= mb * 1e6
+    one = lib.skv_paged_attend_workspace_size(1, n, 2 * G, 2, d)
+    assert all(lib.skv_paged_attend_workspace_size(1, m, 2 * G, 2, d) <= one for m in range(1, n, max(1, n // 50)))
