@@ -787,7 +787,8 @@ int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int rot, int int
  * SKV_DEV_RANGE.
  *   q  bf16 [n_tok][Hq][d], tokens q_stride elements apart
  *   k_pool, v_pool  bf16 or int8 [n_pool_rows][Hkv][d]
- *   k_scale, v_scale  fp16 [n_pool_rows][Hkv] (SKV_KV_INT8 only)
+ *   k_scale, v_scale  fp16 [n_pool_rows][Hkv] (SKV_KV_INT8 only; the codes of
+ *            a row whose V scale is zero are zero, as the encoding has them)
  *   block_table int32 [B][n_pages]     lengths int32 [B]
  *   q_start  int32 [B+1], ascending (a request may have no token), or NULL:
  *            one token per request (n_tok == B).  Tokens before q_start[0] and

@@ -185,3 +185,42 @@ def test_a_value_under_a_vanishing_weight_reaches_the_output(skv, d, T, n, value
         same = torch.ones_like(got, dtype=torch.bool)
         same[:, 0, col] = False
         assert torch.equal(got[same], clean[same])
+
+
+FORMS = [  # single tokens, drafts, pairs
+    (256, [700, 64, 1, 3000], [1, 1, 1, 1], True), (128, [700, 64, 1, 3000], [1, 1, 1, 1], True),
+    (256, [2000, 90], [3, 5], False), (128, [2000, 90], [7, 2], False),
+    (256, [2000, 300], [400, 300], False), (128, [2000, 300], [400, 300], False),
+]
+
+
+@pytest.mark.parametrize("d,lens,new,single", FORMS)
+def test_value_rows_of_zeros(skv, d, lens, new, single):  # noqa: F811
+    """An all-zero value row has a zero scale: its weight counts in the sum.  Half the rows, every row of the first
+    request (exact zeros come out), and none elsewhere in turn."""
+    for seed, share in ((90, 0.5), (91, 0.9), (92, 1.0)):
+        c = Case(skv, skv.KV_INT8, d, 8, 2, 16, lens, new, seed=seed)
+        zero = (torch.rand(c.vs.shape, generator=gen(seed), device="cuda") < share) & c.owned[:, None]
+        t = np.arange(lens[0])
+        zero[torch.from_numpy(c.table[0][t // 16].astype(np.int64) * 16 + t % 16).cuda()] = True
+        c.vs[zero], c.v[zero] = 0, 0
+        c.check(single=single)
+        assert (c.out[:new[0]] == 0).all()
+
+
+@pytest.mark.parametrize("d,lens,new,single", FORMS)
+def test_value_scales_of_every_size(skv, d, lens, new, single):  # noqa: F811
+    """Scales from the smallest fp16 subnormal to the largest number within a tile, a tenth of the rows zero: the sum
+    takes every weight through the reciprocal of its scale.  Keys' scales from zero to large ones, too."""
+    for seed, lo, hi in ((93, -24.0, 15.9), (94, -24.0, -20.0), (95, -12.0, 4.0), (96, 10.0, 15.9)):
+        c = Case(skv, skv.KV_INT8, d, 8, 2, 16, lens, new, seed=seed)
+        g = gen(seed)
+        scale = torch.exp2(lo + (hi - lo) * torch.rand(c.vs.shape, generator=g, device="cuda")).half()
+        scale[torch.rand(c.vs.shape, generator=g, device="cuda") < 0.1] = 0
+        scale = torch.where(torch.rand(c.vs.shape, generator=g, device="cuda") < 0.2, -scale, scale)
+        c.v[(scale == 0) & c.owned[:, None]] = 0
+        c.vs = torch.where(c.owned[:, None], scale, c.vs)
+        ks = torch.exp2(-24.0 + 18.0 * torch.rand(c.ks.shape, generator=g, device="cuda")).half()
+        ks[torch.rand(c.ks.shape, generator=g, device="cuda") < 0.1] = 0
+        c.ks = torch.where(c.owned[:, None], ks, c.ks)
+        c.check(single=single)
