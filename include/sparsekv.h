@@ -408,8 +408,8 @@ int skv_decode_layer_step(const skv_layer_step *a, void *workspace, size_t works
 /* ========================================================================== */
 /*
  * int8 rows with one fp16 scale per (row, head): scale = fp16_rne(max|x| /
- * 127) (fp32 division), code = clamp(rint(x / scale), -127, 127); a zero scale
- * gives zero codes.  Bit-exact.
+ * 127) (fp32 division), code = clamp(rint(x / scale), -127, 127); a zero or
+ * infinite scale gives zero codes.  Bit-exact.
  *   x          bf16 [n_rows][Hkv][d]
  *   out_rows   int64 [n_rows] destination row, or NULL (identity)
  *   q          int8 [rows][Hkv][d]     scale  fp16 [rows][Hkv]

@@ -131,10 +131,10 @@ __device__ __forceinline__ void store_int8(const Vals& z, int8_t* row, int xa, i
   const __half sh = __float2half_rn(__fdiv_rn(m, 127.f));
   const float s = __half2float(sh);
   uint32_t w[2] = {0u, 0u};
-  if (s != 0.f) {
+  if (s != 0.f && s < 3.0e38f) {  // a zero or infinite scale: zero codes
     const float inv = __frcp_rn(s);
     float y[8];
-    bool near = !(s < 3.0e38f);
+    bool near = false;
 #pragma unroll
     for (int e = 0; e < 8; e++) {
       y[e] = x[e] * inv;

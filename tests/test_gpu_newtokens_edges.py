@@ -224,3 +224,30 @@ def test_value_scales_of_every_size(skv, d, lens, new, single):  # noqa: F811
         ks[torch.rand(c.ks.shape, generator=g, device="cuda") < 0.1] = 0
         c.ks = torch.where(c.owned[:, None], ks, c.ks)
         c.check(single=single)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_append_encodes_rows_of_any_value(skv, d):  # noqa: F811
+    """Zeros, subnormals, numbers too small or too large for the scale, infinities, NaN: int8 rows are what
+    skv_quantize_int8_rows makes of the bf16 rows."""
+    g, n, H = gen(100), 400, 3
+    size = torch.exp2(torch.randint(-130, 127, (n, H, 1), generator=g, device="cuda").float())
+    x = (torch.randn((n, H, d), generator=g, device="cuda") * size).bfloat16()
+    x[:8] = 0
+    pick = lambda: torch.rand(x.shape, generator=g, device="cuda") < 0.01  # noqa: E731
+    for i, value in enumerate([float("inf"), float("-inf"), float("nan"), 1e-40, 3.38e38, 127 * 2.0 ** -25,
+                               127 * 1.5 * 2.0 ** -24]):
+        m = pick()
+        m[:40 + 40 * i] = False
+        x[m] = value
+    pos = torch.arange(n, device="cuda", dtype=torch.int32)
+    rows = [torch.zeros_like(x) for _ in range(2)]
+    skv.norm_rope_append(None, x, x, pos, None, None, *rows)
+    codes = [torch.full(x.shape, 99, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [torch.full((n, H), 9.0, dtype=torch.float16, device="cuda") for _ in range(2)]
+    skv.norm_rope_append(None, x, x, pos, None, None, *codes, kv_kind=skv.KV_INT8, k_scale=scales[0], v_scale=scales[1])
+    for r, c, s in zip(rows, codes, scales):
+        rc, rs = torch.zeros_like(c), torch.zeros_like(s)
+        skv.quantize_int8_rows(r, rc, rs)
+        assert torch.equal(rc, c) and torch.equal(rs.view(torch.int16), s.view(torch.int16))
+    assert torch.equal(rows[1].view(torch.int16), x.view(torch.int16))  # values as they are, bit for bit
