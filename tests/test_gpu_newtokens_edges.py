@@ -251,3 +251,16 @@ def test_append_encodes_rows_of_any_value(skv, d):  # noqa: F811
         skv.quantize_int8_rows(r, rc, rs)
         assert torch.equal(rc, c) and torch.equal(rs.view(torch.int16), s.view(torch.int16))
     assert torch.equal(rows[1].view(torch.int16), x.view(torch.int16))  # values as they are, bit for bit
+
+
+def test_outputs_may_take_the_queries_place(skv):  # noqa: F811
+    """Attention whose output is its queries' tensor: a query is read before its row is written, also where the keys are
+    cut and joined."""
+    for kind, d, lens, new in [("bf16", 256, [5000, 30], [1, 1]), ("int8", 128, [2000, 900], [300, 5])]:
+        c = Case(skv, kind_of(skv, kind), d, 8, 2, 16, lens, new, seed=101)
+        want = c.run().clone()
+        q = c.q.clone()
+        c.run(q=q)
+        skv.paged_attend(c.kind, q, c.k, c.v, c.dev[0], 16, c.dev[1], c.scale, q, c.ws, q_start=c.dev[2], k_scale=c.ks,
+                         v_scale=c.vs, status=c.st)
+        assert torch.equal(q, want)
