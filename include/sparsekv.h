@@ -752,7 +752,7 @@ int skv_prefill_attend(int nq, int Hq, int Hkv, int d, const uint16_t *q, const 
  *   out_rows int64 [n_tok], or NULL (token i -> row i); a negative row: the
  *            token has none (padding) and only its q_out is written; a row >=
  *            n_pool_rows is skipped and sets SKV_DEV_RANGE.  Two tokens with
- *            the same row leave either's bytes there
+ *            the same row leave bytes of either there, not all of one
  *   k_pool, v_pool  bf16 or int8 [n_pool_rows][Hkv][d]
  *   k_scale, v_scale  fp16 [n_pool_rows][Hkv] (SKV_KV_INT8 only)
  * Constraints: d in {64, 128, 256}; rot a multiple of 16, 0 <= rot <= d;
@@ -791,7 +791,8 @@ int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int rot, int int
  *            a row whose V scale is zero are zero, as the encoding has them)
  *   block_table int32 [B][n_pages]     lengths int32 [B]
  *   q_start  int32 [B+1], ascending (a request may have no token), or NULL:
- *            one token per request (n_tok == B).  Tokens before q_start[0] and
+ *            one token per request (n_tok == B; faster for int8 rows than the
+ *            same offsets).  Tokens before q_start[0] and
  *            from q_start[B] on are padding: their output is left as it was.
  *            A request whose offsets descend or leave [0, n_tok], or that has a
  *            token of an earlier request, is skipped (its output is left as it
@@ -811,6 +812,7 @@ int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int rot, int int
  * workspace 16-byte aligned; B <= 4096; n_pages * page < 2^31 - 1024; W <= 2^30
  * or at least n_pages * page; n_tok * Hq < 2^31; tiles of 128 / (Hq/Hkv)
  * tokens by KV heads by 64 keys of the table's width fewer than 2^31.
+ * A long chunk beside many single tokens over int8 rows runs faster as two calls.
  * Errors: SKV_EUNSUPPORTED outside the first three, SKV_ENOMEM for a short
  * workspace, SKV_EINVAL for the rest.
  * Accuracy: logits accumulate exact products in fp32, the probabilities

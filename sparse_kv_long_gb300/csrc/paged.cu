@@ -17,22 +17,29 @@
 // products of its neighbours.  m moves only when a row's maximum grows by
 // more than 2^kLazy; then the row's O is rescaled.  P is bf16 because V is (or
 // widens to it exactly) and a product takes one type; the row sum adds the
-// weights as rounded, so that the weights applied sum to one.  Logits, O, m
-// and the sums are fp32.
+// weights as rounded, so that the weights applied sum to one.  What is left of
+// that rounding takes the error against 64 bits from the output's own (0.0017
+// of the values' size) to 0.0023 at the most; what P leaves out as a second
+// bf16 would be half as many products again.  Logits, O, m and the sums are fp32.
 //
 // What bounds it, and what it measured (bf16 product rate 1916 TFLOP/s, copy
 // rate 6.79 TB/s):
-//  - chunks of 256-dim bf16 rows: the products.  2048 tokens at 65536 keys, 16
-//    heads: 1.09 ms, 1.9 PFLOP/s and more; 256 tokens at 262144 keys 0.58 ms.
+//  - chunks of 256-dim bf16 rows: the products, and with calls back to back the
+//    power limit.  2048 tokens at 65536 keys, 16 heads: 1.19 ms in bursts, 1.23
+//    to 1.25 ms (1.7 PFLOP/s) held; 256 tokens at 262144 keys 0.58 and 0.66 to
+//    0.67 ms.
 //  - chunks of 128 dims: the softmax warps, whose chain per 128 keys (logits
 //    from tensor memory, maximum, exponentials, weights back) takes 2.1 K clocks
 //    against 1.0 K of products: 1.17 PFLOP/s; six prompts of up to 4096 tokens
 //    247 us, 0.8 PFLOP/s with their masked tiles.
-//  - int8 chunks: the same chain with scales and, beside it, the widening:
-//    the issue slots are 58 % used.  4001 tokens in a window: 140 us.
+//  - int8 chunks: the same chain with scales and, beside it, the widening, which
+//    every query tile does again for the keys it sees: the issue slots are 57 %
+//    used.  4001 tokens in a window: 139 us.
 //  - single tokens: reading the cache.  Four requests of 131072 tokens, bf16:
-//    168 us, 94 % of the copy rate; 64 ragged int8 requests 118 us, 50 %, bound
-//    by the widening and the softmax chain.  In a window of a thousand keys
+//    168 us, 94 % of the copy rate; 64 ragged int8 requests 117 us, 50 %: what
+//    bounds them is the order of a tile's steps in the one CTA of an SM (copy,
+//    widen, product, softmax), with no pipe full (issue 52 %, ALU 49 %, memory
+//    44 %).  In a window of a thousand keys
 //    (19.4 us) by what follows one another: launch, lengths, plan, table,
 //    keys, two products, merge.
 //
@@ -1840,7 +1847,9 @@ Layout layout(int n_tok, int G, int d, int ctas, int sms) {
 // the size at 128 dims), the rest staging; where that would leave fewer than
 // two staging slots, as beside a full query tile of 256 dims, a wide stage
 // makes room (64 ragged requests: 3 and 6 slots 130.2 us, 4 and 4 129.3, 5 and
-// 2 156).
+// 2 156).  With q_start the tokens of a request are not known here, so a batch
+// of single tokens gets a full tile's layout: the same requests take 153 us
+// with q_start, 118 without (bf16 rows 134 either way).
 struct Shared {
   int q_bytes, stages, staging, total;
 };
@@ -1925,7 +1934,10 @@ int launch_kind(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm
 // would read the cache twice.  Eight requests of 30000 tokens, rows 128 / 192
 // each, single against pairs: bf16 of 256 dims 127 / 185 us against 126 / 119,
 // int8 136 / 205 against 165 / 157; of 128 dims 90 / 112 against 106 / 96, int8
-// 100 / 134 against 134 / 123.
+// 100 / 134 against 134 / 123.  The rule goes by the batch's mean, the lengths
+// being on the device, so a mixed batch runs as one kind: 63 single tokens at
+// 5000 keys and a chunk of 900 at 20000 (16 / 2 heads of 256) take 337 us as one
+// bf16 call and 328 as two, 502 and 374 for int8 rows.
 int ctas_for(int B, int n_tok, int G, bool single) {
   return !single && static_cast<int64_t>(n_tok) * G > static_cast<int64_t>(B) * kRows ? 2 : 1;
 }
