@@ -472,14 +472,14 @@ def _raw_stream(stream):
 
 
 def _heads(t):
-    """(heads, d, token stride) of a [n][heads][d] tensor whose tokens' heads are consecutive."""
+    """(tokens, heads, d, token stride) of a [n][heads][d] tensor whose tokens' heads are consecutive."""
     if t is None:
-        return 0, 0, 0
+        return 0, 0, 0, 0
     n, H, d = t.shape
     s = t.stride()
     if (H > 1 and s[1] != d) or (d > 1 and s[2] != 1) or t.dtype is not torch.bfloat16:
         raise ValueError("expected bf16 with a token's heads consecutive")
-    return H, d, s[0] if n > 1 else H * d
+    return n, H, d, s[0] if n > 1 else H * d
 
 
 def _want(dev, *wanted):
@@ -518,10 +518,10 @@ def norm_rope_append(q, k, v, positions, inv_freq, q_out, k_pool, v_pool, q_weig
     k and v -> rows out_rows (int64 [n], negative: none; None: row i) of the pools [rows][Hkv][d], scales [rows][Hkv]."""
     some = q if q is not None else k if k is not None else v
     n, _, d = some.shape
-    Hq, qd, qs = _heads(q)
-    kh, kd, ks = _heads(k)
-    vh, vd, vs = _heads(v)
-    if (k is not None and (k.shape[0] != n or kd != d)) or (v is not None and (v.shape[0] != n or vd != d)) or \
+    _, Hq, _, qs = _heads(q)
+    kn, kh, kd, ks = _heads(k)
+    vn, vh, vd, vs = _heads(v)
+    if (k is not None and (kn != n or kd != d)) or (v is not None and (vn != n or vd != d)) or \
             (kh and vh and kh != vh):
         raise ValueError("q, k and v differ in tokens, head dimension or KV heads")
     kind = torch.int8 if kv_kind == KV_INT8 else torch.bfloat16
@@ -552,10 +552,10 @@ def paged_attend(kv_kind, q, k_pool, v_pool, block_table, page, lengths, softmax
     """q bf16 [n][Hq][d] (any token stride): the newest tokens of each request, request b's at q_start[b] ..
     q_start[b+1] (None: one each); pools [rows][Hkv][d], scales [rows][Hkv]; block_table int32 [B][n_pages] -> out
     bf16 [n][Hq][d]."""
-    Hq, d, qs = _heads(q)
+    n, Hq, d, qs = _heads(q)
     B, n_pages = block_table.shape
     rows, Hkv, kd = k_pool.shape
-    n, kind = q.shape[0], torch.int8 if kv_kind == KV_INT8 else torch.bfloat16
+    kind = torch.int8 if kv_kind == KV_INT8 else torch.bfloat16
     if kd != d:
         raise ValueError(f"queries of {d} values, rows of {kd}")
     dev, row, scales = q.get_device(), (rows, Hkv, d), (rows, Hkv)
