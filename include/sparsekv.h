@@ -746,7 +746,8 @@ int skv_prefill_attend(int nq, int Hq, int Hkv, int d, const uint16_t *q, const 
  *      of a fused projection).  Each of the three may be NULL: that part is
  *      left out (with only q and k and out_rows NULL the call norms and
  *      rotates q and k into plain arrays, for skv_decode_layer_step)
- *   q_weight, k_weight  fp32 [d] or NULL     inv_freq  fp32 [rot/2]
+ *   q_weight, k_weight  fp32 [d] or NULL
+ *   inv_freq  fp32 [rot/2]; NULL where rot is 0 or both q and k are left out
  *   positions  int32 [n_tok]
  *   q_out    bf16 [n_tok][Hq][d]
  *   out_rows int64 [n_tok], or NULL (token i -> row i); a negative row: the

@@ -368,7 +368,7 @@ SKV_EXPORT int skv_norm_rope_append(int64_t n_tok, int Hq, int Hkv, int d, int r
   a.n_tok = n_tok;
   a.Hq = Hq;
   a.Hkv = Hkv;
-  a.rot = rot;
+  a.rot = q || k ? rot : 0;  // values are not rotated: inv_freq may be NULL, and is not read
   const int hpw = 256 / d;
   a.steps_q = q ? (Hq + hpw - 1) / hpw : 0;
   a.steps_k = k ? (Hkv + hpw - 1) / hpw : 0;

@@ -264,3 +264,22 @@ def test_outputs_may_take_the_queries_place(skv):  # noqa: F811
         skv.paged_attend(c.kind, q, c.k, c.v, c.dev[0], 16, c.dev[1], c.scale, q, c.ws, q_start=c.dev[2], k_scale=c.ks,
                          v_scale=c.vs, status=c.st)
         assert torch.equal(q, want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_values_alone_read_no_frequencies(skv, kind):  # noqa: F811
+    """With q and k left out nothing is rotated, whatever rot says: inv_freq may be NULL."""
+    n, H, d = 5, 2, 128
+    v = torch.randn((n, H, d), device="cuda").bfloat16()
+    pos = torch.arange(n, device="cuda", dtype=torch.int32)
+    pool = torch.zeros((n, H, d), dtype=torch.int8 if kind == "int8" else torch.bfloat16, device="cuda")
+    scale = torch.zeros((n, H), dtype=torch.float16, device="cuda")
+    at = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    assert skv.lib().skv_norm_rope_append(
+        n, 0, H, d, 64, 0, None, 0, None, 0, at(v), H * d, None, None, 1e-6, at(pos), None, None, kind_of(skv, kind), None, n,
+        None, at(pool), None, at(scale), None, None) == 0
+    torch.cuda.synchronize()
+    want, ws = torch.zeros_like(pool), torch.zeros_like(scale)
+    if kind == "int8":
+        skv.quantize_int8_rows(v, want, ws)
+    assert torch.equal(pool, want if kind == "int8" else v) and torch.equal(scale, ws)
