@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         }
       }
       __syncthreads();
-      if (known || !ax->disorder) break;
+      if (!a.q_start || known || !ax->disorder) break;
       again();
     }
     total = ax->items;
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         }
       }
       __syncthreads();
-      if (known || !ax->disorder) break;
+      if (!a.q_start || known || !ax->disorder) break;
       again();
     }
     const int nmax = ax->nmax, items = ax->items * a.Hkv;
