@@ -830,6 +830,54 @@ int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, int d, cons
                      float softmax_scale, uint16_t *out, void *workspace, size_t workspace_bytes,
                      int32_t *dev_status, void *stream);
 
+/*
+ * skv_shared_attend -- skv_paged_attend for a batch whose requests share long
+ * prefixes (a system prompt, a document, the prompt of several samples): each
+ * prefix is read once for all of its requests.  Group g are the requests
+ * [group_start[g], group_start[g+1]); requests before group_start[0], from
+ * group_start[n_groups] on, or in a group whose prefix length is 0 have no
+ * prefix.  The keys of a group's prefix are t < prefix_lengths[g], key t in pool
+ * row prefix_table[g][t / page] * page + t % page; its length need not fill its
+ * last page.  Request b's own keys follow it: lengths[b] tokens in the pages of
+ * block_table[b], which start a page of their own, the last n_b of them its new
+ * tokens (as for skv_paged_attend).  Token i of request b sees
+ *   every key of its group's prefix, and its own keys t <= lengths[b] - n_b + i,
+ * and out[i] is one softmax over both:
+ *   out[i][h] = sum_t softmax_t(softmax_scale q[i][h] . k[t]) v[t]
+ * (with lengths[b] - n_b + i < 0 the prefix alone, as for the last token of a
+ * prefix that is asked again; zeros where there is no prefix either).  Positions
+ * play no part: keys and queries are rotated before.  A prefix may be in several
+ * groups, and its pages in requests' own tables.
+ *   group_start     int32 [n_groups+1], ascending (a group may have no request)
+ *   prefix_table    int32 [n_groups][n_prefix_pages]
+ *   prefix_lengths  int32 [n_groups]
+ *   block_table     int32 [B][n_pages], and lengths int32 [B]: own keys only
+ *   workspace  skv_shared_attend_workspace_size(...) bytes; nothing in it
+ *            outlasts a call.  Beside the partial sums of skv_paged_attend it
+ *            holds 8 d + 24 bytes per token and query head.  The size depends on
+ *            n_tok and the heads alone: enough for every batch of up to n_tok
+ *            tokens
+ * The other arguments are those of skv_paged_attend.  Where q_start or
+ * group_start descends or leaves [0, n_tok] or [0, B] the call writes nothing
+ * and sets SKV_DEV_RANGE; pages beyond a table or the pool are skipped and set
+ * it, too.
+ * Constraints: n_groups <= 4096 (0: no prefixes; the three arrays above may then
+ * be NULL); n_tok * Hq < 2^29; n_prefix_pages as n_pages, and the tiles of both
+ * tables together as those of one; others as skv_paged_attend.
+ * Errors and accuracy: as skv_paged_attend.  A call's result does not change
+ * from run to run.
+ */
+size_t skv_shared_attend_workspace_size(int B, int n_groups, int n_tok, int Hq, int Hkv, int d);
+int skv_shared_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, int d, const uint16_t *q,
+                      int64_t q_stride, const void *k_pool, const void *v_pool,
+                      const uint16_t *k_scale, const uint16_t *v_scale, int64_t n_pool_rows,
+                      int page, int n_groups, const int32_t *group_start,
+                      const int32_t *prefix_table, int64_t n_prefix_pages,
+                      const int32_t *prefix_lengths, const int32_t *block_table, int64_t n_pages,
+                      const int32_t *q_start, const int32_t *lengths, float softmax_scale,
+                      uint16_t *out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                      void *stream);
+
 /* ========================================================================== */
 /* Pressure-driven residency ([P2] "vLLM's Hybrid HiSparse ...", "Three       */
 /* residency states, one block pool": KV stays on the GPU while there is room */

@@ -107,6 +107,9 @@ def _load():
                 "skv_paged_attend_workspace_size": ([i32, i32, i32, i32, i32], sz),
                 "skv_paged_attend": ([i32, i32, i32, i32, i32, i32, P, i64, P, P, P, P, i64, i32, P, i64, P, P, i32,
                                       i32, f32, P, P, sz, P, P], i32),
+                "skv_shared_attend_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
+                "skv_shared_attend": ([i32, i32, i32, i32, i32, i32, P, i64, P, P, P, P, i64, i32, i32, P, P, i64, P, P,
+                                       i64, P, P, f32, P, P, sz, P, P], i32),
                 "skv_residency_create": ([i32, i32, i32, i64, i32, ctypes.POINTER(ctypes.c_void_p)], i32),
                 "skv_residency_destroy": ([P], None),
                 "skv_residency_add": ([P, i32, i64, i32], i32),
@@ -568,6 +571,36 @@ def paged_attend(kv_kind, q, k_pool, v_pool, block_table, page, lengths, softmax
         _at(v_scale), rows, page, block_table.data_ptr(), n_pages, _at(q_start), lengths.data_ptr(), S, W,
         softmax_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _at(status), _raw_stream(stream)))
+    return out
+
+
+def shared_attend_workspace_size(B, n_groups, n_tok, Hq, Hkv, d) -> int:
+    return (_lib or _load()).skv_shared_attend_workspace_size(B, n_groups, n_tok, Hq, Hkv, d)
+
+
+def shared_attend(kv_kind, q, k_pool, v_pool, group_start, prefix_table, prefix_lengths, block_table, page, lengths,
+                  softmax_scale, out, workspace, q_start=None, k_scale=None, v_scale=None, status=None, stream=None):
+    """paged_attend behind shared prefixes: the requests group_start[g] .. group_start[g+1] (int32 [n_groups+1]) see the
+    prefix of prefix_lengths[g] tokens (int32 [n_groups]) in the pages prefix_table[g] (int32 [n_groups][pages]), then
+    their own keys; block_table and lengths are of the own keys alone.  The three may be None: no prefixes."""
+    n, Hq, d, qs = _heads(q)
+    B, n_pages = block_table.shape
+    groups, pages = (0, 0) if prefix_table is None else prefix_table.shape
+    rows, Hkv, kd = k_pool.shape
+    kind = torch.int8 if kv_kind == KV_INT8 else torch.bfloat16
+    if kd != d:
+        raise ValueError(f"queries of {d} values, rows of {kd}")
+    dev, row, scales = q.get_device(), (rows, Hkv, d), (rows, Hkv)
+    _want_rows(dev, (k_pool, kind, row), (v_pool, kind, row), (k_scale, torch.float16, scales),
+               (v_scale, torch.float16, scales))
+    _want(dev, (out, torch.bfloat16, n * Hq * d), (block_table, torch.int32, 0), (lengths, torch.int32, B),
+          (group_start, torch.int32, groups + 1), (prefix_table, torch.int32, 0), (prefix_lengths, torch.int32, groups),
+          (q_start, torch.int32, B + 1), (status, torch.int32, 1), (workspace, workspace.dtype, 0))
+    _check("skv_shared_attend", (_lib or _load()).skv_shared_attend(
+        kv_kind, B, n, Hq, Hkv, d, q.data_ptr(), qs, k_pool.data_ptr(), v_pool.data_ptr(), _at(k_scale),
+        _at(v_scale), rows, page, groups, _at(group_start), _at(prefix_table), pages, _at(prefix_lengths),
+        block_table.data_ptr(), n_pages, _at(q_start), lengths.data_ptr(), softmax_scale, out.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _at(status), _raw_stream(stream)))
     return out
 
 
