@@ -77,6 +77,8 @@ extern "C" {
 /* KV row encodings of skv_sparse_attend_decode. */
 #define SKV_KV_BF16 0   /* bf16 K and V rows                                      */
 #define SKV_KV_INT8 1   /* int8 K and V rows, one fp16 scale per (row, head) each  */
+#define SKV_KV_INT4 2   /* int4 rows with 64-dim groups, as skv_quantize_int4_rows */
+                        /* encodes them (skv_move_rows only)                       */
 
 /* Returns the ABI version (incremented on any incompatible change). */
 int skv_version(void);
@@ -877,6 +879,64 @@ int skv_shared_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, int d, con
                       const int32_t *q_start, const int32_t *lengths, float softmax_scale,
                       uint16_t *out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
                       void *stream);
+
+/*
+ * Rows of one cache, for skv_move_rows (all pointers are device pointers; int4
+ * rows may lie behind the device alias of a registered host tier).
+ */
+typedef struct skv_row_set {
+  int kind;              /* SKV_KV_BF16, SKV_KV_INT8 or SKV_KV_INT4                         */
+  void *k, *v;           /* bf16 or int8 [n_rows][Hkv][d]; int4: K and V of (row, head)     */
+                         /* at row*token_pitch + head*head_pitch from here.  Either may be  */
+                         /* NULL: that part is not moved                                    */
+  uint16_t *k_scale, *v_scale;     /* fp16 [n_rows][Hkv] (SKV_KV_INT8 only)                 */
+  int64_t n_rows;
+  int64_t token_pitch, head_pitch; /* bytes (SKV_KV_INT4 only).  A host tier                */
+                                   /* [n_rows][Hkv][2][d/2+d/32]: v = k + d/2 + d/32,       */
+                                   /* head_pitch = d + d/16, token_pitch = Hkv*head_pitch   */
+} skv_row_set;
+
+/*
+ * skv_move_rows -- cached rows to other rows, positions and encodings: a document
+ * cached once placed behind another prompt, a prefix brought back from the int4
+ * tier, cold bf16 rows made int8, keys turned as a context's frequencies change.
+ * Token i's rows src_rows[i] of src become the rows dst_rows[i] of dst, K and V
+ * of every head:
+ *   x = the values of the source row (zeros under a scale that is not finite, as
+ *       the encodings give such rows zero codes)
+ *   keys, with rot > 0 and positions given: for the pairs (a, b) = (f, f + rot/2),
+ *       or (2f, 2f + 1) when interleaved, of the dims [0, rot):
+ *       t = new_positions[i] * new_inv_freq[f] - old_positions[i] * old_inv_freq[f],
+ *       (x_a, x_b) = (x_a cos t - x_b sin t, x_b cos t + x_a sin t)        (fp32)
+ *   destination row = x in its encoding: bf16 rounded to nearest even, int8 as
+ *       skv_quantize_int8_rows and int4 as skv_quantize_int4_rows encode, from the
+ *       fp32 values.  Parts that are not turned and whose encoding stays the same
+ *       are copied bit by bit.
+ * The angle is taken modulo one turn as a 64-bit integer, as in
+ * skv_norm_rope_append: a key moved to another position is the one appended
+ * there, but for the roundings of the two rows.  Dims from rot on and values are
+ * not turned.
+ *   src, dst        HOST pointers, read before the call returns; both have K, V
+ *                   or both
+ *   src_rows, dst_rows  int64 [n], or NULL (token i -> row i); a token with a
+ *                   negative row is left out (padding); a row >= n_rows is
+ *                   skipped and sets SKV_DEV_RANGE.  Two tokens with the same
+ *                   destination leave bytes of either there, not all of one
+ *   old_positions, new_positions  int32 [n]; NULL: the keys were not rotated, or
+ *                   are left so (both NULL: keys keep their rotation)
+ *   old_inv_freq, new_inv_freq    fp32 [rot/2], finite; NULL where the positions are
+ * A row of one cache may be its own destination (keys turned in place: the same
+ * addresses on both sides); otherwise no destination overlaps a source.
+ * Constraints: d in {64, 128, 256}, 256 with int4 rows; rot a multiple of 16, 0 <=
+ * rot <= d; Hkv <= 4096; bf16 and int8 rows 16-byte aligned; int4 rows and pitches
+ * multiples of 4, head_pitch >= d/2 + d/32, token_pitch >= Hkv*head_pitch.
+ * Errors: SKV_EUNSUPPORTED for another d, SKV_EINVAL for the rest.
+ */
+int skv_move_rows(int64_t n, int Hkv, int d, const skv_row_set *src, const int64_t *src_rows,
+                  const skv_row_set *dst, const int64_t *dst_rows, int rot, int interleaved,
+                  const int32_t *old_positions, const float *old_inv_freq,
+                  const int32_t *new_positions, const float *new_inv_freq, int32_t *dev_status,
+                  void *stream);
 
 /* ========================================================================== */
 /* Pressure-driven residency ([P2] "vLLM's Hybrid HiSparse ...", "Three       */

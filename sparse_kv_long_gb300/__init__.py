@@ -20,7 +20,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsparsekv.so")
 
 SKETCH_INT4, SKETCH_F32, POOLED_BF16 = 0, 1, 2
-KV_BF16, KV_INT8 = 0, 1
+KV_BF16, KV_INT8, KV_INT4 = 0, 1, 2  # (KV_INT4: move_rows only)
 RESIDENT, HOST_CLOCK = 0, 1
 DEV_NAN, DEV_RANGE, DEV_TIMEOUT, DEV_COUNT = 1, 2, 4, 8
 
@@ -42,6 +42,15 @@ class LayerStep(ctypes.Structure):
         ("q", ctypes.c_void_p), ("new_k", ctypes.c_void_p), ("new_v", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
         ("idx", ctypes.c_void_p), ("count", ctypes.c_void_p), ("n_miss", ctypes.c_void_p), ("q8_out", ctypes.c_void_p),
         ("out", ctypes.c_void_p),
+    ]
+
+
+class RowSet(ctypes.Structure):
+    """The C struct skv_row_set, with what move_rows checks: see row_set and tier_rows."""
+    _fields_ = [
+        ("kind", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("n_rows", ctypes.c_int64), ("token_pitch", ctypes.c_int64),
+        ("head_pitch", ctypes.c_int64),
     ]
 
 
@@ -110,6 +119,8 @@ def _load():
                 "skv_shared_attend_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
                 "skv_shared_attend": ([i32, i32, i32, i32, i32, i32, P, i64, P, P, P, P, i64, i32, i32, P, P, i64, P, P,
                                        i64, P, P, f32, P, P, sz, P, P], i32),
+                "skv_move_rows": ([i64, i32, i32, ctypes.POINTER(RowSet), P, ctypes.POINTER(RowSet), P, i32, i32, P, P, P, P,
+                                   P, P], i32),
                 "skv_residency_create": ([i32, i32, i32, i64, i32, ctypes.POINTER(ctypes.c_void_p)], i32),
                 "skv_residency_destroy": ([P], None),
                 "skv_residency_add": ([P, i32, i64, i32], i32),
@@ -602,6 +613,69 @@ def shared_attend(kv_kind, q, k_pool, v_pool, group_start, prefix_table, prefix_
         block_table.data_ptr(), n_pages, _at(q_start), lengths.data_ptr(), softmax_scale, out.data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _at(status), _raw_stream(stream)))
     return out
+
+
+def row_set(kv_kind, k, v, k_scale=None, v_scale=None) -> RowSet:
+    """The rows of a cache, for move_rows: k, v bf16 or int8 [rows][Hkv][d] with scales fp16 [rows][Hkv], or int4 uint8
+    [rows][Hkv][d/2 + d/32] with any token and head stride.  k or v may be None."""
+    some = k if k is not None else v
+    rows, Hkv, d = some.shape
+    pitch = 0, 0
+    dev = some.get_device()
+    if kv_kind == KV_INT4:
+        pitch = some.stride()[:2]
+        for t in (k, v):
+            if t is not None and (t.dtype is not torch.uint8 or t.shape != some.shape or t.stride() != some.stride() or
+                                  t.stride(2) != 1 or t.get_device() != dev):
+                raise ValueError("expected uint8 K and V of one shape and layout")
+        d = d * 32 // 17
+    else:
+        kind = torch.int8 if kv_kind == KV_INT8 else torch.bfloat16
+        for t in (k, v):
+            if t is not None and t.shape != some.shape:
+                raise ValueError("expected K and V of one shape")
+        _want_rows(dev, (k, kind, (rows, Hkv, d)), (v, kind, (rows, Hkv, d)), (k_scale, torch.float16, (rows, Hkv)),
+                   (v_scale, torch.float16, (rows, Hkv)))
+    r = RowSet(kv_kind, _at(k), _at(v), _at(k_scale), _at(v_scale), rows, *pitch)
+    r.shape, r.device, r.tensors = (Hkv, d), dev, (k, v, k_scale, v_scale)
+    return r
+
+
+def tier_rows(tier, keys=True, values=True) -> RowSet:
+    """The rows of an int4 tier [..rows..][Hkv][2][d/2 + d/32], K then V of each head: a uint8 tensor, or a HostView."""
+    *rows, Hkv, two, vec = tier.shape
+    if not rows or two != 2 or (isinstance(tier, torch.Tensor) and (tier.dtype is not torch.uint8 or not tier.is_contiguous())):
+        raise ValueError("expected contiguous uint8 rows of [Hkv][2][d/2 + d/32]")
+    n = 1
+    for s in rows:
+        n *= s
+    at = tier.data_ptr()
+    r = RowSet(KV_INT4, at if keys else None, at + vec if values else None, None, None, n, 2 * Hkv * vec, 2 * vec)
+    r.shape, r.tensors = (Hkv, vec * 32 // 17), (tier,)
+    r.device = tier.get_device() if isinstance(tier, torch.Tensor) else None
+    return r
+
+
+def move_rows(src, dst, n, src_rows=None, dst_rows=None, old_positions=None, old_inv_freq=None, new_positions=None,
+              new_inv_freq=None, interleaved=False, status=None, stream=None):
+    """Rows src_rows (int64 [n], None: row i; negative: left out) of src to rows dst_rows of dst (row_set, tier_rows),
+    re-encoded; keys turned from old_positions * old_inv_freq to new_positions * new_inv_freq (int32 [n], fp32
+    [rot/2]; None: not rotated)."""
+    if src.shape != dst.shape:
+        raise ValueError(f"rows of (heads, values) {src.shape} and {dst.shape}")
+    freqs = [f for f in (old_inv_freq, new_inv_freq) if f is not None]
+    rot = 2 * freqs[0].shape[0] if freqs else 0
+    if any(2 * f.shape[0] != rot for f in freqs):
+        raise ValueError("frequencies of different numbers of pairs")
+    dev = torch.cuda.current_device()
+    if src.device not in (dev, None) or dst.device not in (dev, None):
+        raise ValueError("expected rows on the current CUDA device")
+    _want(dev, (src_rows, torch.int64, n), (dst_rows, torch.int64, n), (old_positions, torch.int32, n),
+          (new_positions, torch.int32, n), (old_inv_freq, torch.float32, 0), (new_inv_freq, torch.float32, 0),
+          (status, torch.int32, 1))
+    _check("skv_move_rows", (_lib or _load()).skv_move_rows(
+        n, *src.shape, src, _at(src_rows), dst, _at(dst_rows), rot, 1 if interleaved else 0, _at(old_positions),
+        _at(old_inv_freq), _at(new_positions), _at(new_inv_freq), _at(status), _raw_stream(stream)))
 
 
 # ---- pressure-driven residency -----------------------------------------------------
