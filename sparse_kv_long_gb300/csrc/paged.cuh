@@ -143,7 +143,7 @@ struct PagedArgs {
   uint16_t* out;
   int32_t* status;
   int stages, staging;        // ring depths
-  int thin;                   // int8: query tiles of at most 32 rows; the other rows' softmax warps widen instead
+  int thin;                   // int8: query tiles of at most 32 rows (2: 64); the other rows' softmax warps widen instead
   int q_bytes;                // shared memory of the query tile: D / 64 column blocks of q_sub bytes
   int q_sub, q_box;           // (128 per row, rounded up to 1024; pairs: 128 rows); bytes a copy of one brings
   int part_rows;              // rows of a partial slot
@@ -689,10 +689,12 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   // Softmax warps and widening warps: with at most 32 rows a tile, as single
   // tokens have, warps 4 and 8 do the softmax and 5, 6, 7, 11 join the widening (9 and
   // 10 rest: at most two widen per scheduler that has other work).  64 ragged
-  // requests took 190 us with four widening warps, 166 with these eight.
+  // requests took 190 us with four widening warps, 166 with these eight.  With
+  // prefixes also at most 64 rows: 4, 5, 8 and 9, and 6, 7, 10 and 11.
   const bool thin = INT8 && CTAS == 1 && a.thin;
-  const uint32_t n_soft = thin ? 2 : 8, n_wide = thin ? 8 : 4;
-  const bool softer = warp >= 4 && warp < 12 && (!thin || (warp & 3) == 0);
+  const bool half = PRE && thin && a.thin == 2;
+  const uint32_t n_soft = half ? 4 : thin ? 2 : 8, n_wide = thin ? 8 : 4;
+  const bool softer = warp >= 4 && warp < 12 && (!thin || (warp & 3) <= (half ? 1 : 0));
   const int unit = blockIdx.x / CTAS, n_units = gridDim.x / CTAS;
   volatile int* abort = &ax->abort;
 
@@ -841,8 +843,8 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     // Items kept whole in the second half of the candidates: the full rounds,
     // in the work list's order; only a batch that one warp holds is looked at
     // this way.
-    const int x1 = n_req <= 32 && items > n_units ? items / n_units * n_units : 0;
-    const int nk = min(nmax, n_req > 512 ? 8 : kCand);
+    const int x1 = !PRE && n_req <= 32 && items > n_units ? items / n_units * n_units : 0;
+    const int nk = min(nmax, n_req > 512 ? 8 : PRE ? n_units : kCand);
     float best = 3e38f;
     int pick = 0;
 #pragma unroll 1
@@ -852,6 +854,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       const int c = (nmax + k - 1) / k;
       const float rc = 1.f / c;
       int P = 0, S = 0, u = 0, main_u = 0;  // pieces, those of cut items, tiles of the items looked at, of the others
+      int PL = 0, uL = 0;                   // long pieces, their tiles
 #pragma unroll 1
       for (int b0 = 0; b0 < n_req; b0 += 32) {
         const int2 r = b0 + lane < n_req ? req[b0 + lane] : make_int2(0, 0);
@@ -872,6 +875,10 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         S += ps > 1 ? n * ps : 0;
         u += n * r.y;
         main_u += (all - n) * r.y;
+        if (PRE && 2 * r.y >= c) {
+          PL += n * ps;
+          uL += n * r.y;
+        }
       }
       P = __reduce_add_sync(0xffffffffu, P);
       S = __reduce_add_sync(0xffffffffu, S);
@@ -879,7 +886,14 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       if (rest) main_u = __reduce_add_sync(0xffffffffu, main_u);
       if (S <= a.max_split) {
         float cost = rest ? static_cast<float>(main_u) / n_units + x1 / n_units * kOvh : 0.f;
-        if (P > 0)
+        if (PRE) {
+          PL = __reduce_add_sync(0xffffffffu, PL);
+          uL = __reduce_add_sync(0xffffffffu, uL);
+          const int rounds = (P + n_units - 1) / n_units, long_rounds = (PL + n_units - 1) / n_units;
+          if (PL > 0) cost += long_rounds * (static_cast<float>(uL) / PL + kOvh);
+          if (rounds > long_rounds) cost += (rounds - long_rounds) * (static_cast<float>(u - uL) / (P - PL) + kOvh);
+          if (S > 0) cost += kJoin + S * a.part_cost;
+        } else if (P > 0)
           cost += static_cast<float>((P - 1) / n_units) * (static_cast<float>(u) / P + kOvh) + c + kOvh +
                   (S > 0 ? kJoin + S * a.part_cost : 0.f);
         if (cost < best) {
@@ -1696,9 +1710,10 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       tc::tmem_wait_ld();
     }
     for (float other = 0.f; __float_as_uint(other) != kGone;) exchange(__uint_as_float(kGone), other);
-  } else if (INT8 && (warp >= 12 || warp < 8 || warp == 11)) {
+  } else if (INT8 && (warp >= 12 || warp < 8 || warp == 11 || half)) {
     // ---------------- int8 -> bf16 (warps 12-15, and where they are free 5, 6, 7, 11) ----------------
-    const int ct = warp >= 12 ? tid - 384 : 128 + 32 * (warp == 11 ? 3 : warp - 5) + lane;
+    const int extra = half ? (warp >= 10 ? warp - 8 : warp - 6) : warp == 11 ? 3 : warp - 5;
+    const int ct = warp >= 12 ? tid - 384 : 128 + 32 * extra + lane;
     // Thread -> 16 codes of one row, a few times a stage: ct % 8 is the row
     // of its 8-row group, so eight lanes read eight rows' swizzled pieces
     // (distinct banks) and write them the same way.  Piece `pce` of a row is

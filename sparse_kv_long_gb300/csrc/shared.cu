@@ -298,7 +298,7 @@ SKV_EXPORT int skv_shared_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv,
   const int most_toks = n_groups > 0 ? toks : own_toks;  // per CTA
   a.q_box = most_toks * G * 128;
   a.q_box_own = own_toks * G * 128;
-  a.thin = int8 && ctas == 1 && most_toks * G <= 32;
+  a.thin = !int8 || ctas == 2 ? 0 : most_toks * G <= 32 ? 1 : most_toks * G <= 64 ? 2 : 0;
   a.q_sub = ctas == 2 ? kRows * 128 : (a.q_box + 1023) / 1024 * 1024;
   const Shared sh = shared_layout(d, ctas, int8, a.q_sub);
   a.q_bytes = sh.q_bytes;
