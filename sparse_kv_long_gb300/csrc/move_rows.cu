@@ -39,8 +39,9 @@ struct MoveArgs {
   int64_t n;
   int Hkv, rot;
   int turn;                  // keys are turned
-  int steps_k, steps_v;      // warp steps (256 / d heads) per token; 0: part left out
-  int chunk, chunks;         // steps per work item, work items per token
+  int steps;                 // warp steps (256 / d heads) of a token's K or V
+  int chunk;                 // steps per work item
+  int chunks_k, chunks_v;    // work items per token; 0: part left out
   RowSet src, dst;
   const int64_t *src_rows, *dst_rows;
   const int32_t *old_pos, *new_pos;
@@ -91,130 +92,199 @@ __device__ __forceinline__ Raw load(const unsigned char* vec, const __half* scal
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The larger of |a| and |b|, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
+// The eight values, exact: run a in x[0], x[1], run b in x[2], x[3].  A code
+// becomes a float as the low bits of 2^23: conversions run at an eighth of the
+// rate of the rest.
 template <int KIND>
-__device__ __forceinline__ void decode(const Raw& r, float (&x)[8]) {
+__device__ __forceinline__ void decode(const Raw& r, F2 (&x)[4]) {
   if (KIND == SKV_KV_BF16) {
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
-      x[2 * e] = __uint_as_float(r.w[e] << 16);
-      x[2 * e + 1] = __uint_as_float(r.w[e] & 0xffff0000u);
-    }
+    for (int e = 0; e < 4; e++) x[e] = unpack2(r.w[e]);
   } else {
 #pragma unroll
     for (int run = 0; run < 2; run++) {
       float s = __half2float(__ushort_as_half(r.s[run]));
       if (!(fabsf(s) <= 65504.f)) s = 0.f;  // the encodings give such a row zero codes
-      const int w = static_cast<int>(r.w[2 * run]);
+      float f[4];
+      const uint32_t w = r.w[2 * run] ^ (KIND == SKV_KV_INT8 ? 0x80808080u : 0x8888u);  // offset binary
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const int c = KIND == SKV_KV_INT8 ? (w << (24 - 8 * e)) >> 24 : (w << (28 - 4 * e)) >> 28;
-        x[4 * run + e] = static_cast<float>(c) * s;
-      }
+      for (int e = 0; e < 4; e++)
+        f[e] = __uint_as_float(KIND == SKV_KV_INT8 ? prmt(w, 0x4b000000u, 0x7650u + e)
+                                                   : ((w >> (4 * e)) & 15u) | 0x4b000000u);
+      const float zero = KIND == SKV_KV_INT8 ? -8388736.f : -8388616.f;  // 2^23 and the offset
+#pragma unroll
+      for (int e = 0; e < 2; e++)
+        x[2 * run + e] = f2_mul(f2_add(f2(f[2 * e], f[2 * e + 1]), f2(zero, zero)), f2(s, s));
     }
   }
 }
 
-// rint(x / s) of four values, clamped.  The quotients come from a reciprocal
-// (off by at most 127 * 3 * 2^-24 < 3e-5) unless one lies that near a
-// half-integer; then from the correctly rounded division.
-__device__ __forceinline__ void codes_of(const float* x, float s, int lo, int hi, int (&c)[4]) {
-  const float inv = __frcp_rn(s);
-  float y[4];
-  bool near = false;
+__device__ __forceinline__ float amax8(const F2 (&x)[4]) {  // a NaN takes no part
+  float m = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; e++) {
-    y[e] = x[e] * inv;
-    near |= !(fabsf(y[e] - rintf(y[e])) < 0.49995f);  // also where x is not finite
+    const float2 v = f2_out(x[e]);
+    m = max3(m, fabsf(v.x), fabsf(v.y));
   }
-  if (near) {
-#pragma unroll
-    for (int e = 0; e < 4; e++) y[e] = __fdiv_rn(x[e], s);
-  }
-#pragma unroll
-  for (int e = 0; e < 4; e++) c[e] = rint_clamp(y[e], lo, hi);
+  return m;
 }
 
 // A zero or infinite scale gives zero codes.
 __device__ __forceinline__ bool usable(float s) { return s != 0.f && s < 3.0e38f; }
 
-__device__ __forceinline__ float max4(const float* x) {  // of the absolute values; a NaN takes no part
-  return fmaxf(fmaxf(fmaxf(0.f, fabsf(x[0])), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+// A scale and what the values are multiplied with: its reciprocal, 0 where the
+// codes are zero, NaN where fp16's small numbers hold the scale too coarsely for
+// the largest code to stay in range by itself.
+__device__ __forceinline__ float factor_of(float s) {
+  return !usable(s) ? 0.f : s < 6.103515625e-5f ? __uint_as_float(0x7fc00000u) : __frcp_rn(s);
 }
 
-// Every lane of the warp takes part; `write`: this lane's head is written.
-template <int KIND, bool RUN, int LPH>
-__device__ __forceinline__ void encode(const float (&x)[8], unsigned char* vec, __half* scale, int xa, int xb, bool write) {
-  constexpr int D = 8 * LPH;
-  if (KIND == SKV_KV_BF16) {
-    uint32_t w[4];
+// Four values' codes rint(x / s) as the low bits of 2^23 + 2^22.  The products
+// with the reciprocal are off by at most 127 * 3 * 2^-24 < 3e-5; where one lies
+// that near a half-integer, or is no number, the correctly rounded divisions
+// decide.
+__device__ __forceinline__ void codes_of(F2 a, F2 b, float s, float inv, int lo, int hi, uint32_t (&c)[4]) {
+  const F2 up = f2(12582912.f, 12582912.f), down = f2(-12582912.f, -12582912.f), i2 = f2(inv, inv), minus = f2(-1.f, -1.f);
+  const F2 y0 = f2_mul(a, i2), y1 = f2_mul(b, i2);
+  const F2 r0 = f2_add(y0, up), r1 = f2_add(y1, up);
+  const float2 d0 = f2_out(f2_fma(f2_add(r0, down), minus, y0)), d1 = f2_out(f2_fma(f2_add(r1, down), minus, y1));
+  const float2 q0 = f2_out(r0), q1 = f2_out(r1);
+  c[0] = __float_as_uint(q0.x), c[1] = __float_as_uint(q0.y), c[2] = __float_as_uint(q1.x), c[3] = __float_as_uint(q1.y);
+  if (!(max_nan(max_nan(d0.x, d0.y), max_nan(d1.x, d1.y)) < 0.49995f)) {
+    const float2 x0 = f2_out(a), x1 = f2_out(b);
+    const float x[4] = {x0.x, x0.y, x1.x, x1.y};
+    const bool ok = usable(s);
 #pragma unroll
-    for (int e = 0; e < 4; e++) w[e] = pack2(f2(x[2 * e], x[2 * e + 1]));
-    if (!write) return;
-    if (RUN) {
-      *reinterpret_cast<uint4*>(vec + 2 * xa) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      *reinterpret_cast<uint2*>(vec + 2 * xa) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2*>(vec + 2 * xb) = make_uint2(w[2], w[3]);
+    for (int e = 0; e < 4; e++) c[e] = ok ? static_cast<uint32_t>(rint_clamp(__fdiv_rn(x[e], s), lo, hi)) : 0u;
+  }
+}
+
+__device__ __forceinline__ uint32_t bytes_of(const uint32_t (&c)[4]) {
+  return prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
+}
+
+// Encodes the heads of a batch, v[u] of step s0 + u; every lane of the warp takes
+// part.  One lane per scale makes it and its reciprocal for all.
+template <int KIND, bool RUN, int LPH>
+__device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* dst, int64_t pitch, __half* scale, int h0,
+                                       int H, int steps, int lane, int xa, int xb) {
+  constexpr int D = 8 * LPH, HPW = 32 / LPH;
+  const int sub = lane % LPH;
+  if (KIND == SKV_KV_BF16) {
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {
+      const int h = h0 + u * HPW;
+      if (u >= steps || h >= H) break;
+      unsigned char* vec = dst + h * pitch;
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) w[e] = pack2(v[u][e]);
+      if (RUN) {
+        *reinterpret_cast<uint4*>(vec + 2 * xa) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        *reinterpret_cast<uint2*>(vec + 2 * xa) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(vec + 2 * xb) = make_uint2(w[2], w[3]);
+      }
     }
   } else if (KIND == SKV_KV_INT8) {
-    float m = fmaxf(max4(x), max4(x + 4));
+    float mine = 0.f;
 #pragma unroll
-    for (int o = LPH / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const __half sh = __float2half_rn(__fdiv_rn(m, 127.f));
-    const float s = __half2float(sh);
-    uint32_t w[2] = {0u, 0u};
-    if (usable(s)) {
+    for (int u = 0; u < kBatch; u++) {
+      float m = amax8(v[u]);
+      if (LPH == 32) {  // as bits: neither NaN nor negative
+        m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+      } else {
 #pragma unroll
-      for (int run = 0; run < 2; run++) {
-        int c[4];
-        codes_of(x + 4 * run, s, -127, 127, c);
+        for (int o = LPH / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      }
+      if (sub == u) mine = m;
+    }
+    const __half sh = __float2half_rn(__fdiv_rn(mine, 127.f));
+    const float s_own = __half2float(sh), i_own = factor_of(s_own);
+    if (sub < steps && h0 + sub * HPW < H) scale[h0 + sub * HPW] = sh;
 #pragma unroll
-        for (int e = 0; e < 4; e++) w[run] |= static_cast<uint32_t>(c[e] & 255) << (8 * e);
+    for (int u = 0; u < kBatch; u++) {
+      if (u >= steps) break;
+      const int from = lane - sub + u, h = h0 + u * HPW;
+      const float s = __shfl_sync(0xffffffffu, s_own, from), inv = __shfl_sync(0xffffffffu, i_own, from);
+      uint32_t c[4], w[2];
+      codes_of(v[u][0], v[u][1], s, inv, -127, 127, c);
+      w[0] = bytes_of(c);
+      codes_of(v[u][2], v[u][3], s, inv, -127, 127, c);
+      w[1] = bytes_of(c);
+      unsigned char* vec = dst + h * pitch;
+      if (HPW > 1 && h >= H) continue;
+      if (RUN) {
+        *reinterpret_cast<uint2*>(vec + xa) = make_uint2(w[0], w[1]);
+      } else {
+        *reinterpret_cast<uint32_t*>(vec + xa) = w[0];
+        *reinterpret_cast<uint32_t*>(vec + xb) = w[1];
       }
     }
-    if (!write) return;
-    if (RUN) {
-      *reinterpret_cast<uint2*>(vec + xa) = make_uint2(w[0], w[1]);
-    } else {
-      *reinterpret_cast<uint32_t*>(vec + xa) = w[0];
-      *reinterpret_cast<uint32_t*>(vec + xb) = w[1];
-    }
-    if (xa == 0) *scale = sh;
   } else {
     static_assert(KIND != SKV_KV_INT4 || LPH == 32, "a warp per vector");
-    const float ma = max4(x), mb = max4(x + 4);
+    // Lane 8 g + u: the scale of group g of step u.
     const int ga = xa >> 6, gb = xb >> 6;
-    float m[2] = {0.f, 0.f};
+    float mine = 0.f;
 #pragma unroll
-    for (int g = 0; g < D / 64; g++) {  // as bits: neither NaN nor negative
-      const float mine = fmaxf(ga == g ? ma : 0.f, gb == g ? mb : 0.f);
-      const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
-      if (ga == g) m[0] = all;
-      if (gb == g) m[1] = all;
-    }
-    uint32_t w[2] = {0u, 0u};
-    uint16_t sb[2];
+    for (int u = 0; u < kBatch; u++) {
+      if (RUN) {
+        float m = amax8(v[u]);
 #pragma unroll
-    for (int run = 0; run < 2; run++) {
-      const __half sh = __float2half_rn(__fdiv_rn(m[run], 7.f));
-      const float s = __half2float(sh);
-      sb[run] = __half_as_ushort(sh);
-      if (usable(s)) {
-        int c[4];
-        codes_of(x + 4 * run, s, -8, 7, c);
+        for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if ((lane & 7) == u) mine = m;
+      } else {
+        const float2 a0 = f2_out(v[u][0]), a1 = f2_out(v[u][1]), b0 = f2_out(v[u][2]), b1 = f2_out(v[u][3]);
+        const float ma = max3(max3(0.f, fabsf(a0.x), fabsf(a0.y)), fabsf(a1.x), fabsf(a1.y));
+        const float mb = max3(max3(0.f, fabsf(b0.x), fabsf(b0.y)), fabsf(b1.x), fabsf(b1.y));
 #pragma unroll
-        for (int e = 0; e < 4; e++) w[run] |= static_cast<uint32_t>(c[e] & 15) << (4 * e);
+        for (int g = 0; g < D / 64; g++) {
+          const float m = fmaxf(ga == g ? ma : 0.f, gb == g ? mb : 0.f);
+          const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+          if (lane == 8 * g + u) mine = all;
+        }
       }
     }
-    if (!write) return;
-    if (RUN) {
-      *reinterpret_cast<uint32_t*>(vec + xa / 2) = w[0] | w[1] << 16;
-    } else {
-      *reinterpret_cast<uint16_t*>(vec + xa / 2) = static_cast<uint16_t>(w[0]);
-      *reinterpret_cast<uint16_t*>(vec + xb / 2) = static_cast<uint16_t>(w[1]);
+    const __half sh = __float2half_rn(__fdiv_rn(mine, 7.f));
+    const float s_own = __half2float(sh), i_own = factor_of(s_own);
+    if ((lane & 7) < steps)
+      *reinterpret_cast<uint16_t*>(dst + (h0 + (lane & 7)) * pitch + D / 2 + 2 * (lane >> 3)) = __half_as_ushort(sh);
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {
+      if (u >= steps) break;
+      uint32_t c[4], w[2];
+      float s = __shfl_sync(0xffffffffu, s_own, 8 * ga + u), inv = __shfl_sync(0xffffffffu, i_own, 8 * ga + u);
+      codes_of(v[u][0], v[u][1], s, inv, -8, 7, c);
+      w[0] = bytes_of(c) & 0x0f0f0f0fu;
+      if (!RUN) {
+        s = __shfl_sync(0xffffffffu, s_own, 8 * gb + u);
+        inv = __shfl_sync(0xffffffffu, i_own, 8 * gb + u);
+      }
+      codes_of(v[u][2], v[u][3], s, inv, -8, 7, c);
+      w[1] = bytes_of(c) & 0x0f0f0f0fu;
+      w[0] |= w[0] >> 4;  // bytes 0 and 2 hold two codes each
+      w[1] |= w[1] >> 4;
+      unsigned char* vec = dst + (h0 + u) * pitch;
+      if (RUN) {
+        *reinterpret_cast<uint32_t*>(vec + xa / 2) = prmt(w[0], w[1], 0x6420u);
+      } else {
+        *reinterpret_cast<uint16_t*>(vec + xa / 2) = static_cast<uint16_t>(prmt(w[0], 0u, 0x0020u));
+        *reinterpret_cast<uint16_t*>(vec + xb / 2) = static_cast<uint16_t>(prmt(w[1], 0u, 0x0020u));
+      }
     }
-    if ((xa & 63) == 0) *reinterpret_cast<uint16_t*>(vec + D / 2 + 2 * ga) = sb[0];
-    if ((xb & 63) == 0) *reinterpret_cast<uint16_t*>(vec + D / 2 + 2 * gb) = sb[1];
   }
 }
 
@@ -241,61 +311,52 @@ __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_
   const int sub = lane % LPH, grp = lane / LPH, half = a.rot / 2;
   const bool rotated = MODE == kTurn && sub < a.rot / 8;
   const int xa = !RUN && rotated ? 4 * sub : 8 * sub, xb = !RUN && rotated ? xa + half : xa + 4;
-  F2 co[4], si[4];
-  if (MODE == kTurn) {
-#pragma unroll
-    for (int e = 0; e < 4; e++) {  // of values 2 e, 2 e + 1
-      float2 c0 = make_float2(1.f, 0.f), c1 = c0;
-      if (rotated) {
-        c0 = cs[INTER ? xa / 2 + e : xa + 2 * (e & 1)];
-        c1 = INTER ? c0 : cs[xa + 2 * (e & 1) + 1];
-      }
-      co[e] = f2(c0.x, c1.x);
-      si[e] = INTER ? f2(-c0.y, c0.y) : e < 2 ? f2(-c0.y, -c1.y) : f2(c0.y, c1.y);
-    }
-  }
   const unsigned char* src = (values ? a.src.v : a.src.k) + from * a.src.token_pitch;
   unsigned char* dst = const_cast<unsigned char*>(values ? a.dst.v : a.dst.k) + to * a.dst.token_pitch;
   const __half* sscale = SRC == SKV_KV_INT8 ? (values ? a.src.v_scale : a.src.k_scale) + from * a.Hkv : nullptr;
   __half* dscale = DST == SKV_KV_INT8 ? const_cast<__half*>(values ? a.dst.v_scale : a.dst.k_scale) + to * a.Hkv : nullptr;
   for (int s0 = lo; s0 < hi; s0 += kBatch) {
     Raw raw[kBatch];
+    const int h0 = s0 * HPW + grp;
 #pragma unroll
     for (int u = 0; u < kBatch; u++) {  // every load of the batch first
-      const int h = (s0 + u) * HPW + grp;
+      const int h = h0 + u * HPW;
       raw[u] = Raw{};
       if (s0 + u < hi && (HPW == 1 || h < a.Hkv)) raw[u] = load<SRC, RUN>(src + h * a.src.head_pitch, sscale + h, xa, xb, D);
     }
+    if constexpr (MODE == kCopy) {
 #pragma unroll
-    for (int u = 0; u < kBatch; u++) {
-      if (s0 + u >= hi) break;
-      const int h = (s0 + u) * HPW + grp;
-      const bool live = HPW == 1 || h < a.Hkv;
-      unsigned char* vec = dst + h * a.dst.head_pitch;
-      if constexpr (MODE == kCopy) {
-        if (live) store<SRC, LPH>(raw[u], vec, dscale + h, xa);
-      } else {
-        float x[8];
-        decode<SRC>(raw[u], x);
-        if constexpr (MODE == kTurn) {
-          if (rotated) {  // elsewhere an infinite neighbour would make 0 * inf
-            F2 y[4];
+      for (int u = 0; u < kBatch; u++) {
+        const int h = h0 + u * HPW;
+        if (s0 + u < hi && (HPW == 1 || h < a.Hkv)) store<SRC, LPH>(raw[u], dst + h * a.dst.head_pitch, dscale + h, xa);
+      }
+    } else {
+      F2 v[kBatch][4];
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-              const F2 own = f2(x[2 * e], x[2 * e + 1]);
-              const F2 other = INTER ? f2(x[2 * e + 1], x[2 * e]) : f2(x[2 * (e ^ 2)], x[2 * (e ^ 2) + 1]);
-              y[e] = f2_fma(other, si[e], f2_mul(own, co[e]));
-            }
+      for (int u = 0; u < kBatch; u++) decode<SRC>(raw[u], v[u]);
+      if constexpr (MODE == kTurn) {
+        if (rotated) {  // elsewhere an infinite neighbour would make 0 * inf
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-              const float2 z = f2_out(y[e]);
-              x[2 * e] = z.x;
-              x[2 * e + 1] = z.y;
+          for (int e = 0; e < (INTER ? 4 : 2); e++) {
+            // of values 2 e, 2 e + 1 (and, halves, of their partners)
+            const float2 c0 = cs[INTER ? xa / 2 + e : xa + 2 * e], c1 = INTER ? c0 : cs[xa + 2 * e + 1];
+            const F2 co = f2(c0.x, c1.x), si = INTER ? f2(-c0.y, c0.y) : f2(c0.y, c1.y), ni = f2(-c0.y, -c1.y);
+#pragma unroll
+            for (int u = 0; u < kBatch; u++) {
+              const F2 p = v[u][e];
+              if (INTER) {
+                const float2 x = f2_out(p);
+                v[u][e] = f2_fma(f2(x.y, x.x), si, f2_mul(p, co));
+              } else {
+                const F2 q = v[u][e ^ 2];
+                v[u][e] = f2_fma(q, ni, f2_mul(p, co));
+                v[u][e ^ 2] = f2_fma(p, si, f2_mul(q, co));
+              }
             }
           }
         }
-        encode<DST, RUN, LPH>(x, vec, dscale + h, xa, xb, live);
       }
+      encode<DST, RUN, LPH>(v, dst, a.dst.head_pitch, dscale, h0, a.Hkv, min(kBatch, hi - s0), lane, xa, xb);
     }
   }
 }
@@ -314,35 +375,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) move_kernel(const MoveAr
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
-  const int64_t items = a.n * a.chunks;
+  // First every token's keys, then every token's values, so that each warp gets
+  // as much of the one as of the other.
+  const int64_t keys = a.n * a.chunks_k, items = keys + a.n * a.chunks_v;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int end = a.steps_k + a.steps_v;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items; item += step) {
-    const int64_t tok = a.chunks == 1 ? item : item / a.chunks;
-    const int p0 = static_cast<int>(item - tok * a.chunks) * a.chunk, p1 = min(end, p0 + a.chunk);
+    const bool values = item >= keys;
+    const int64_t i = values ? item - keys : item;
+    const int chunks = values ? a.chunks_v : a.chunks_k;
+    const int64_t tok = chunks == 1 ? i : i / chunks;
+    const int lo = static_cast<int>(i - tok * chunks) * a.chunk, hi = min(a.steps, lo + a.chunk);
     const int64_t from = a.src_rows ? a.src_rows[tok] : tok, to = a.dst_rows ? a.dst_rows[tok] : tok;
     if (from < 0 || to < 0) continue;  // padding
     if (from >= a.src.n_rows || to >= a.dst.n_rows) {
       if (lane == 0) set_status(a.status, SKV_DEV_RANGE);
       continue;
     }
-    if (p0 < a.steps_k) {
-      if (a.turn) {
-        const uint64_t old_pos = a.old_pos ? static_cast<int64_t>(a.old_pos[tok]) : 0;
-        const uint64_t new_pos = a.new_pos ? static_cast<int64_t>(a.new_pos[tok]) : 0;
-        __syncwarp();  // the previous token's values have been read
-        for (int f = lane; f < half; f += 32)
-          cs[warp][f] = cos_sin(static_cast<uint32_t>((new_pos * turns[1][f] - old_pos * turns[0][f]) >> 32));
-        __syncwarp();
-        run_heads<LPH, SRC, DST, INTER, kTurn>(a, false, from, to, p0, min(p1, a.steps_k), lane, cs[warp]);
-      } else {
-        run_heads<LPH, SRC, DST, INTER, SRC == DST ? kCopy : kConvert>(a, false, from, to, p0, min(p1, a.steps_k), lane,
-                                                                       nullptr);
-      }
+    if (!values && a.turn) {
+      const uint64_t old_pos = a.old_pos ? static_cast<int64_t>(a.old_pos[tok]) : 0;
+      const uint64_t new_pos = a.new_pos ? static_cast<int64_t>(a.new_pos[tok]) : 0;
+      __syncwarp();  // the previous token's values have been read
+      for (int f = lane; f < half; f += 32)
+        cs[warp][f] = cos_sin(static_cast<uint32_t>((new_pos * turns[1][f] - old_pos * turns[0][f]) >> 32));
+      __syncwarp();
+      run_heads<LPH, SRC, DST, INTER, kTurn>(a, false, from, to, lo, hi, lane, cs[warp]);
+    } else {
+      run_heads<LPH, SRC, DST, INTER, SRC == DST ? kCopy : kConvert>(a, values, from, to, lo, hi, lane, nullptr);
     }
-    if (p1 > a.steps_k)
-      run_heads<LPH, SRC, DST, INTER, SRC == DST ? kCopy : kConvert>(a, true, from, to, max(p0, a.steps_k) - a.steps_k,
-                                                                     p1 - a.steps_k, lane, nullptr);
   }
 }
 
@@ -420,9 +479,8 @@ SKV_EXPORT int skv_move_rows(int64_t n, int Hkv, int d, const skv_row_set* src, 
   a.Hkv = Hkv;
   a.rot = rot;
   a.turn = turn;
-  const int hpw = 256 / d;
-  a.steps_k = src->k ? (Hkv + hpw - 1) / hpw : 0;
-  a.steps_v = src->v ? (Hkv + hpw - 1) / hpw : 0;
+  const int hpw = 256 / d, parts = (src->k ? 1 : 0) + (src->v ? 1 : 0);
+  a.steps = (Hkv + hpw - 1) / hpw;
   a.src_rows = src_rows;
   a.dst_rows = dst_rows;
   a.old_pos = old_positions;
@@ -430,23 +488,25 @@ SKV_EXPORT int skv_move_rows(int64_t n, int Hkv, int d, const skv_row_set* src, 
   a.old_freq = old_inv_freq;
   a.new_freq = new_inv_freq;
   a.status = dev_status;
-  // Work items: a token's heads in `chunks` parts, so that the rounds of the
-  // resident warps times the steps of a part (each paying about three steps for
+  // Work items: a token's K or V heads in pieces, so that the rounds of the
+  // resident warps times the steps of a piece (each paying about three steps for
   // its rows and sines) come out lowest.
   const int64_t warps = static_cast<int64_t>(sms) * kCtasPerSm * kWarps;
-  const int steps = a.steps_k + a.steps_v;
   int64_t best = INT64_MAX;
-  for (int c = 1; c <= steps; c++) {
-    const int per = (steps + c - 1) / c, parts = (steps + per - 1) / per;
-    const int64_t cost = (n * parts + warps - 1) / warps * (per + 3);
+  int chunks = 1;
+  for (int c = 1; c <= a.steps; c++) {
+    const int per = (a.steps + c - 1) / c, pieces = (a.steps + per - 1) / per;
+    const int64_t cost = (n * parts * pieces + warps - 1) / warps * (per + 3);
     if (cost < best) {
       best = cost;
       a.chunk = per;
-      a.chunks = parts;
+      chunks = pieces;
     }
-    if (n >= 16 * warps) break;  // whole tokens
+    if (n * parts >= 16 * warps) break;  // whole tokens
   }
-  const int64_t want = (n * a.chunks + kWarps - 1) / kWarps;
+  a.chunks_k = src->k ? chunks : 0;
+  a.chunks_v = src->v ? chunks : 0;
+  const int64_t want = (n * parts * chunks + kWarps - 1) / kWarps;
   const int64_t cap = static_cast<int64_t>(sms) * kCtasPerSm;
   const int grid = static_cast<int>(want < cap ? want : cap);
   cudaStream_t st = as_stream(stream);
