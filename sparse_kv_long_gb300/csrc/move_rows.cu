@@ -92,19 +92,6 @@ __device__ __forceinline__ Raw load(const unsigned char* vec, const __half* scal
   return r;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// The larger of |a| and |b|, NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
-  return r;
-}
-
 // The eight values, exact: run a in x[0], x[1], run b in x[2], x[3].  A code
 // becomes a float as the low bits of 2^23: conversions run at an eighth of the
 // rate of the rest.
@@ -120,10 +107,11 @@ __device__ __forceinline__ void decode(const Raw& r, F2 (&x)[4]) {
       if (!(fabsf(s) <= 65504.f)) s = 0.f;  // the encodings give such a row zero codes
       float f[4];
       const uint32_t w = r.w[2 * run] ^ (KIND == SKV_KV_INT8 ? 0x80808080u : 0x8888u);  // offset binary
+      const uint32_t even = w & 0x0f0fu, odd = (w >> 4) & 0x0f0fu;  // (int4)
 #pragma unroll
       for (int e = 0; e < 4; e++)
         f[e] = __uint_as_float(KIND == SKV_KV_INT8 ? prmt(w, 0x4b000000u, 0x7650u + e)
-                                                   : ((w >> (4 * e)) & 15u) | 0x4b000000u);
+                                                   : prmt(e & 1 ? odd : even, 0x4b000000u, 0x7650u + e / 2));
       const float zero = KIND == SKV_KV_INT8 ? -8388736.f : -8388616.f;  // 2^23 and the offset
 #pragma unroll
       for (int e = 0; e < 2; e++)
@@ -137,7 +125,7 @@ __device__ __forceinline__ float amax8(const F2 (&x)[4]) {  // a NaN takes no pa
 #pragma unroll
   for (int e = 0; e < 4; e++) {
     const float2 v = f2_out(x[e]);
-    m = max3(m, fabsf(v.x), fabsf(v.y));
+    m = fmaxf(fmaxf(m, fabsf(v.x)), fabsf(v.y));
   }
   return m;
 }
@@ -152,28 +140,36 @@ __device__ __forceinline__ float factor_of(float s) {
   return !usable(s) ? 0.f : s < 6.103515625e-5f ? __uint_as_float(0x7fc00000u) : __frcp_rn(s);
 }
 
-// Four values' codes rint(x / s) as the low bits of 2^23 + 2^22.  The products
-// with the reciprocal are off by at most 127 * 3 * 2^-24 < 3e-5; where one lies
-// that near a half-integer, or is no number, the correctly rounded divisions
-// decide.
-__device__ __forceinline__ void codes_of(F2 a, F2 b, float s, float inv, int lo, int hi, uint32_t (&c)[4]) {
+// The bytes rint(x / s) of four values, by the correctly rounded divisions.
+__device__ __noinline__ uint32_t divided(float a, float b, float c, float d, float s, int lo, int hi) {
+  if (!usable(s)) return 0;
+  const float x[4] = {a, b, c, d};
+  uint32_t w = 0;
+#pragma unroll 1
+  for (int e = 0; e < 4; e++) w |= static_cast<uint32_t>(rint_clamp(__fdiv_rn(x[e], s), lo, hi) & 255) << (8 * e);
+  return w;
+}
+
+// The same from products with the reciprocal, which are off by at most 127 * 3 *
+// 2^-24 < 3e-5: rounded by adding 2^23 + 2^22; where one lies that near a
+// half-integer, or is no number, the divisions decide.
+__device__ __forceinline__ uint32_t codes_of(F2 a, F2 b, float s, float inv, int lo, int hi) {
   const F2 up = f2(12582912.f, 12582912.f), down = f2(-12582912.f, -12582912.f), i2 = f2(inv, inv), minus = f2(-1.f, -1.f);
   const F2 y0 = f2_mul(a, i2), y1 = f2_mul(b, i2);
   const F2 r0 = f2_add(y0, up), r1 = f2_add(y1, up);
-  const float2 d0 = f2_out(f2_fma(f2_add(r0, down), minus, y0)), d1 = f2_out(f2_fma(f2_add(r1, down), minus, y1));
+  const F2 d0 = f2_fma(f2_add(r0, down), minus, y0), d1 = f2_fma(f2_add(r1, down), minus, y1);
+  // squares, compared as bits: a NaN is the largest
+  const float2 e0 = f2_out(f2_mul(d0, d0)), e1 = f2_out(f2_mul(d1, d1));
+  const uint32_t worst = max(max(__float_as_uint(e0.x), __float_as_uint(e0.y)),
+                             max(__float_as_uint(e1.x), __float_as_uint(e1.y)));
   const float2 q0 = f2_out(r0), q1 = f2_out(r1);
-  c[0] = __float_as_uint(q0.x), c[1] = __float_as_uint(q0.y), c[2] = __float_as_uint(q1.x), c[3] = __float_as_uint(q1.y);
-  if (!(max_nan(max_nan(d0.x, d0.y), max_nan(d1.x, d1.y)) < 0.49995f)) {
+  uint32_t w = prmt(prmt(__float_as_uint(q0.x), __float_as_uint(q0.y), 0x0040u),
+                    prmt(__float_as_uint(q1.x), __float_as_uint(q1.y), 0x0040u), 0x5410u);
+  if (worst >= 0x3e7ff2e5u) {  // 0.49995^2
     const float2 x0 = f2_out(a), x1 = f2_out(b);
-    const float x[4] = {x0.x, x0.y, x1.x, x1.y};
-    const bool ok = usable(s);
-#pragma unroll
-    for (int e = 0; e < 4; e++) c[e] = ok ? static_cast<uint32_t>(rint_clamp(__fdiv_rn(x[e], s), lo, hi)) : 0u;
+    w = divided(x0.x, x0.y, x1.x, x1.y, s, lo, hi);
   }
-}
-
-__device__ __forceinline__ uint32_t bytes_of(const uint32_t (&c)[4]) {
-  return prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
+  return w;
 }
 
 // Encodes the heads of a batch, v[u] of step s0 + u; every lane of the warp takes
@@ -188,7 +184,7 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
     for (int u = 0; u < kBatch; u++) {
       const int h = h0 + u * HPW;
       if (u >= steps || h >= H) break;
-      unsigned char* vec = dst + h * pitch;
+      unsigned char* vec = dst + u * HPW * pitch;
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; e++) w[e] = pack2(v[u][e]);
@@ -220,12 +216,8 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
       if (u >= steps) break;
       const int from = lane - sub + u, h = h0 + u * HPW;
       const float s = __shfl_sync(0xffffffffu, s_own, from), inv = __shfl_sync(0xffffffffu, i_own, from);
-      uint32_t c[4], w[2];
-      codes_of(v[u][0], v[u][1], s, inv, -127, 127, c);
-      w[0] = bytes_of(c);
-      codes_of(v[u][2], v[u][3], s, inv, -127, 127, c);
-      w[1] = bytes_of(c);
-      unsigned char* vec = dst + h * pitch;
+      const uint32_t w[2] = {codes_of(v[u][0], v[u][1], s, inv, -127, 127), codes_of(v[u][2], v[u][3], s, inv, -127, 127)};
+      unsigned char* vec = dst + u * HPW * pitch;
       if (HPW > 1 && h >= H) continue;
       if (RUN) {
         *reinterpret_cast<uint2*>(vec + xa) = make_uint2(w[0], w[1]);
@@ -248,8 +240,8 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
         if ((lane & 7) == u) mine = m;
       } else {
         const float2 a0 = f2_out(v[u][0]), a1 = f2_out(v[u][1]), b0 = f2_out(v[u][2]), b1 = f2_out(v[u][3]);
-        const float ma = max3(max3(0.f, fabsf(a0.x), fabsf(a0.y)), fabsf(a1.x), fabsf(a1.y));
-        const float mb = max3(max3(0.f, fabsf(b0.x), fabsf(b0.y)), fabsf(b1.x), fabsf(b1.y));
+        const float ma = fmaxf(fmaxf(fmaxf(fmaxf(0.f, fabsf(a0.x)), fabsf(a0.y)), fabsf(a1.x)), fabsf(a1.y));
+        const float mb = fmaxf(fmaxf(fmaxf(fmaxf(0.f, fabsf(b0.x)), fabsf(b0.y)), fabsf(b1.x)), fabsf(b1.y));
 #pragma unroll
         for (int g = 0; g < D / 64; g++) {
           const float m = fmaxf(ga == g ? ma : 0.f, gb == g ? mb : 0.f);
@@ -261,23 +253,21 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
     const __half sh = __float2half_rn(__fdiv_rn(mine, 7.f));
     const float s_own = __half2float(sh), i_own = factor_of(s_own);
     if ((lane & 7) < steps)
-      *reinterpret_cast<uint16_t*>(dst + (h0 + (lane & 7)) * pitch + D / 2 + 2 * (lane >> 3)) = __half_as_ushort(sh);
+      *reinterpret_cast<uint16_t*>(dst + (lane & 7) * pitch + D / 2 + 2 * (lane >> 3)) = __half_as_ushort(sh);
 #pragma unroll
     for (int u = 0; u < kBatch; u++) {
       if (u >= steps) break;
-      uint32_t c[4], w[2];
+      uint32_t w[2];
       float s = __shfl_sync(0xffffffffu, s_own, 8 * ga + u), inv = __shfl_sync(0xffffffffu, i_own, 8 * ga + u);
-      codes_of(v[u][0], v[u][1], s, inv, -8, 7, c);
-      w[0] = bytes_of(c) & 0x0f0f0f0fu;
+      w[0] = codes_of(v[u][0], v[u][1], s, inv, -8, 7) & 0x0f0f0f0fu;
       if (!RUN) {
         s = __shfl_sync(0xffffffffu, s_own, 8 * gb + u);
         inv = __shfl_sync(0xffffffffu, i_own, 8 * gb + u);
       }
-      codes_of(v[u][2], v[u][3], s, inv, -8, 7, c);
-      w[1] = bytes_of(c) & 0x0f0f0f0fu;
+      w[1] = codes_of(v[u][2], v[u][3], s, inv, -8, 7) & 0x0f0f0f0fu;
       w[0] |= w[0] >> 4;  // bytes 0 and 2 hold two codes each
       w[1] |= w[1] >> 4;
-      unsigned char* vec = dst + (h0 + u) * pitch;
+      unsigned char* vec = dst + u * pitch;
       if (RUN) {
         *reinterpret_cast<uint32_t*>(vec + xa / 2) = prmt(w[0], w[1], 0x6420u);
       } else {
@@ -315,20 +305,25 @@ __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_
   unsigned char* dst = const_cast<unsigned char*>(values ? a.dst.v : a.dst.k) + to * a.dst.token_pitch;
   const __half* sscale = SRC == SKV_KV_INT8 ? (values ? a.src.v_scale : a.src.k_scale) + from * a.Hkv : nullptr;
   __half* dscale = DST == SKV_KV_INT8 ? const_cast<__half*>(values ? a.dst.v_scale : a.dst.k_scale) + to * a.Hkv : nullptr;
+  // from head to head: known but for int4 rows
+  const int64_t src_pitch = SRC == SKV_KV_BF16 ? 2 * D : SRC == SKV_KV_INT8 ? D : a.src.head_pitch;
+  const int64_t dst_pitch = DST == SKV_KV_BF16 ? 2 * D : DST == SKV_KV_INT8 ? D : a.dst.head_pitch;
   for (int s0 = lo; s0 < hi; s0 += kBatch) {
     Raw raw[kBatch];
     const int h0 = s0 * HPW + grp;
+    const unsigned char* src0 = src + h0 * src_pitch;
+    unsigned char* dst0 = dst + h0 * dst_pitch;
 #pragma unroll
     for (int u = 0; u < kBatch; u++) {  // every load of the batch first
       const int h = h0 + u * HPW;
       raw[u] = Raw{};
-      if (s0 + u < hi && (HPW == 1 || h < a.Hkv)) raw[u] = load<SRC, RUN>(src + h * a.src.head_pitch, sscale + h, xa, xb, D);
+      if (s0 + u < hi && (HPW == 1 || h < a.Hkv)) raw[u] = load<SRC, RUN>(src0 + u * HPW * src_pitch, sscale + h, xa, xb, D);
     }
     if constexpr (MODE == kCopy) {
 #pragma unroll
       for (int u = 0; u < kBatch; u++) {
         const int h = h0 + u * HPW;
-        if (s0 + u < hi && (HPW == 1 || h < a.Hkv)) store<SRC, LPH>(raw[u], dst + h * a.dst.head_pitch, dscale + h, xa);
+        if (s0 + u < hi && (HPW == 1 || h < a.Hkv)) store<SRC, LPH>(raw[u], dst0 + u * HPW * dst_pitch, dscale + h, xa);
       }
     } else {
       F2 v[kBatch][4];
@@ -356,7 +351,7 @@ __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_
           }
         }
       }
-      encode<DST, RUN, LPH>(v, dst, a.dst.head_pitch, dscale, h0, a.Hkv, min(kBatch, hi - s0), lane, xa, xb);
+      encode<DST, RUN, LPH>(v, dst0, dst_pitch, dscale, h0, a.Hkv, min(kBatch, hi - s0), lane, xa, xb);
     }
   }
 }
