@@ -95,7 +95,7 @@ __device__ __forceinline__ Raw load(const unsigned char* vec, const __half* scal
 // The eight values, exact: run a in x[0], x[1], run b in x[2], x[3].  A code
 // becomes a float as the low bits of 2^23: conversions run at an eighth of the
 // rate of the rest.
-template <int KIND>
+template <int KIND, bool RUN>
 __device__ __forceinline__ void decode(const Raw& r, F2 (&x)[4]) {
   if (KIND == SKV_KV_BF16) {
 #pragma unroll
@@ -103,7 +103,7 @@ __device__ __forceinline__ void decode(const Raw& r, F2 (&x)[4]) {
   } else {
 #pragma unroll
     for (int run = 0; run < 2; run++) {
-      float s = __half2float(__ushort_as_half(r.s[run]));
+      float s = __half2float(__ushort_as_half(r.s[RUN ? 0 : run]));
       if (!(fabsf(s) <= 65504.f)) s = 0.f;  // the encodings give such a row zero codes
       float f[4];
       const uint32_t w = r.w[2 * run] ^ (KIND == SKV_KV_INT8 ? 0x80808080u : 0x8888u);  // offset binary
@@ -120,27 +120,59 @@ __device__ __forceinline__ void decode(const Raw& r, F2 (&x)[4]) {
   }
 }
 
-__device__ __forceinline__ float amax8(const F2 (&x)[4]) {  // a NaN takes no part
+__device__ __forceinline__ float max_nan(float a, float b, float c) {  // NaN if one is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The largest absolute value of N pairs: NaN if one is, or (NUMBERS) of those that are not.
+template <bool NUMBERS, int N>
+__device__ __forceinline__ float amax(const F2* x) {
   float m = 0.f;
 #pragma unroll
-  for (int e = 0; e < 4; e++) {
+  for (int e = 0; e < N; e++) {
     const float2 v = f2_out(x[e]);
-    m = fmaxf(fmaxf(m, fabsf(v.x)), fabsf(v.y));
+    m = NUMBERS ? fmaxf(fmaxf(m, fabsf(v.x)), fabsf(v.y)) : max_nan(m, fabsf(v.x), fabsf(v.y));
   }
   return m;
+}
+
+// The largest of each `LANES` lanes, as bits: a NaN is above the numbers.
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float m) {
+  uint32_t b = __float_as_uint(m);
+  if (LANES == 32) return __uint_as_float(__reduce_max_sync(0xffffffffu, b));
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
+  return __uint_as_float(b);
 }
 
 // A zero or infinite scale gives zero codes.
 __device__ __forceinline__ bool usable(float s) { return s != 0.f && s < 3.0e38f; }
 
-// A scale and what the values are multiplied with: its reciprocal, 0 where the
-// codes are zero, NaN where fp16's small numbers hold the scale too coarsely for
-// the largest code to stay in range by itself.
-__device__ __forceinline__ float factor_of(float s) {
-  return !usable(s) ? 0.f : s < 6.103515625e-5f ? __uint_as_float(0x7fc00000u) : __frcp_rn(s);
+// fp16(m / top), as the division rounded to fp32 and then to fp16 gives it.  The
+// product with 1 / top is within three steps of the quotient, so the two round
+// alike unless that near to the middle between two fp16 numbers.
+template <int TOP>
+__device__ __forceinline__ __half scale_of(float m) {
+  float q = m * (1.f / TOP);
+  const uint32_t rest = __float_as_uint(q) & 0x1fffu;  // beyond fp16's ten bits
+  if (rest - 0x0ff8u <= 0x10u || !(q >= 6.2e-5f)) q = __fdiv_rn(m, static_cast<float>(TOP));
+  return __float2half_rn(q);
 }
 
-// The bytes rint(x / s) of four values, by the correctly rounded divisions.
+// What values of a scale are multiplied with: its reciprocal (to 2^-23), or NaN
+// where the divisions decide: where fp16's small numbers hold the scale too
+// coarsely for the largest code to stay in range by itself, and (`odd`) beside
+// values that are no numbers.
+__device__ __forceinline__ float factor_of(float s, bool odd) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return s >= 6.103515625e-5f && usable(s) && !odd ? r : s == 0.f && !odd ? 0.f : __uint_as_float(0x7fc00000u);
+}
+
+// rint(x / s) of four values as bytes, by the correctly rounded divisions.
 __device__ __noinline__ uint32_t divided(float a, float b, float c, float d, float s, int lo, int hi) {
   if (!usable(s)) return 0;
   const float x[4] = {a, b, c, d};
@@ -150,26 +182,61 @@ __device__ __noinline__ uint32_t divided(float a, float b, float c, float d, flo
   return w;
 }
 
-// The same from products with the reciprocal, which are off by at most 127 * 3 *
-// 2^-24 < 3e-5: rounded by adding 2^23 + 2^22; where one lies that near a
-// half-integer, or is no number, the divisions decide.
-__device__ __forceinline__ uint32_t codes_of(F2 a, F2 b, float s, float inv, int lo, int hi) {
-  const F2 up = f2(12582912.f, 12582912.f), down = f2(-12582912.f, -12582912.f), i2 = f2(inv, inv), minus = f2(-1.f, -1.f);
-  const F2 y0 = f2_mul(a, i2), y1 = f2_mul(b, i2);
-  const F2 r0 = f2_add(y0, up), r1 = f2_add(y1, up);
-  const F2 d0 = f2_fma(f2_add(r0, down), minus, y0), d1 = f2_fma(f2_add(r1, down), minus, y1);
-  // squares, compared as bits: a NaN is the largest
-  const float2 e0 = f2_out(f2_mul(d0, d0)), e1 = f2_out(f2_mul(d1, d1));
-  const uint32_t worst = max(max(__float_as_uint(e0.x), __float_as_uint(e0.y)),
-                             max(__float_as_uint(e1.x), __float_as_uint(e1.y)));
+// The same from products with the reciprocal, rounded by adding 2^23 + 2^22.  They
+// are off from the rounded quotients by at most 2^-23 (the reciprocal) and 2^-24
+// (the quotient) of up to TOP: `off`, the largest distance from a product to its
+// code, says whether one lies that near a half-integer.  (With a factor of NaN
+// every distance is NaN.)
+template <int TOP>
+constexpr float kSafe = 0.5f - TOP * 2.2e-7f;
+__device__ __forceinline__ uint32_t codes_of(F2 a, F2 b, F2 inv, F2 minus_inv, float& off) {
+  const F2 up = f2(12582912.f, 12582912.f), down = f2(-12582912.f, -12582912.f);
+  const F2 r0 = f2_fma(a, inv, up), r1 = f2_fma(b, inv, up);
+  const float2 d0 = f2_out(f2_fma(a, minus_inv, f2_add(r0, down))), d1 = f2_out(f2_fma(b, minus_inv, f2_add(r1, down)));
+  off = fmaxf(fmaxf(fmaxf(fabsf(d0.x), fabsf(d0.y)), fabsf(d1.x)), fabsf(d1.y));
   const float2 q0 = f2_out(r0), q1 = f2_out(r1);
-  uint32_t w = prmt(prmt(__float_as_uint(q0.x), __float_as_uint(q0.y), 0x0040u),
-                    prmt(__float_as_uint(q1.x), __float_as_uint(q1.y), 0x0040u), 0x5410u);
-  if (worst >= 0x3e7ff2e5u) {  // 0.49995^2
-    const float2 x0 = f2_out(a), x1 = f2_out(b);
-    w = divided(x0.x, x0.y, x1.x, x1.y, s, lo, hi);
+  return prmt(prmt(__float_as_uint(q0.x), __float_as_uint(q0.y), 0x0040u),
+              prmt(__float_as_uint(q1.x), __float_as_uint(q1.y), 0x0040u), 0x5410u);
+}
+
+// The codes of a step's two runs, of scales that lanes la and lb hold.
+template <int TOP, bool ONE>  // one scale for both
+__device__ __forceinline__ void codes_of(const F2 (&v)[4], float s_own, float i_own, int la, int lb, uint32_t (&w)[2]) {
+  constexpr uint32_t full = 0xffffffffu;
+  constexpr int lo = TOP == 7 ? -8 : -TOP;
+  const float ia = __shfl_sync(full, i_own, la), ib = ONE ? ia : __shfl_sync(full, i_own, lb);
+  float oa, ob;
+  w[0] = codes_of(v[0], v[1], f2(ia, ia), f2(-ia, -ia), oa);
+  w[1] = codes_of(v[2], v[3], f2(ib, ib), f2(-ib, -ib), ob);
+  const bool good = fmaxf(oa, ob) < kSafe<TOP>;  // (both are NaN, or none)
+  if (__any_sync(full, ONE ? !good : !(oa < kSafe<TOP>) || !(ob < kSafe<TOP>))) {
+    const float sa = __shfl_sync(full, s_own, la), sb = ONE ? sa : __shfl_sync(full, s_own, lb);
+    const float2 x0 = f2_out(v[0]), x1 = f2_out(v[1]), x2 = f2_out(v[2]), x3 = f2_out(v[3]);
+    if (!(oa < kSafe<TOP>)) w[0] = divided(x0.x, x0.y, x1.x, x1.y, sa, lo, TOP);
+    if (!(ob < kSafe<TOP>)) w[1] = divided(x2.x, x2.y, x3.x, x3.y, sb, lo, TOP);
   }
-  return w;
+}
+
+// This lane's scale's largest value: lane `sub` of LANES holds the one of step
+// sub.  NaN takes no part, but marks the value with a minus: the divisions will
+// see to its code.
+template <int LANES>
+__device__ __forceinline__ float scale_max(const F2 (&v)[kBatch][4], int sub) {
+  float mine = 0.f, all = 0.f;
+#pragma unroll
+  for (int u = 0; u < kBatch; u++) {
+    const float m = lanes_max<LANES>(amax<false, 4>(v[u]));
+    if (sub == u) mine = m;
+    all += m;  // not finite where one is not
+  }
+  if (__any_sync(0xffffffffu, !(all < INFINITY))) {
+#pragma unroll
+    for (int u = 0; u < kBatch; u++) {
+      const float m = lanes_max<LANES>(amax<true, 4>(v[u]));
+      if (sub == u && mine != mine) mine = -m;
+    }
+  }
+  return mine;
 }
 
 // Encodes the heads of a batch, v[u] of step s0 + u; every lane of the warp takes
@@ -196,27 +263,16 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
       }
     }
   } else if (KIND == SKV_KV_INT8) {
-    float mine = 0.f;
-#pragma unroll
-    for (int u = 0; u < kBatch; u++) {
-      float m = amax8(v[u]);
-      if (LPH == 32) {  // as bits: neither NaN nor negative
-        m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-      } else {
-#pragma unroll
-        for (int o = LPH / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      }
-      if (sub == u) mine = m;
-    }
-    const __half sh = __float2half_rn(__fdiv_rn(mine, 127.f));
-    const float s_own = __half2float(sh), i_own = factor_of(s_own);
+    const float mine = scale_max<LPH>(v, sub);
+    const __half sh = scale_of<127>(fabsf(mine));
+    const float s_own = __half2float(sh), i_own = factor_of(s_own, __float_as_uint(mine) >> 31);
     if (sub < steps && h0 + sub * HPW < H) scale[h0 + sub * HPW] = sh;
 #pragma unroll
     for (int u = 0; u < kBatch; u++) {
       if (u >= steps) break;
       const int from = lane - sub + u, h = h0 + u * HPW;
-      const float s = __shfl_sync(0xffffffffu, s_own, from), inv = __shfl_sync(0xffffffffu, i_own, from);
-      const uint32_t w[2] = {codes_of(v[u][0], v[u][1], s, inv, -127, 127), codes_of(v[u][2], v[u][3], s, inv, -127, 127)};
+      uint32_t w[2];
+      codes_of<127, true>(v[u], s_own, i_own, from, from, w);
       unsigned char* vec = dst + u * HPW * pitch;
       if (HPW > 1 && h >= H) continue;
       if (RUN) {
@@ -231,40 +287,40 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
     // Lane 8 g + u: the scale of group g of step u.
     const int ga = xa >> 6, gb = xb >> 6;
     float mine = 0.f;
+    if constexpr (RUN) {
+      mine = scale_max<8>(v, lane & 7);
+    } else {
 #pragma unroll
-    for (int u = 0; u < kBatch; u++) {
-      if (RUN) {
-        float m = amax8(v[u]);
-#pragma unroll
-        for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((lane & 7) == u) mine = m;
-      } else {
-        const float2 a0 = f2_out(v[u][0]), a1 = f2_out(v[u][1]), b0 = f2_out(v[u][2]), b1 = f2_out(v[u][3]);
-        const float ma = fmaxf(fmaxf(fmaxf(fmaxf(0.f, fabsf(a0.x)), fabsf(a0.y)), fabsf(a1.x)), fabsf(a1.y));
-        const float mb = fmaxf(fmaxf(fmaxf(fmaxf(0.f, fabsf(b0.x)), fabsf(b0.y)), fabsf(b1.x)), fabsf(b1.y));
+      for (int u = 0; u < kBatch; u++) {
+        const float ma = amax<false, 2>(&v[u][0]), mb = amax<false, 2>(&v[u][2]);
+        bool nan = false;
 #pragma unroll
         for (int g = 0; g < D / 64; g++) {
-          const float m = fmaxf(ga == g ? ma : 0.f, gb == g ? mb : 0.f);
-          const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+          const float all = lanes_max<32>(max_nan(ga == g ? ma : 0.f, gb == g ? mb : 0.f, 0.f));
           if (lane == 8 * g + u) mine = all;
+          nan |= all != all;
+        }
+        if (nan) {
+          const float na = amax<true, 2>(&v[u][0]), nb = amax<true, 2>(&v[u][2]);
+#pragma unroll 1
+          for (int g = 0; g < D / 64; g++) {
+            const float all = lanes_max<32>(fmaxf(ga == g ? na : 0.f, gb == g ? nb : 0.f));
+            if (lane == 8 * g + u && mine != mine) mine = -all;
+          }
         }
       }
     }
-    const __half sh = __float2half_rn(__fdiv_rn(mine, 7.f));
-    const float s_own = __half2float(sh), i_own = factor_of(s_own);
+    const __half sh = scale_of<7>(fabsf(mine));
+    const float s_own = __half2float(sh), i_own = factor_of(s_own, __float_as_uint(mine) >> 31);
     if ((lane & 7) < steps)
       *reinterpret_cast<uint16_t*>(dst + (lane & 7) * pitch + D / 2 + 2 * (lane >> 3)) = __half_as_ushort(sh);
 #pragma unroll
     for (int u = 0; u < kBatch; u++) {
       if (u >= steps) break;
       uint32_t w[2];
-      float s = __shfl_sync(0xffffffffu, s_own, 8 * ga + u), inv = __shfl_sync(0xffffffffu, i_own, 8 * ga + u);
-      w[0] = codes_of(v[u][0], v[u][1], s, inv, -8, 7) & 0x0f0f0f0fu;
-      if (!RUN) {
-        s = __shfl_sync(0xffffffffu, s_own, 8 * gb + u);
-        inv = __shfl_sync(0xffffffffu, i_own, 8 * gb + u);
-      }
-      w[1] = codes_of(v[u][2], v[u][3], s, inv, -8, 7) & 0x0f0f0f0fu;
+      codes_of<7, RUN>(v[u], s_own, i_own, 8 * ga + u, 8 * gb + u, w);
+      w[0] &= 0x0f0f0f0fu;
+      w[1] &= 0x0f0f0f0fu;
       w[0] |= w[0] >> 4;  // bytes 0 and 2 hold two codes each
       w[1] |= w[1] >> 4;
       unsigned char* vec = dst + u * pitch;
@@ -313,11 +369,16 @@ __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_
     const int h0 = s0 * HPW + grp;
     const unsigned char* src0 = src + h0 * src_pitch;
     unsigned char* dst0 = dst + h0 * dst_pitch;
+    if (s0 + kBatch <= hi && (HPW == 1 || (s0 + kBatch) * HPW <= a.Hkv)) {  // every load of the batch first
 #pragma unroll
-    for (int u = 0; u < kBatch; u++) {  // every load of the batch first
-      const int h = h0 + u * HPW;
-      raw[u] = Raw{};
-      if (s0 + u < hi && (HPW == 1 || h < a.Hkv)) raw[u] = load<SRC, RUN>(src0 + u * HPW * src_pitch, sscale + h, xa, xb, D);
+      for (int u = 0; u < kBatch; u++) raw[u] = load<SRC, RUN>(src0 + u * HPW * src_pitch, sscale + h0 + u * HPW, xa, xb, D);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kBatch; u++) {
+        const int h = h0 + u * HPW;
+        raw[u] = Raw{};
+        if (s0 + u < hi && h < a.Hkv) raw[u] = load<SRC, RUN>(src0 + u * HPW * src_pitch, sscale + h, xa, xb, D);
+      }
     }
     if constexpr (MODE == kCopy) {
 #pragma unroll
@@ -328,7 +389,7 @@ __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_
     } else {
       F2 v[kBatch][4];
 #pragma unroll
-      for (int u = 0; u < kBatch; u++) decode<SRC>(raw[u], v[u]);
+      for (int u = 0; u < kBatch; u++) decode<SRC, RUN>(raw[u], v[u]);
       if constexpr (MODE == kTurn) {
         if (rotated) {  // elsewhere an infinite neighbour would make 0 * inf
 #pragma unroll
