@@ -52,7 +52,8 @@ struct MoveArgs {
 enum Mode { kCopy, kConvert, kTurn };
 
 // A lane's eight values as they lie in a row: bf16 words 0, 1 at dims xa .. and
-// 2, 3 at dims xb ..; int8 words 0 and 2; int4 the low halves of words 0 and 2.
+// 2, 3 at dims xb ..; int8 words 0 and 2; int4 (RUN) word 0, else the low halves of
+// words 0 and 2.
 struct Raw {
   uint32_t w[4];
   uint16_t s[2];  // scales of the two runs
@@ -80,8 +81,7 @@ __device__ __forceinline__ Raw load(const unsigned char* vec, const __half* scal
     r.s[0] = r.s[1] = *reinterpret_cast<const uint16_t*>(scale);
   } else {
     if (RUN) {
-      const uint32_t x = *reinterpret_cast<const uint32_t*>(vec + xa / 2);
-      r.w[0] = x & 0xffffu, r.w[2] = x >> 16;
+      r.w[0] = *reinterpret_cast<const uint32_t*>(vec + xa / 2);
     } else {
       r.w[0] = *reinterpret_cast<const uint16_t*>(vec + xa / 2);
       r.w[2] = *reinterpret_cast<const uint16_t*>(vec + xb / 2);
@@ -101,24 +101,78 @@ __device__ __forceinline__ void decode(const Raw& r, F2 (&x)[4]) {
 #pragma unroll
     for (int e = 0; e < 4; e++) x[e] = unpack2(r.w[e]);
   } else {
+    const float zero = KIND == SKV_KV_INT8 ? -8388736.f : -8388616.f;  // 2^23 and the codes' offset
+    float s[2], f[8];
 #pragma unroll
     for (int run = 0; run < 2; run++) {
-      float s = __half2float(__ushort_as_half(r.s[RUN ? 0 : run]));
-      if (!(fabsf(s) <= 65504.f)) s = 0.f;  // the encodings give such a row zero codes
-      float f[4];
-      const uint32_t w = r.w[2 * run] ^ (KIND == SKV_KV_INT8 ? 0x80808080u : 0x8888u);  // offset binary
-      const uint32_t even = w & 0x0f0fu, odd = (w >> 4) & 0x0f0fu;  // (int4)
+      s[run] = run && RUN ? s[0] : __half2float(__ushort_as_half(r.s[run]));
+      if (!(fabsf(s[run]) <= 65504.f)) s[run] = 0.f;  // the encodings give such a row zero codes
+      if (KIND == SKV_KV_INT8) {
+        const uint32_t w = r.w[2 * run] ^ 0x80808080u;
 #pragma unroll
-      for (int e = 0; e < 4; e++)
-        f[e] = __uint_as_float(KIND == SKV_KV_INT8 ? prmt(w, 0x4b000000u, 0x7650u + e)
-                                                   : prmt(e & 1 ? odd : even, 0x4b000000u, 0x7650u + e / 2));
-      const float zero = KIND == SKV_KV_INT8 ? -8388736.f : -8388616.f;  // 2^23 and the offset
+        for (int e = 0; e < 4; e++) f[4 * run + e] = __uint_as_float(prmt(w, 0x4b000000u, 0x7650u + e));
+      } else {
+        const uint32_t w = (RUN ? r.w[0] : r.w[2 * run]) ^ 0x88888888u;
+        const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
 #pragma unroll
-      for (int e = 0; e < 2; e++)
-        x[2 * run + e] = f2_mul(f2_add(f2(f[2 * e], f[2 * e + 1]), f2(zero, zero)), f2(s, s));
+        for (int e = 0; e < 4; e++)
+          f[4 * run + e] = __uint_as_float(prmt(e & 1 ? odd : even, 0x4b000000u, 0x7650u + e / 2 + (RUN ? 2 * run : 0)));
+      }
     }
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      x[e] = f2_mul(f2_add(f2(f[2 * e], f[2 * e + 1]), f2(zero, zero)), f2(s[e / 2], s[e / 2]));
   }
 }
+
+// The largest absolute value of N pairs; a NaN takes no part.
+template <int N>
+__device__ __forceinline__ float amax(const F2* x) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < N; e++) {
+    const float2 v = f2_out(x[e]);
+    m = fmaxf(fmaxf(m, fabsf(v.x)), fabsf(v.y));
+  }
+  return m;
+}
+
+// The largest of each LANES lanes (not negative, no NaN).
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float m) {
+  if (LANES == 32) return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// This lane's scale's largest value: lane `sub` of LANES holds the one of step sub.
+template <int LANES>
+__device__ __forceinline__ float scale_max(const F2 (&v)[kBatch][4], int sub) {
+  float mine = 0.f;
+#pragma unroll
+  for (int u = 0; u < kBatch; u++) {
+    const float m = lanes_max<LANES>(amax<4>(v[u]));
+    if (sub == u) mine = m;
+  }
+  return mine;
+}
+
+// fp16(m / TOP), the quotient rounded to fp32 and then to fp16: q0 = m c with c =
+// 1 / TOP rounded, and q0 + (m - TOP q0) c, which rounds as the quotient does
+// (Markstein's correction; tried for every mantissa of m).  A quotient too small
+// for that is zero in fp16, and an infinite m is replaced by the largest number,
+// whose quotient is beyond fp16, too.
+template <int TOP>
+__device__ __forceinline__ __half scale_of(float m) {
+  constexpr float c = 1.f / TOP;
+  m = fminf(m, 3.402823466e38f);
+  const float q0 = m * c;
+  return __float2half_rn(fmaf(fmaf(-q0, static_cast<float>(TOP), m), c, q0));
+}
+
+// A zero or infinite scale gives zero codes.
+__device__ __forceinline__ bool usable(float s) { return s != 0.f && s < 3.0e38f; }
 
 __device__ __forceinline__ float max_nan(float a, float b, float c) {  // NaN if one is
   float r;
@@ -126,117 +180,70 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {  // NaN if
   return r;
 }
 
-// The largest absolute value of N pairs: NaN if one is, or (NUMBERS) of those that are not.
-template <bool NUMBERS, int N>
-__device__ __forceinline__ float amax(const F2* x) {
-  float m = 0.f;
+// The codes rint(x / s) of a run's four values, clamped, as bytes.  x is multiplied
+// with the reciprocal and rounded to r by adding 2^23 + 2^22; the remainder x - r s
+// is exact (r s has 19 bits) and below s / 2 wherever r is the nearest integer.
+// `off` is the largest remainder, NaN where there is none.  (The values of bf16,
+// int8 and int4 rows are too coarse for the quotient's own rounding to meet a
+// half-integer that it is not, so this is the rounded quotient's code, too.)
+struct Codes {
+  F2 r[2], e[2];
+};
+__device__ __forceinline__ float try_codes(const F2* x, float s, float inv, Codes& c) {
+  const F2 up = f2(12582912.f, 12582912.f), down = f2(-12582912.f, -12582912.f), i2 = f2(inv, inv), ms = f2(-s, -s);
 #pragma unroll
-  for (int e = 0; e < N; e++) {
-    const float2 v = f2_out(x[e]);
-    m = NUMBERS ? fmaxf(fmaxf(m, fabsf(v.x)), fabsf(v.y)) : max_nan(m, fabsf(v.x), fabsf(v.y));
+  for (int p = 0; p < 2; p++) {
+    c.r[p] = f2_fma(x[p], i2, up);
+    c.e[p] = f2_fma(f2_add(c.r[p], down), ms, x[p]);
   }
-  return m;
+  const float2 e0 = f2_out(c.e[0]), e1 = f2_out(c.e[1]);
+  return max_nan(max_nan(0.f, fabsf(e0.x), fabsf(e0.y)), fabsf(e1.x), fabsf(e1.y));
 }
-
-// The largest of each `LANES` lanes, as bits: a NaN is above the numbers.
-template <int LANES>
-__device__ __forceinline__ float lanes_max(float m) {
-  uint32_t b = __float_as_uint(m);
-  if (LANES == 32) return __uint_as_float(__reduce_max_sync(0xffffffffu, b));
-#pragma unroll
-  for (int o = LANES / 2; o; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
-  return __uint_as_float(b);
+__device__ __forceinline__ uint32_t bytes_of(const Codes& c) {
+  const float2 a = f2_out(c.r[0]), b = f2_out(c.r[1]);
+  return prmt(prmt(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040u),
+              prmt(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040u), 0x5410u);
 }
-
-// A zero or infinite scale gives zero codes.
-__device__ __forceinline__ bool usable(float s) { return s != 0.f && s < 3.0e38f; }
-
-// fp16(m / top), as the division rounded to fp32 and then to fp16 gives it.  The
-// product with 1 / top is within three steps of the quotient, so the two round
-// alike unless that near to the middle between two fp16 numbers.
+// Where a remainder is s / 2 (ties go to the even code) or more, a value is no
+// number, or the scale is so small that fp16 holds it too coarsely for the largest
+// code to stay in range by itself.
 template <int TOP>
-__device__ __forceinline__ __half scale_of(float m) {
-  float q = m * (1.f / TOP);
-  const uint32_t rest = __float_as_uint(q) & 0x1fffu;  // beyond fp16's ten bits
-  if (rest - 0x0ff8u <= 0x10u || !(q >= 6.2e-5f)) q = __fdiv_rn(m, static_cast<float>(TOP));
-  return __float2half_rn(q);
-}
-
-// What values of a scale are multiplied with: its reciprocal (to 2^-23), or NaN
-// where the divisions decide: where fp16's small numbers hold the scale too
-// coarsely for the largest code to stay in range by itself, and (`odd`) beside
-// values that are no numbers.
-__device__ __forceinline__ float factor_of(float s, bool odd) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  return s >= 6.103515625e-5f && usable(s) && !odd ? r : s == 0.f && !odd ? 0.f : __uint_as_float(0x7fc00000u);
-}
-
-// rint(x / s) of four values as bytes, by the correctly rounded divisions.
-__device__ __noinline__ uint32_t divided(float a, float b, float c, float d, float s, int lo, int hi) {
-  if (!usable(s)) return 0;
-  const float x[4] = {a, b, c, d};
+__device__ __forceinline__ uint32_t other_codes(const Codes& c, const F2* x, float s) {
+  constexpr int lo = TOP == 7 ? -8 : -TOP;
   uint32_t w = 0;
-#pragma unroll 1
-  for (int e = 0; e < 4; e++) w |= static_cast<uint32_t>(rint_clamp(__fdiv_rn(x[e], s), lo, hi) & 255) << (8 * e);
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const float2 rr = f2_out(c.r[i / 2]), ee = f2_out(c.e[i / 2]), xx = f2_out(x[i / 2]);
+    const float r = i & 1 ? rr.y : rr.x, e = i & 1 ? ee.y : ee.x, v = i & 1 ? xx.y : xx.x;
+    int q = static_cast<int>(__float_as_uint(r)) - 0x4b400000;
+    if (fabsf(e) > 0.5f * s || (fabsf(e) == 0.5f * s && (q & 1))) q += e > 0.f ? 1 : -1;
+    q = v != v ? lo : min(max(q, lo), TOP);
+    if (usable(s)) w |= static_cast<uint32_t>(q & 255) << (8 * i);
+  }
   return w;
-}
-
-// The same from products with the reciprocal, rounded by adding 2^23 + 2^22.  They
-// are off from the rounded quotients by at most 2^-23 (the reciprocal) and 2^-24
-// (the quotient) of up to TOP: `off`, the largest distance from a product to its
-// code, says whether one lies that near a half-integer.  (With a factor of NaN
-// every distance is NaN.)
-template <int TOP>
-constexpr float kSafe = 0.5f - TOP * 2.2e-7f;
-__device__ __forceinline__ uint32_t codes_of(F2 a, F2 b, F2 inv, F2 minus_inv, float& off) {
-  const F2 up = f2(12582912.f, 12582912.f), down = f2(-12582912.f, -12582912.f);
-  const F2 r0 = f2_fma(a, inv, up), r1 = f2_fma(b, inv, up);
-  const float2 d0 = f2_out(f2_fma(a, minus_inv, f2_add(r0, down))), d1 = f2_out(f2_fma(b, minus_inv, f2_add(r1, down)));
-  off = fmaxf(fmaxf(fmaxf(fabsf(d0.x), fabsf(d0.y)), fabsf(d1.x)), fabsf(d1.y));
-  const float2 q0 = f2_out(r0), q1 = f2_out(r1);
-  return prmt(prmt(__float_as_uint(q0.x), __float_as_uint(q0.y), 0x0040u),
-              prmt(__float_as_uint(q1.x), __float_as_uint(q1.y), 0x0040u), 0x5410u);
 }
 
 // The codes of a step's two runs, of scales that lanes la and lb hold.
 template <int TOP, bool ONE>  // one scale for both
 __device__ __forceinline__ void codes_of(const F2 (&v)[4], float s_own, float i_own, int la, int lb, uint32_t (&w)[2]) {
   constexpr uint32_t full = 0xffffffffu;
-  constexpr int lo = TOP == 7 ? -8 : -TOP;
-  const float ia = __shfl_sync(full, i_own, la), ib = ONE ? ia : __shfl_sync(full, i_own, lb);
-  float oa, ob;
-  w[0] = codes_of(v[0], v[1], f2(ia, ia), f2(-ia, -ia), oa);
-  w[1] = codes_of(v[2], v[3], f2(ib, ib), f2(-ib, -ib), ob);
-  const bool good = fmaxf(oa, ob) < kSafe<TOP>;  // (both are NaN, or none)
-  if (__any_sync(full, ONE ? !good : !(oa < kSafe<TOP>) || !(ob < kSafe<TOP>))) {
-    const float sa = __shfl_sync(full, s_own, la), sb = ONE ? sa : __shfl_sync(full, s_own, lb);
-    const float2 x0 = f2_out(v[0]), x1 = f2_out(v[1]), x2 = f2_out(v[2]), x3 = f2_out(v[3]);
-    if (!(oa < kSafe<TOP>)) w[0] = divided(x0.x, x0.y, x1.x, x1.y, sa, lo, TOP);
-    if (!(ob < kSafe<TOP>)) w[1] = divided(x2.x, x2.y, x3.x, x3.y, sb, lo, TOP);
+  const float sa = __shfl_sync(full, s_own, la), ia = __shfl_sync(full, i_own, la);
+  const float sb = ONE ? sa : __shfl_sync(full, s_own, lb), ib = ONE ? ia : __shfl_sync(full, i_own, lb);
+  Codes a, b;
+  const float oa = try_codes(&v[0], sa, ia, a), ob = try_codes(&v[2], sb, ib, b);
+  w[0] = bytes_of(a);
+  w[1] = bytes_of(b);
+  const float ha = sa < 6.103515625e-5f ? -1.f : 0.5f * sa, hb = ONE ? ha : sb < 6.103515625e-5f ? -1.f : 0.5f * sb;
+  if (!(oa < ha) || !(ob < hb)) {
+    w[0] = other_codes<TOP>(a, &v[0], sa);
+    w[1] = other_codes<TOP>(b, &v[2], sb);
   }
 }
 
-// This lane's scale's largest value: lane `sub` of LANES holds the one of step
-// sub.  NaN takes no part, but marks the value with a minus: the divisions will
-// see to its code.
-template <int LANES>
-__device__ __forceinline__ float scale_max(const F2 (&v)[kBatch][4], int sub) {
-  float mine = 0.f, all = 0.f;
-#pragma unroll
-  for (int u = 0; u < kBatch; u++) {
-    const float m = lanes_max<LANES>(amax<false, 4>(v[u]));
-    if (sub == u) mine = m;
-    all += m;  // not finite where one is not
-  }
-  if (__any_sync(0xffffffffu, !(all < INFINITY))) {
-#pragma unroll
-    for (int u = 0; u < kBatch; u++) {
-      const float m = lanes_max<LANES>(amax<true, 4>(v[u]));
-      if (sub == u && mine != mine) mine = -m;
-    }
-  }
-  return mine;
+__device__ __forceinline__ float reciprocal(float s) {  // to 2^-23
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
 }
 
 // Encodes the heads of a batch, v[u] of step s0 + u; every lane of the warp takes
@@ -264,8 +271,8 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
     }
   } else if (KIND == SKV_KV_INT8) {
     const float mine = scale_max<LPH>(v, sub);
-    const __half sh = scale_of<127>(fabsf(mine));
-    const float s_own = __half2float(sh), i_own = factor_of(s_own, __float_as_uint(mine) >> 31);
+    const __half sh = scale_of<127>(mine);
+    const float s_own = __half2float(sh), i_own = reciprocal(s_own);
     if (sub < steps && h0 + sub * HPW < H) scale[h0 + sub * HPW] = sh;
 #pragma unroll
     for (int u = 0; u < kBatch; u++) {
@@ -292,26 +299,16 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
     } else {
 #pragma unroll
       for (int u = 0; u < kBatch; u++) {
-        const float ma = amax<false, 2>(&v[u][0]), mb = amax<false, 2>(&v[u][2]);
-        bool nan = false;
+        const float ma = amax<2>(&v[u][0]), mb = amax<2>(&v[u][2]);
 #pragma unroll
         for (int g = 0; g < D / 64; g++) {
-          const float all = lanes_max<32>(max_nan(ga == g ? ma : 0.f, gb == g ? mb : 0.f, 0.f));
+          const float all = lanes_max<32>(fmaxf(ga == g ? ma : 0.f, gb == g ? mb : 0.f));
           if (lane == 8 * g + u) mine = all;
-          nan |= all != all;
-        }
-        if (nan) {
-          const float na = amax<true, 2>(&v[u][0]), nb = amax<true, 2>(&v[u][2]);
-#pragma unroll 1
-          for (int g = 0; g < D / 64; g++) {
-            const float all = lanes_max<32>(fmaxf(ga == g ? na : 0.f, gb == g ? nb : 0.f));
-            if (lane == 8 * g + u && mine != mine) mine = -all;
-          }
         }
       }
     }
-    const __half sh = scale_of<7>(fabsf(mine));
-    const float s_own = __half2float(sh), i_own = factor_of(s_own, __float_as_uint(mine) >> 31);
+    const __half sh = scale_of<7>(mine);
+    const float s_own = __half2float(sh), i_own = reciprocal(s_own);
     if ((lane & 7) < steps)
       *reinterpret_cast<uint16_t*>(dst + (lane & 7) * pitch + D / 2 + 2 * (lane >> 3)) = __half_as_ushort(sh);
 #pragma unroll
@@ -343,7 +340,7 @@ __device__ __forceinline__ void store(const Raw& r, unsigned char* vec, __half* 
     *reinterpret_cast<uint2*>(vec + xa) = make_uint2(r.w[0], r.w[2]);
     if (xa == 0) *reinterpret_cast<uint16_t*>(scale) = r.s[0];
   } else {
-    *reinterpret_cast<uint32_t*>(vec + xa / 2) = r.w[0] | r.w[2] << 16;
+    *reinterpret_cast<uint32_t*>(vec + xa / 2) = r.w[0];
     if ((xa & 63) == 0) *reinterpret_cast<uint16_t*>(vec + 4 * LPH + (xa >> 6) * 2) = r.s[0];
   }
 }
