@@ -928,7 +928,7 @@ typedef struct skv_row_set {
  * A row of one cache may be its own destination (keys turned in place: the same
  * addresses on both sides); otherwise no destination overlaps a source.
  * Constraints: d in {64, 128, 256}, 256 with int4 rows; rot a multiple of 16, 0 <=
- * rot <= d; Hkv <= 4096; bf16 and int8 rows 16-byte aligned; int4 rows and pitches
+ * rot <= d; Hkv <= 4096; n <= 2^29; bf16 and int8 rows 16-byte aligned; int4 rows and pitches
  * multiples of 4, head_pitch >= d/2 + d/32, token_pitch >= Hkv*head_pitch.
  * Errors: SKV_EUNSUPPORTED for another d, SKV_EINVAL for the rest.
  */

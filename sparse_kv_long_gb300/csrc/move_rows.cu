@@ -27,7 +27,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4;
-constexpr int kBatch = 4;  // heads per lane group whose loads are in flight together
+constexpr int kLoad = 4;   // heads per lane group whose loads are in flight together
+constexpr int kBatch = 2;  // of them decoded and encoded together
 
 struct RowSet {
   const unsigned char *k, *v;  // (written through on the destination's side)
@@ -361,17 +362,17 @@ __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_
   // from head to head: known but for int4 rows
   const int64_t src_pitch = SRC == SKV_KV_BF16 ? 2 * D : SRC == SKV_KV_INT8 ? D : a.src.head_pitch;
   const int64_t dst_pitch = DST == SKV_KV_BF16 ? 2 * D : DST == SKV_KV_INT8 ? D : a.dst.head_pitch;
-  for (int s0 = lo; s0 < hi; s0 += kBatch) {
-    Raw raw[kBatch];
+  for (int s0 = lo; s0 < hi; s0 += kLoad) {
+    Raw raw[kLoad];
     const int h0 = s0 * HPW + grp;
     const unsigned char* src0 = src + h0 * src_pitch;
     unsigned char* dst0 = dst + h0 * dst_pitch;
-    if (s0 + kBatch <= hi && (HPW == 1 || (s0 + kBatch) * HPW <= a.Hkv)) {  // every load of the batch first
+    if (s0 + kLoad <= hi && (HPW == 1 || (s0 + kLoad) * HPW <= a.Hkv)) {  // every load first
 #pragma unroll
-      for (int u = 0; u < kBatch; u++) raw[u] = load<SRC, RUN>(src0 + u * HPW * src_pitch, sscale + h0 + u * HPW, xa, xb, D);
+      for (int u = 0; u < kLoad; u++) raw[u] = load<SRC, RUN>(src0 + u * HPW * src_pitch, sscale + h0 + u * HPW, xa, xb, D);
     } else {
 #pragma unroll
-      for (int u = 0; u < kBatch; u++) {
+      for (int u = 0; u < kLoad; u++) {
         const int h = h0 + u * HPW;
         raw[u] = Raw{};
         if (s0 + u < hi && h < a.Hkv) raw[u] = load<SRC, RUN>(src0 + u * HPW * src_pitch, sscale + h, xa, xb, D);
@@ -379,37 +380,42 @@ __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_
     }
     if constexpr (MODE == kCopy) {
 #pragma unroll
-      for (int u = 0; u < kBatch; u++) {
+      for (int u = 0; u < kLoad; u++) {
         const int h = h0 + u * HPW;
         if (s0 + u < hi && (HPW == 1 || h < a.Hkv)) store<SRC, LPH>(raw[u], dst0 + u * HPW * dst_pitch, dscale + h, xa);
       }
     } else {
-      F2 v[kBatch][4];
 #pragma unroll
-      for (int u = 0; u < kBatch; u++) decode<SRC, RUN>(raw[u], v[u]);
-      if constexpr (MODE == kTurn) {
-        if (rotated) {  // elsewhere an infinite neighbour would make 0 * inf
+      for (int first = 0; first < kLoad; first += kBatch) {
+        if (s0 + first >= hi) break;
+        F2 v[kBatch][4];
 #pragma unroll
-          for (int e = 0; e < (INTER ? 4 : 2); e++) {
-            // of values 2 e, 2 e + 1 (and, halves, of their partners)
-            const float2 c0 = cs[INTER ? xa / 2 + e : xa + 2 * e], c1 = INTER ? c0 : cs[xa + 2 * e + 1];
-            const F2 co = f2(c0.x, c1.x), si = INTER ? f2(-c0.y, c0.y) : f2(c0.y, c1.y), ni = f2(-c0.y, -c1.y);
+        for (int u = 0; u < kBatch; u++) decode<SRC, RUN>(raw[first + u], v[u]);
+        if constexpr (MODE == kTurn) {
+          if (rotated) {  // elsewhere an infinite neighbour would make 0 * inf
 #pragma unroll
-            for (int u = 0; u < kBatch; u++) {
-              const F2 p = v[u][e];
-              if (INTER) {
-                const float2 x = f2_out(p);
-                v[u][e] = f2_fma(f2(x.y, x.x), si, f2_mul(p, co));
-              } else {
-                const F2 q = v[u][e ^ 2];
-                v[u][e] = f2_fma(q, ni, f2_mul(p, co));
-                v[u][e ^ 2] = f2_fma(p, si, f2_mul(q, co));
+            for (int e = 0; e < (INTER ? 4 : 2); e++) {
+              // of values 2 e, 2 e + 1 (and, halves, of their partners)
+              const float2 c0 = cs[INTER ? xa / 2 + e : xa + 2 * e], c1 = INTER ? c0 : cs[xa + 2 * e + 1];
+              const F2 co = f2(c0.x, c1.x), si = INTER ? f2(-c0.y, c0.y) : f2(c0.y, c1.y), ni = f2(-c0.y, -c1.y);
+#pragma unroll
+              for (int u = 0; u < kBatch; u++) {
+                const F2 p = v[u][e];
+                if (INTER) {
+                  const float2 x = f2_out(p);
+                  v[u][e] = f2_fma(f2(x.y, x.x), si, f2_mul(p, co));
+                } else {
+                  const F2 q = v[u][e ^ 2];
+                  v[u][e] = f2_fma(q, ni, f2_mul(p, co));
+                  v[u][e ^ 2] = f2_fma(p, si, f2_mul(q, co));
+                }
               }
             }
           }
         }
+        encode<DST, RUN, LPH>(v, dst0 + first * HPW * dst_pitch, dst_pitch, dscale, h0 + first * HPW, a.Hkv,
+                              min(kBatch, hi - s0 - first), lane, xa, xb);
       }
-      encode<DST, RUN, LPH>(v, dst0, dst_pitch, dscale, h0, a.Hkv, min(kBatch, hi - s0), lane, xa, xb);
     }
   }
 }
@@ -430,13 +436,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) move_kernel(const MoveAr
   __syncthreads();
   // First every token's keys, then every token's values, so that each warp gets
   // as much of the one as of the other.
-  const int64_t keys = a.n * a.chunks_k, items = keys + a.n * a.chunks_v;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items; item += step) {
+  const uint32_t keys = static_cast<uint32_t>(a.n) * a.chunks_k, items = keys + static_cast<uint32_t>(a.n) * a.chunks_v;
+  for (uint32_t item = blockIdx.x * kWarps + warp; item < items; item += gridDim.x * kWarps) {
     const bool values = item >= keys;
-    const int64_t i = values ? item - keys : item;
-    const int chunks = values ? a.chunks_v : a.chunks_k;
-    const int64_t tok = chunks == 1 ? i : i / chunks;
+    const uint32_t i = values ? item - keys : item, chunks = values ? a.chunks_v : a.chunks_k;
+    const uint32_t tok = chunks == 1 ? i : i / chunks;
     const int lo = static_cast<int>(i - tok * chunks) * a.chunk, hi = min(a.steps, lo + a.chunk);
     const int64_t from = a.src_rows ? a.src_rows[tok] : tok, to = a.dst_rows ? a.dst_rows[tok] : tok;
     if (from < 0 || to < 0) continue;  // padding
@@ -559,6 +563,7 @@ SKV_EXPORT int skv_move_rows(int64_t n, int Hkv, int d, const skv_row_set* src, 
   }
   a.chunks_k = src->k ? chunks : 0;
   a.chunks_v = src->v ? chunks : 0;
+  if (n > (1 << 30) / (parts * chunks)) return SKV_EINVAL;  // work items are counted in 32 bits
   const int64_t want = (n * parts * chunks + kWarps - 1) / kWarps;
   const int64_t cap = static_cast<int64_t>(sms) * kCtasPerSm;
   const int grid = static_cast<int>(want < cap ? want : cap);
