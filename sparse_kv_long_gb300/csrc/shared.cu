@@ -18,10 +18,11 @@
 namespace skv {
 namespace {
 
-// Joins the state rows of each token and head, the prefix's first.  A block per
-// row while there is one for each, its warps every eighth state row; else a warp
-// per row.  Launched early, as the merge of paged.cu, and for the same reasons
-// nothing here is declared read-only and nothing starts early behind it.
+// Joins the state rows of each token and head, the prefix's first.  Launched
+// early, as the merge of paged.cu, and for the same reasons nothing here is
+// declared read-only and nothing starts early behind it.  With a warp per row as
+// soon as rows outnumber blocks, 64 samples at 131072 tokens (1024 rows) took 118
+// us, with four 110.
 template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const int* head, const int4* rows, const float2* ml, const float* o,
                                                     const int32_t* q_start, int B, int n_tok, int Hkv, int G,
@@ -36,17 +37,23 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* head, const int4*
   const int disorder = head[0];
   const int first_tok = q_start ? q_start[0] : 0, end_tok = q_start ? q_start[B] : n_tok;
   if (disorder) return;
-  const bool wide = tasks <= static_cast<int>(gridDim.x);
-  const int step = wide ? gridDim.x : gridDim.x * 8, first = wide ? blockIdx.x : blockIdx.x * 8 + warp;
-  const int s0 = wide ? warp : 0, ds = wide ? 8 : 1;
+  // as many warps to a row as there are for each
+  int team = 8;
+  while (team > 1 && tasks > static_cast<int>(gridDim.x) * 8 / team) team >>= 1;
+  const int s0 = warp & (team - 1), per_block = 8 / team;
 #pragma unroll 1
-  for (int w = first; w < tasks; w += step) {
-    const int tok = w / Hq, hq = w - tok * Hq, h = hq / G, g = hq - h * G;
-    if (tok < first_tok || tok >= end_tok) continue;  // padding: its rows were not listed
-    const int4 x = rows[static_cast<int64_t>(tok) * Hkv + h], y = rows[(static_cast<int64_t>(n_tok) + tok) * Hkv + h];
+  for (int w0 = blockIdx.x * per_block; w0 < tasks; w0 += gridDim.x * per_block) {
+    const int w = w0 + warp / team;
+    const int tok = min(w, tasks - 1) / Hq, hq = w - tok * Hq, h = hq / G, g = hq - h * G;
+    bool live = w < tasks && tok >= first_tok && tok < end_tok;  // padding: its rows were not listed
+    int4 x = make_int4(0, 0, 0, 0), y = x;
+    if (live) {
+      x = rows[static_cast<int64_t>(tok) * Hkv + h];
+      y = rows[(static_cast<int64_t>(n_tok) + tok) * Hkv + h];
+    }
     const int n_own = min(x.x & (kHasPrefix - 1), kMaxPieces), n_pre = x.x & kHasPrefix ? min(y.x, kMaxPieces) : 0;
-    if (n_own == 0) continue;  // written directly
-    const int n = n_pre + n_own;
+    live &= n_own > 0;  // else written directly
+    const int n = live ? n_pre + n_own : 0;
     auto row_of = [&](int s) -> int64_t {
       if (s < n_pre) return g + (s == 0 ? y.y : y.z + (s - 1) * y.w);
       s -= n_pre;
@@ -81,7 +88,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* head, const int4*
 #pragma unroll
     for (int e = 0; e < E; e++) acc[e] = 0.f;
 #pragma unroll 8
-    for (int s = s0; s < n; s += ds) {
+    for (int s = s0; s < n; s += team) {
       const float f = weight[warp][s];
       if (f < 0.f) continue;
       const float* src = o + row_of(s) * D + 4 * lane;
@@ -95,24 +102,25 @@ __global__ void __launch_bounds__(256) merge_kernel(const int* head, const int4*
       }
     }
     const float inv = den != 0.f ? 1.f / den : 0.f;
-    uint16_t* dst = out + static_cast<int64_t>(w) * D;
-    if (wide) {
+    uint16_t* dst = out + static_cast<int64_t>(min(w, tasks - 1)) * D;
+    if (team > 1) {
 #pragma unroll
       for (int e = 0; e < E; e += 4)
         *reinterpret_cast<float4*>(&red[warp][4 * lane + 32 * e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
       __syncthreads();
-      if (threadIdx.x < D / 2) {
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          const float2 z = *reinterpret_cast<const float2*>(&red[i][2 * threadIdx.x]);
-          sum.x += z.x;
-          sum.y += z.y;
+      if (live) {
+        for (int c = 32 * s0 + lane; c < D / 2; c += 32 * team) {
+          float2 sum = make_float2(0.f, 0.f);
+          for (int i = 0; i < team; i++) {
+            const float2 z = *reinterpret_cast<const float2*>(&red[warp - s0 + i][2 * c]);
+            sum.x += z.x;
+            sum.y += z.y;
+          }
+          *reinterpret_cast<uint32_t*>(dst + 2 * c) = pack_bf16(sum.x * inv, sum.y * inv);
         }
-        *reinterpret_cast<uint32_t*>(dst + 2 * threadIdx.x) = pack_bf16(sum.x * inv, sum.y * inv);
       }
       __syncthreads();
-    } else {
+    } else if (live) {
 #pragma unroll
       for (int e = 0; e < E; e += 4)
         *reinterpret_cast<uint2*>(dst + 4 * lane + 32 * e) =
@@ -144,11 +152,16 @@ Layout layout(int n_tok, int Hkv, int G, int d, int ctas, int sms) {
   return w;
 }
 
-// CTA pairs where a group, or without groups a request, has more rows than a
-// single CTA's query tile on average.
-int ctas_for(int B, int n_groups, int n_tok, int G, bool single) {
+// CTA pairs or single CTAs, by the query tiles of an average group (without
+// groups, of an average request) that each CTA takes: a pair's tile is two.  A
+// single CTA's costs more, as it copies and widens all of a key tile: 192 rows, two
+// tiles or a pair, over 30000 keys took 185 / 119 us (bf16 rows of 256 dims), 205 /
+// 157 (int8), 112 / 96 and 134 / 123 (128 dims).
+int ctas_for(int B, int n_groups, int n_tok, int d, int G, bool int8, bool single) {
   if (n_groups == 0 && single) return 1;
-  return static_cast<int64_t>(n_tok) * G > static_cast<int64_t>(n_groups > 0 ? n_groups : B) * kRows ? 2 : 1;
+  const int n = n_groups > 0 ? n_groups : B, toks = (n_tok + n - 1) / n, tpc = kRows / G;
+  const float one = static_cast<float>((toks + tpc - 1) / tpc), two = 2.f * ((toks + 2 * tpc - 1) / (2 * tpc));
+  return one * (d == 256 ? (int8 ? 1.3f : 1.55f) : int8 ? 1.09f : 1.17f) <= two ? 1 : 2;
 }
 
 template <int D, int CTAS, bool INT8>
@@ -243,7 +256,7 @@ SKV_EXPORT int skv_shared_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv,
       static_cast<int64_t>(n_tok) * Hq >= 1 << 29 || n_pool_rows > (static_cast<int64_t>(1) << 33))
     return SKV_EINVAL;
   const int G = Hq / Hkv;
-  const int ctas = ctas_for(B, n_groups, n_tok, G, !q_start);
+  const int ctas = ctas_for(B, n_groups, n_tok, d, G, int8, !q_start);
   const int tpt = ctas * (kRows / G);  // tokens per query tile
   const int kt = keys_per_tile(d, ctas);
   const int64_t own_tiles = n_pages * page / kt + 1 + kItem, pre_tiles = n_prefix_pages * page / kt + 1 + kItem;
