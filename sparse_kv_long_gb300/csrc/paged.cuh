@@ -121,8 +121,9 @@ constexpr int kHasPrefix = 1 << 16;  // beside the number of a token's rows: it 
 struct Piece {
   int tok0, toks;     // first token, tokens of the whole tile
   int pos0;           // position of the first token
-  int b, h;           // request; with prefixes: ~group for the keys of a prefix
-  int lo, nsink;      // first window tile, sink tiles before it
+  int b, h;           // request; with prefixes: -1 for a group's tokens over its prefix
+  int lo, nsink;      // first window tile, sink tiles before it; with prefixes: group, prefix tiles before the request's
+  int plen;           // with prefixes: the prefix's keys
   int j0, n;          // this piece's tiles: j0 .. j0 + n of the item's list
   int slot;           // partial slot, -1: whole item, kDense: whole, but joined with its prefix or its own keys
   int last;           // no piece follows
@@ -217,10 +218,12 @@ struct Req {
   int nqt, ntmax;    // query tiles, key tiles of the last one
 };
 struct PreReq : Req {
-  int kind = 0;      // kPrefix, kBehind or neither
+  int kind = 0;
+  int g = 0, plen = 0;  // group, keys of its prefix
 };
 constexpr int kPrefix = 1;  // the tokens of a group over its prefix
-constexpr int kBehind = 2;  // a request's own keys, behind a prefix
+constexpr int kBehind = 2;  // a request's own keys, behind a prefix that its group's tokens share
+constexpr int kFull = 3;    // a request's keys, those of its prefix before its own
 template <bool PRE>
 using ReqOf = std::conditional_t<PRE, PreReq, Req>;
 
@@ -291,9 +294,35 @@ __device__ __noinline__ Req request(const PagedArgs& a, int b, bool report, int*
   return r;
 }
 
+// Whether the requests [lo, hi) of a group go through the prefix each for itself:
+// their query tiles then see the prefix's keys and their own in one pass, with no
+// state rows to write and to join, but a request's last tile may be part empty
+// where the group's tokens together would fill it.  Those tiles cost the prefix's
+// key tiles; the state rows and the second pass over a query tile, about nine.
+__device__ __noinline__ bool one_by_one(const PagedArgs& a, int lo, int hi, int key_tiles) {
+  const int n = hi - lo;
+  if (n <= 1) return true;
+  if (!a.q_start) return false;
+  const int first = a.q_start[lo], tiles = (a.q_start[hi] - first + a.tpt - 1) / a.tpt;
+  if (2 * tiles < n) return false;  // (also many requests of few tokens)
+  int each = 0;
+  if (n <= 32) {
+#pragma unroll 1
+    for (int i = lo, s = first; i < hi; i++) {
+      const int e = a.q_start[i + 1];
+      each += (e - s + a.tpt - 1) / a.tpt;
+      s = e;
+    }
+  } else {
+    each = tiles + n / 2;
+  }
+  return static_cast<int64_t>(each - tiles) * key_tiles <= static_cast<int64_t>(9) * tiles;
+}
+
 // Entry i of a call with prefixes: group i's tokens over its prefix, or request
-// i - n_groups over its own keys.  Where any offset or group boundary is out of
-// order there are none (*disorder, once known).
+// i - n_groups over its own keys or, where its group's requests go one by one, the
+// prefix and its own.  Where any offset or group boundary is out of order there are
+// none (*disorder, once known).
 template <int KT>
 __device__ __noinline__ PreReq pre_request(const PagedArgs& a, int i, bool report, int* disorder, bool known) {
   PreReq r;
@@ -320,20 +349,31 @@ __device__ __noinline__ PreReq pre_request(const PagedArgs& a, int i, bool repor
   r.start = s;
   r.nq = e - s;
   if (r.nq > 0 && r.T > cap && report) set_status(a.status, SKV_DEV_RANGE);
+  r.nqt = (r.nq + a.tpt - 1) / a.tpt;
+  // every query tile sees a whole prefix; of its own keys a request's last tile the most
+  r.ntmax = static_cast<int>((min(static_cast<int64_t>(r.T), cap) + KT - 1) / KT);
   if (prefix) {
     r.kind = kPrefix;
-    if (r.T == 0) r.nq = 0;
+    r.g = i;
+    r.plen = r.T;
+    if (r.T == 0 || one_by_one(a, lo, hi, r.ntmax)) r.nq = r.nqt = 0;
   } else if (a.n_groups > 0) {  // the last group that begins at b or before
     int g = 0, end = a.n_groups;
     while (end - g > 1) {
       const int mid = (g + end) / 2;
       (a.group_start[mid] <= b ? g : end) = mid;
     }
-    if (a.group_start[g] <= b && b < a.group_start[g + 1] && a.prefix_lengths[g] > 0) r.kind = kBehind;
+    const int from = a.group_start[g], to = a.group_start[g + 1];
+    if (from <= b && b < to && to <= a.B) {  // (else out of order, which whoever looks at the group sees)
+      const int64_t pcap = a.n_prefix_pages * a.page;
+      r.g = g;
+      r.plen = max(0, a.prefix_lengths[g]);
+      const int tiles = static_cast<int>((min(static_cast<int64_t>(r.plen), pcap) + KT - 1) / KT);
+      if (r.plen > 0) r.kind = one_by_one(a, from, to, tiles) ? kFull : kBehind;
+      if (r.kind == kFull) r.ntmax += tiles;
+    }
   }
-  r.nqt = (r.nq + a.tpt - 1) / a.tpt;
-  // every query tile sees a whole prefix; of its own keys a request's last tile the most
-  if (r.nqt > 0) r.ntmax = static_cast<int>((min(static_cast<int64_t>(r.T), cap) + KT - 1) / KT);
+  if (r.nqt == 0) r.ntmax = 0;
   return r;
 }
 
@@ -543,22 +583,26 @@ struct Ring {  // a stage index and the parity of its current use
   }
 };
 
-// Whether a piece's keys are a prefix, which every row sees up to position pos0.
+// Whether tile j of a piece is of a prefix, which every row sees all of.
 template <bool PRE>
-__device__ __forceinline__ bool of_prefix(const Piece& pc) {
-  return PRE && pc.b < 0;
+__device__ __forceinline__ bool of_prefix(const Piece& pc, int j) {
+  return PRE && pc.j0 + j < pc.nsink;
 }
-// The position of a piece's last query.
+// The last key of tile j's part that the row of position `pos` (of the request's own keys) sees.
 template <bool PRE>
-__device__ __forceinline__ int last_pos(const Piece& pc) {
-  return of_prefix<PRE>(pc) ? pc.pos0 : pc.pos0 + pc.toks - 1;
+__device__ __forceinline__ int seen(const Piece& pc, int j, int pos) {
+  return of_prefix<PRE>(pc, j) ? pc.plen - 1 : pos;
 }
-// A piece's row of the block table, and its length.
 template <bool PRE>
-__device__ __forceinline__ const int32_t* pages_of(const PagedArgs& a, const Piece& pc, int64_t& n) {
-  if (of_prefix<PRE>(pc)) {
+__device__ __forceinline__ int last_seen(const Piece& pc, int j) {
+  return seen<PRE>(pc, j, pc.pos0 + pc.toks - 1);
+}
+// Tile j's row of the block table, and its length.
+template <bool PRE>
+__device__ __forceinline__ const int32_t* pages_of(const PagedArgs& a, const Piece& pc, int j, int64_t& n) {
+  if (of_prefix<PRE>(pc, j)) {
     n = a.n_prefix_pages;
-    return a.prefix_table + ~pc.b * n;
+    return a.prefix_table + pc.lo * n;
   }
   n = a.n_pages;
   return a.block_table + pc.b * n;
@@ -593,9 +637,10 @@ __device__ __forceinline__ void put_rows(unsigned char* buf, int lane, const uin
 }
 
 // Key tile j of a piece.
+template <bool PRE>
 __device__ __forceinline__ int tile_of(const Piece& pc, int j) {
   j += pc.j0;
-  return j < pc.nsink ? j : pc.lo + j - pc.nsink;
+  return j < pc.nsink ? j : (PRE ? 0 : pc.lo) + j - pc.nsink;
 }
 
 // A lane's box of tile j of a piece (lanes past the tile's boxes: none).
@@ -610,10 +655,10 @@ template <int KT, bool PRE>
 __device__ __forceinline__ BoxLoad box_load(const PagedArgs& a, const Piece& pc, int j, int lane) {
   BoxLoad x{-1, 0, 0};
   if (j < pc.n && lane * a.rb < KT) {
-    x.t = tile_of(pc, j) * KT + lane * a.rb;
+    x.t = tile_of<PRE>(pc, j) * KT + lane * a.rb;
     x.pg = page_of(a, x.t);
     int64_t n_pages;
-    const int32_t* pages = pages_of<PRE>(a, pc, n_pages);
+    const int32_t* pages = pages_of<PRE>(a, pc, j, n_pages);
     if (x.pg < n_pages) x.blk = pages[x.pg];
   }
   return x;
@@ -632,12 +677,12 @@ __device__ __forceinline__ Box box_of(const PagedArgs& a, const Piece& pc, const
 template <int D, int KT, bool PRE>
 __device__ __noinline__ void add_nonfinite(const PagedArgs& a, const Piece& pc, int p, int p_last, int c0,
                                            float (&sum)[32]) {
-  int64_t n_pages;
-  const int32_t* pages = pages_of<PRE>(a, pc, n_pages);
 #pragma unroll 1
   for (int j = 0; j < pc.n; j++) {
-    const int t0 = tile_of(pc, j) * KT;
-    bool masked = t0 + KT - 1 > pc.pos0 || (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S);
+    int64_t n_pages;
+    const int32_t* pages = pages_of<PRE>(a, pc, j, n_pages);
+    const int t0 = tile_of<PRE>(pc, j) * KT, last = seen<PRE>(pc, j, p);
+    bool masked = t0 + KT - 1 > seen<PRE>(pc, j, pc.pos0) || (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S);
 #pragma unroll 1
     for (int x = 0; x < KT && !masked; x += 8) {  // or a row without a page
       const int pg = page_of(a, t0 + x);
@@ -648,7 +693,7 @@ __device__ __noinline__ void add_nonfinite(const PagedArgs& a, const Piece& pc, 
 #pragma unroll 1
     for (int x = 0; x < KT; x++) {
       const int key = t0 + x;
-      if (key > p || !(a.W == 0 || key > p - a.W || key < a.S)) continue;
+      if (key > last || !(a.W == 0 || key > p - a.W || key < a.S)) continue;
       const int pg = page_of(a, key);
       const int blk = pg < n_pages ? pages[pg] : -1;
       if (blk < 0 || blk >= a.n_blocks) continue;
@@ -1026,7 +1071,11 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         q.T = __shfl_sync(full, r.T, w);
         q.nqt = __shfl_sync(full, r.nqt, w);
         q.ntmax = __shfl_sync(full, r.ntmax, w);
-        if constexpr (PRE) q.kind = __shfl_sync(full, r.kind, w);
+        if constexpr (PRE) {
+          q.kind = __shfl_sync(full, r.kind, w);
+          q.g = __shfl_sync(full, r.g, w);
+          q.plen = __shfl_sync(full, r.plen, w);
+        }
         const int before = __shfl_sync(full, pp, w);
         int item, nt, first = 0, n_seg = 1, seg = 0, list = 0;  // of a split item: pieces, this one's number, its place in the list
         if (CTAS == 1) {
@@ -1055,16 +1104,17 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         pc.pos0 = q.T - q.nq + qt * a.tpt;
         pc.last = 0;
         if constexpr (PRE) {
-          if (q.kind == kPrefix) {
-            pc.b = ~pc.b;
-            pc.pos0 = q.T - 1;
-            pc.lo = pc.nsink = 0;
-            nt = q.ntmax;
-          } else {
-            pc.b -= a.n_groups;
-            tile_range<KT>(a, q, qt, pc.lo, pc.nsink, nt);
-          }
-          if (pc.slot < 0 && q.kind != 0) pc.slot = kDense;
+          int own = 0, none;
+          if (q.kind != kPrefix) tile_range<KT>(a, q, qt, none, none, own);
+          // the longest list has every prefix tile and the request's
+          pc.nsink = q.kind == kPrefix ? q.ntmax
+                     : q.kind == kFull ? static_cast<int>((min(static_cast<int64_t>(q.plen), a.n_prefix_pages * a.page) + KT - 1) / KT)
+                                       : 0;
+          nt = pc.nsink + own;
+          pc.b = q.kind == kPrefix ? -1 : pc.b - a.n_groups;
+          pc.lo = q.g;
+          pc.plen = q.plen;
+          if (pc.slot < 0 && (q.kind == kPrefix || q.kind == kBehind)) pc.slot = kDense;
         } else {
           tile_range<KT>(a, q, qt, pc.lo, pc.nsink, nt);
         }
@@ -1132,14 +1182,13 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       if (!ok) continue;
       // Copies, in the order the products take them.  Lane i holds the box of
       // rows [i rb, i rb + rb) of a tile; table entries are read two tiles ahead.
-      const int p_hi = last_pos<PRE>(pc);  // keys past it are not copied
       BoxLoad l0 = box_load<KT, PRE>(a, pc, 0, lane), l1 = box_load<KT, PRE>(a, pc, 1, lane);
       Box cur{-1, false}, prev;
 #pragma unroll 1
       for (int j = 0; ok && pc.n > 0 && j <= pc.n; j++) {
         const BoxLoad l2 = box_load<KT, PRE>(a, pc, j + 2, lane);
         prev = cur;
-        cur = box_of<KT>(a, pc, l0, p_hi, lane);
+        cur = box_of<KT>(a, pc, l0, last_seen<PRE>(pc, j), lane);  // keys past it are not copied
         l0 = l1;
         l1 = l2;
         if (j < pc.n) {  // which 8-row groups have no page
@@ -1339,13 +1388,12 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&ax->pc_empty[slot]);
         if (pc.last) break;
-        const int p_hi = last_pos<PRE>(pc);
         const int rb_log = 31 - __clz(a.rb);
         int j = static_cast<int>((g ^ (warp & 1)) & 1);  // first tile of this warp's parity
         BoxLoad l0 = box_load<KT, PRE>(a, pc, j, lane);
 #pragma unroll 1
         for (; j < pc.n; j += 2) {
-          const Box box = box_of<KT>(a, pc, l0, p_hi, lane);
+          const Box box = box_of<KT>(a, pc, l0, last_seen<PRE>(pc, j), lane);
           const int rg = box.want ? box.rg : -1;
           float ks[KT / 32], vs[KT / 32];
 #pragma unroll
@@ -1425,17 +1473,18 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     for (int k = 0; ok && !pc.last; k++) {
       const int tok_i = static_cast<int>(rank) * a.tpc + tok_r;  // this row's token within the tile
       const bool live = tok_r < a.tpc && tok_i < pc.toks;
-      const int p = live ? pc.pos0 + (of_prefix<PRE>(pc) ? 0 : tok_i) : -1;  // this row's position: keys 0 .. p
+      const int pos = live ? pc.pos0 + tok_i : -1;  // this row's position: keys 0 .. pos
       // some row of the warp is used
       const bool warp_live = 32 * quad < min(a.tpc, pc.toks - static_cast<int>(rank) * a.tpc) * a.G;
       float m_ref = -INFINITY, l = 0.f;           // the maximum that l is relative to
-      const int p_last = last_pos<PRE>(pc);
+      const int pos_last = pc.pos0 + pc.toks - 1;
 #pragma unroll 1
       for (int j = 0; j < pc.n; j++) {
         const uint32_t t = g + j;
-        const int t0 = tile_of(pc, j) * KT;
+        const int t0 = tile_of<PRE>(pc, j) * KT;
+        const int p = PRE && !live ? -1 : seen<PRE>(pc, j, pos), p_last = seen<PRE>(pc, j, pos_last);
         // every row of the tile sees every key unless one of these holds, or a page is missing
-        const bool edge = t0 + KT - 1 > pc.pos0 || (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S);
+        const bool edge = t0 + KT - 1 > seen<PRE>(pc, j, pc.pos0) || (a.W > 0 && t0 <= p_last - a.W && t0 + KT > a.S);
         constexpr int HC = KT / 2;  // this group's keys of the tile
         const uint32_t scol = tm + lane_base + kSCol + (t & 1) * 128 + wg * HC;
         const uint32_t sc = t % kScaleRing;
@@ -1639,7 +1688,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         const int64_t tok = static_cast<int64_t>(pc.tok0) + tok_i;
         int64_t prow = static_cast<int64_t>(pc.slot) * a.part_rows + tok_i * a.G + head_r;
         if (PRE)
-          prow = pc.slot == kDense ? ((of_prefix<PRE>(pc) ? a.n_tok : 0) + tok) * (a.Hkv * a.G) + pc.h * a.G + head_r
+          prow = pc.slot == kDense ? ((pc.b < 0 ? a.n_tok : 0) + tok) * (a.Hkv * a.G) + pc.h * a.G + head_r
                                    : prow + a.n_dense;
         unsigned char* buf = sOut + (warp - 4) * 2048;
         const int id = !live ? -1 : whole ? static_cast<int>(tok * (a.Hkv * a.G)) + pc.h * a.G + head_r : static_cast<int>(prow);
@@ -1677,7 +1726,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
             float y[32];
 #pragma unroll 1
             for (int i = 0; i < 32; i++) y[i] = 0.f;
-            if (live) add_nonfinite<D, KT, PRE>(a, pc, p, p_last, c0, y);
+            if (live) add_nonfinite<D, KT, PRE>(a, pc, pos, pos_last, c0, y);
 #pragma unroll
             for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) + y[i]);
             __syncwarp();

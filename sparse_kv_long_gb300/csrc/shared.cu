@@ -13,6 +13,8 @@
 // prefix, then the requests over their own keys.  Pieces and whole items leave
 // fp32 state rows (m, l, o) that merge_kernel joins, the prefix's first; a
 // request without a prefix whose keys are not cut writes its output directly.
+// Chunks fill query tiles by themselves: their requests take the prefix's keys
+// before their own, one by one (see there), and leave nothing to join.
 #include "paged.cuh"
 
 namespace skv {
@@ -259,7 +261,8 @@ SKV_EXPORT int skv_shared_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv,
   const int ctas = ctas_for(B, n_groups, n_tok, d, G, int8, !q_start);
   const int tpt = ctas * (kRows / G);  // tokens per query tile
   const int kt = keys_per_tile(d, ctas);
-  const int64_t own_tiles = n_pages * page / kt + 1 + kItem, pre_tiles = n_prefix_pages * page / kt + 1 + kItem;
+  const int64_t pre_tiles = n_groups > 0 ? n_prefix_pages * page / kt + 1 + kItem : 0;
+  const int64_t own_tiles = pre_tiles + n_pages * page / kt + 1 + kItem;  // a request's with its prefix before them
   const int64_t own_items = (static_cast<int64_t>(B) + n_tok / tpt) * Hkv;
   const int64_t pre_items = n_groups > 0 ? (static_cast<int64_t>(n_groups) + n_tok / tpt) * Hkv : 0;
   if (own_tiles > INT32_MAX / own_items || (pre_items > 0 && pre_tiles > (INT32_MAX - own_tiles * own_items) / pre_items))
