@@ -87,6 +87,10 @@ constexpr int kCand = 64;          // split candidates (pairs)
 // in a window of a thousand keys 19.5 us with 2 and 4, 22.7 with 8.
 constexpr int kItem = 3;
 constexpr int kMinStretch = 4;
+// The same for an item in the row of pairs with prefixes: 64 samples at 131072
+// tokens took 131 us with 3, 100.7 with 5, 103.5 with 8, 112.7 with 12 (111 with all
+// pieces dealt out).
+constexpr int kRowItem = 5;
 constexpr float kLazy = 8.f;       // log2 units a maximum may grow before O is rescaled
 constexpr int kSplitPerPair = 8;   // pieces that write partials, per pair (single CTAs: two each)
 constexpr uint32_t kGone = 0x7fc0dead;  // a NaN that no arithmetic gives
@@ -188,6 +192,7 @@ struct alignas(16) Aux {
     float x[2][2][kRows];  // [exchange parity][group][row]: maxima of a tile, at a piece's end sums
   };
   int nmax, items;
+  int rest;      // pairs, with prefixes: the row's length
   int disorder;  // some request's offsets descend or leave [0, n_tok]
   uint32_t tmem_base;
   alignas(16) uint16_t ones[256];  // 16 rows of 16 ones
@@ -224,6 +229,11 @@ struct PreReq : Req {
 constexpr int kPrefix = 1;  // the tokens of a group over its prefix
 constexpr int kBehind = 2;  // a request's own keys, behind a prefix that its group's tokens share
 constexpr int kFull = 3;    // a request's keys, those of its prefix before its own
+// Pairs, with prefixes: whether an entry's pieces are dealt out (several query tiles
+// or a group's tokens read the same keys, at the same time if they can) or its items
+// lie in the row of which each pair takes a stretch.
+__device__ __forceinline__ bool dealt(const PreReq& r) { return r.kind == kPrefix || r.kind == kFull || r.nqt > 1; }
+__device__ __forceinline__ bool dealt(const Req&) { return true; }
 template <bool PRE>
 using ReqOf = std::conditional_t<PRE, PreReq, Req>;
 
@@ -384,6 +394,49 @@ __device__ __forceinline__ ReqOf<PRE> request_of(const PagedArgs& a, int b, bool
   else
     return request<KT>(a, b, report, disorder, known);
 }
+
+// Pairs, with prefixes: which stretch of the row each takes.  Dealing leaves some
+// with a piece less; they come last and take as much more of the row, so that all end
+// together, as far as it goes.  Stretches of less than kMinStretch go to fewer pairs.
+struct Stretches {
+  int n, o0, r;         // pairs; the first with a share; the first with a longer one
+  int64_t short_, long_;  // shares, in 2^-16 tiles
+  int total;
+  __device__ __forceinline__ void plan(int units, int pieces, int tiles, int row) {
+    const int rounds = (pieces + units - 1) / units;
+    const int64_t a = pieces > 0 ? (static_cast<int64_t>(tiles) + static_cast<int64_t>(pieces) * kItem) * 65536 / pieces : 0;
+    const int64_t w = static_cast<int64_t>(row) * 65536, least = static_cast<int64_t>(kMinStretch) * 65536;
+    n = units;
+    total = row;
+    o0 = 0;
+    r = pieces > 0 ? pieces - (rounds - 1) * units : units;
+    const int64_t less = (units - r) * a;
+    short_ = w > less ? (w - less) / units : 0;
+    long_ = short_ + a;
+    if (short_ < least && r < units) {
+      o0 = r;
+      long_ = w / (units - r);
+    }
+    if ((o0 == r && r < units ? long_ : short_) < least) {
+      const int used = max(1, min(units, row / kMinStretch));
+      o0 = r = units - used;
+      long_ = w / used;
+    }
+  }
+  __device__ __forceinline__ int begin(int o) const {
+    if (o >= n) return total;
+    const int64_t at = o <= o0 ? 0 : o <= r ? (o - o0) * short_ : max(r - o0, 0) * short_ + (o - max(r, o0)) * long_;
+    return static_cast<int>(at >> 16);
+  }
+  __device__ __forceinline__ int owner(int at) const {
+    const int64_t x = static_cast<int64_t>(at) * 65536, split = max(r - o0, 0) * short_;
+    int o = x < split && short_ > 0 ? o0 + static_cast<int>(x / short_) : max(r, o0) + static_cast<int>((x - split) / max(long_, static_cast<int64_t>(1)));
+    o = min(max(o, o0), n - 1);
+    while (o + 1 < n && begin(o + 1) <= at) o++;
+    while (o > o0 && begin(o) > at) o--;
+    return o;
+  }
+};
 
 __device__ __forceinline__ int pieces_of(int ntmax, int c) { return c > 0 && ntmax > c ? (ntmax + c - 1) / c : 1; }
 
@@ -772,6 +825,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     ax->disorder = 0;
     ax->nmax = 0;
     ax->items = 0;
+    ax->rest = 0;
   }
   if (SUM) {
     if (INT8) {
@@ -820,11 +874,13 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
   // request; the batch waits in shared memory that the ring will take over.
   int split_c = 1, split_from = 0;
   int total = 0, n_used = n_units;  // single CTAs: the row's length, the CTAs that share it
+  Stretches row;                    // pairs, with prefixes (warp 0)
+  int n_dealt = 0;
   Req mine;                         // warp 0: the first 32 requests
   mine.start = mine.nq = mine.T = mine.nqt = mine.ntmax = 0;
   auto again = [&]() {  // offsets out of order: the batch is gone through again, without the requests that overlap
     __syncthreads();
-    if (tid == 0) ax->nmax = ax->items = 0;
+    if (tid == 0) ax->nmax = ax->items = ax->rest = 0;
     __syncthreads();
   };
   if (CTAS == 1) {
@@ -863,11 +919,16 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     int2* req = reinterpret_cast<int2*>(sKV);  // (query tiles, key tiles of the longest)
 #pragma unroll 1
     for (bool known = false;; known = true) {
-      int longest = 0, tiles = 0;
+      int longest = 0, tiles = 0, in_row = 0;
 #pragma unroll 1
       for (int b = tid; b < n_req; b += THREADS) {
         const Req r = request_of<KT, PRE>(a, b, unit == 0 && rank == 0, &ax->disorder, known);
         if (b < 32) mine = r;
+        if (PRE && !dealt(r)) {
+          req[b] = make_int2(0, 0);
+          in_row += r.nqt * a.Hkv * (r.ntmax + kRowItem);
+          continue;
+        }
         req[b] = make_int2(r.nqt, r.ntmax);
         longest = max(longest, r.ntmax);
         tiles += r.nqt;
@@ -875,6 +936,8 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       if (warp * 32 < n_req) {
         longest = __reduce_max_sync(0xffffffffu, longest);
         tiles = __reduce_add_sync(0xffffffffu, tiles);
+        if (PRE) in_row = __reduce_add_sync(0xffffffffu, in_row);
+        if (PRE && lane == 0 && in_row > 0) atomicAdd(&ax->rest, in_row);
         if (lane == 0 && tiles > 0) {
           atomicMax(&ax->nmax, longest);
           atomicAdd(&ax->items, tiles);
@@ -899,7 +962,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       const int c = (nmax + k - 1) / k;
       const float rc = 1.f / c;
       int P = 0, S = 0, u = 0, main_u = 0;  // pieces, those of cut items, tiles of the items looked at, of the others
-      int PL = 0, uL = 0;                   // long pieces, their tiles
+      int PL = 0, uL = 0;                   // with prefixes: long pieces, their tiles
 #pragma unroll 1
       for (int b0 = 0; b0 < n_req; b0 += 32) {
         const int2 r = b0 + lane < n_req ? req[b0 + lane] : make_int2(0, 0);
@@ -929,15 +992,17 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       S = __reduce_add_sync(0xffffffffu, S);
       u = __reduce_add_sync(0xffffffffu, u);
       if (rest) main_u = __reduce_add_sync(0xffffffffu, main_u);
-      if (S <= a.max_split) {
+      if (S <= (PRE ? kSplitPerPair * n_units : a.max_split)) {
         float cost = rest ? static_cast<float>(main_u) / n_units + x1 / n_units * kOvh : 0.f;
         if (PRE) {
+          // Long pieces and short ones are dealt out in rounds of their own; the row evens
+          // out what these leave, as far as it goes.
           PL = __reduce_add_sync(0xffffffffu, PL);
           uL = __reduce_add_sync(0xffffffffu, uL);
           const int rounds = (P + n_units - 1) / n_units, long_rounds = (PL + n_units - 1) / n_units;
-          if (PL > 0) cost += long_rounds * (static_cast<float>(uL) / PL + kOvh);
+          if (PL > 0) cost = long_rounds * (static_cast<float>(uL) / PL + kOvh);
           if (rounds > long_rounds) cost += (rounds - long_rounds) * (static_cast<float>(u - uL) / (P - PL) + kOvh);
-          if (S > 0) cost += kJoin + S * a.part_cost;
+          cost = fmaxf(cost, (u + P * kOvh + ax->rest) / n_units) + (S > 0 ? kJoin + S * a.part_cost : 0.f);
         } else if (P > 0)
           cost += static_cast<float>((P - 1) / n_units) * (static_cast<float>(u) / P + kOvh) + c + kOvh +
                   (S > 0 ? kJoin + S * a.part_cost : 0.f);
@@ -963,10 +1028,21 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         pick = oi;
       }
     }
-    tc::fence_async_smem();  // the copies write where the batch was
     split_from = pick >= nk && nk > 0 ? x1 : 0;
     const int k = pick >= nk && nk > 0 ? pick - nk + 1 : pick + 1;
     split_c = max(1, (nmax + k - 1) / k);
+    if (PRE && warp == 0) {
+      int P = 0, u = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < n_req; b0 += 32) {
+        const int2 r = b0 + lane < n_req ? req[b0 + lane] : make_int2(0, 0);
+        P += r.x * a.Hkv * pieces_of(r.y, split_c);
+        u += r.x * a.Hkv * r.y;
+      }
+      row.plan(n_units, __reduce_add_sync(0xffffffffu, P), __reduce_add_sync(0xffffffffu, u), ax->rest);
+      n_dealt = __reduce_add_sync(0xffffffffu, P);
+    }
+    tc::fence_async_smem();  // the copies write where the batch was
     tc::cluster_sync();  // also: the peer's barriers exist before any remote access
   }
   const int c = split_c, whole = split_from;  // tiles per piece; items before this one are not cut
@@ -984,10 +1060,13 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     int b32 = 0, base = 0, ibase = 0, sbase = 0, seen = 0;  // first request of the window; pieces, split items, slots, items before it
     Req r = mine;
     int pp, ii = 0, ss = 0, tt = 0, ns = 1, nw = 0;  // inclusive sums over the window's requests; pieces per cut item, items kept whole
+    constexpr int OVH = CTAS == 1 ? kItem : kRowItem;
+    bool stretch = CTAS == 1;  // walking the row; pairs, with prefixes: once the pieces are dealt out
     auto scan = [&]() {
-      const int items = r.nqt * a.Hkv;
-      if (CTAS == 1) {
-        pp = items * (r.ntmax + kItem);
+      const int items = !PRE || CTAS == 1 || dealt(r) != stretch ? r.nqt * a.Hkv : 0;
+      if (stretch) {
+        ii = ss = tt = 0;
+        pp = items * (r.ntmax + OVH);
       } else {
         ns = pieces_of(r.ntmax, c);
         tt = items;
@@ -1014,15 +1093,24 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       }
     };
     scan();
-    // single CTAs: this one's stretch, and the CTA that has a place of the row
-    int x = 0, x_end = 0;
+    // single CTAs: this one's stretch, and the CTA that has a place of the row; of
+    // pairs with prefixes, their places in the order of shares
+    int x = 0, x_end = 0, me = unit, slots = 0;  // slots: before the row's
     bool listed = false;  // a split item begins here
     if (CTAS == 1 && unit < n_used) {
       x = static_cast<int>(static_cast<int64_t>(total) * unit / n_used);
       x_end = static_cast<int>(static_cast<int64_t>(total) * (unit + 1) / n_used);
     }
+    if (PRE && CTAS == 2) {
+      const int last_round = n_dealt > 0 ? (n_dealt - 1) / n_units : 0;
+      me = (last_round & 1) ? n_units - 1 - unit : unit;
+      x = row.begin(me);
+      x_end = row.begin(me + 1);
+      slots = kSplitPerPair * n_units;
+    }
     const int x_begin = x;
     auto owner = [&](int at) {
+      if (PRE && CTAS == 2) return row.owner(at);
       return static_cast<int>((static_cast<int64_t>(at + 1) * n_used - 1) / total);
     };
     const uint32_t full = 0xffffffffu;
@@ -1051,8 +1139,14 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       const int id = CTAS == 1 ? 0 : k * n_units + ((k & 1) ? n_units - 1 - unit : unit);
 #pragma unroll 1
       while (pc.last) {
-        const int at = CTAS == 1 ? x : id;
-        if (CTAS == 1 && x >= x_end) break;
+        if (PRE && CTAS == 2 && !stretch && id >= n_dealt) {
+          stretch = true;
+          b32 = base = 0;
+          r = request_of<KT, PRE>(a, lane, false, &ax->disorder, true);
+          scan();
+        }
+        const int at = stretch ? x : id;
+        if (stretch && x >= x_end) break;
 #pragma unroll 1
         while (b32 < n_req && at >= base + __shfl_sync(full, pp, 31)) {
           base += __shfl_sync(full, pp, 31);
@@ -1078,8 +1172,8 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         }
         const int before = __shfl_sync(full, pp, w);
         int item, nt, first = 0, n_seg = 1, seg = 0, list = 0;  // of a split item: pieces, this one's number, its place in the list
-        if (CTAS == 1) {
-          const int len = q.ntmax + kItem;
+        if (stretch) {
+          const int len = q.ntmax + OVH;
           const int start = base + before - q.nqt * a.Hkv * len;
           item = (x - start) / len;
           first = start + item * len;  // the item's place in the row
@@ -1118,29 +1212,29 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         } else {
           tile_range<KT>(a, q, qt, pc.lo, pc.nsink, nt);
         }
-        if (CTAS == 1) {
+        if (stretch) {
           // Tiles of the item lie at [first + kItem, first + len), fewer than
           // ntmax of them spread evenly; the CTAs that share these have its pieces.
-          const int len = q.ntmax + kItem, lo = max(0, x - first - kItem), hi = max(0, min(len, x_end - first) - kItem);
-          int f = unit, l = unit;
+          const int len = q.ntmax + OVH, lo = max(0, x - first - OVH), hi = max(0, min(len, x_end - first) - OVH);
+          int f = me, l = me;
           if (q.ntmax == 0) {
             f = l = owner(first);
-          } else if (first + kItem < x_begin || first + len > x_end) {
-            f = owner(first + kItem);
+          } else if (first + OVH < x_begin || first + len > x_end) {
+            f = owner(first + OVH);
             l = owner(first + len - 1);
           }
           x = min(x_end, first + len);
           pc.j0 = 0;
           pc.n = nt;
-          if (unit < f || unit > l) {
+          if (me < f || me > l) {
             pc.last = 1;  // nothing of it but the part that stands for its pipeline
           } else if (f < l) {
             pc.j0 = nt == q.ntmax ? lo : static_cast<int>(static_cast<int64_t>(lo) * nt / q.ntmax);
             pc.n = (nt == q.ntmax ? hi : static_cast<int>(static_cast<int64_t>(hi) * nt / q.ntmax)) - pc.j0;
             n_seg = l - f + 1;
-            seg = unit - f;
+            seg = me - f;
             list = unit;
-            pc.slot = seg == 0 ? 2 * unit + 1 : 2 * unit;
+            pc.slot = slots + (seg == 0 ? 2 * me + 1 : 2 * me);
             listed |= seg == 0;
           }
         } else {
@@ -1153,13 +1247,13 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
             const bool prefix = q.kind == kPrefix;
             const int dense = ((prefix ? a.n_tok : 0) + pc.tok0) * (a.Hkv * a.G) + pc.h * a.G;
             const int one = pc.slot >= 0 ? a.n_dense + pc.slot * a.part_rows : dense;
-            const int two = CTAS == 1 ? a.n_dense + (2 * unit + 2) * a.part_rows : one + a.part_rows;
+            const int two = stretch ? a.n_dense + (slots + 2 * me + 2) * a.part_rows : one + a.part_rows;
             const int n = (pc.slot == -1 ? 0 : n_seg) | (q.kind == kBehind ? kHasPrefix : 0);
             const int pitch = pc.slot >= 0 ? a.G : a.Hkv * a.G;  // from token to token
 #pragma unroll 1
             for (int i = lane; i < pc.toks; i += 32)
               a.ws_rows[(static_cast<int64_t>(prefix ? a.n_tok : 0) + pc.tok0 + i) * a.Hkv + pc.h] =
-                  make_int4(n, one + i * pitch, two + i * a.G, (CTAS == 1 ? 2 : 1) * a.part_rows);
+                  make_int4(n, one + i * pitch, two + i * a.G, (stretch ? 2 : 1) * a.part_rows);
           }
         } else if (!pc.last && n_seg > 1 && seg == 0 && rank == 0 && lane == 0) {
           a.ws_item[2 * list] = make_int4(pc.tok0, pc.toks * a.G, pc.h, pc.slot);

@@ -142,7 +142,7 @@ struct Layout {  // workspace
 Layout layout(int n_tok, int Hkv, int G, int d, int ctas, int sms) {
   Layout w;
   if (sms > kMaxPieces) sms = kMaxPieces;
-  w.max_split = ctas == 1 ? 2 * sms : kSplitPerPair * (sms / 2);
+  w.max_split = ctas == 1 ? 2 * sms : (kSplitPerPair + 2) * (sms / 2);  // (pieces dealt out, and cut by stretches)
   w.part_rows = tile_rows(n_tok, G, ctas);
   w.n_dense = static_cast<int64_t>(2) * n_tok * Hkv * G;
   const size_t state = static_cast<size_t>(w.n_dense) + static_cast<size_t>(w.max_split) * w.part_rows;
@@ -261,8 +261,8 @@ SKV_EXPORT int skv_shared_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv,
   const int ctas = ctas_for(B, n_groups, n_tok, d, G, int8, !q_start);
   const int tpt = ctas * (kRows / G);  // tokens per query tile
   const int kt = keys_per_tile(d, ctas);
-  const int64_t pre_tiles = n_groups > 0 ? n_prefix_pages * page / kt + 1 + kItem : 0;
-  const int64_t own_tiles = pre_tiles + n_pages * page / kt + 1 + kItem;  // a request's with its prefix before them
+  const int64_t pre_tiles = n_groups > 0 ? n_prefix_pages * page / kt + 1 + kRowItem : 0;
+  const int64_t own_tiles = pre_tiles + n_pages * page / kt + 1 + kRowItem;  // a request's with its prefix before them
   const int64_t own_items = (static_cast<int64_t>(B) + n_tok / tpt) * Hkv;
   const int64_t pre_items = n_groups > 0 ? (static_cast<int64_t>(n_groups) + n_tok / tpt) * Hkv : 0;
   if (own_tiles > INT32_MAX / own_items || (pre_items > 0 && pre_tiles > (INT32_MAX - own_tiles * own_items) / pre_items))
