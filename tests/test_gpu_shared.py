@@ -203,6 +203,60 @@ def test_without_prefixes_it_is_the_paged_attention(skv, kind, lens, new, single
     Case(skv, kind_of(skv, kind), 256, 8, 2, 16, [0, 1, len(lens)], [0, 0], lens, new, seed=5).check(single=single)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,B,groups,P,top", [(256, 70, 1, 5000, 3000), (256, 45, 1, 700, 9), (128, 150, 2, 1500, 2500),
+                                               (256, 64, 1, 129, 5000), (128, 200, 1, 1, 40)])
+def test_pairs_share_out_single_tokens(skv, kind, d, B, groups, P, top):
+    """Many tokens behind a prefix run as pairs: the prefix's pieces are dealt out, the requests' own keys lie in a row
+    that the pairs take stretches of, cut anywhere; some requests have none."""
+    rng = np.random.default_rng(B + P)
+    lens = [int(x) - 1 for x in np.exp(rng.uniform(0, math.log(top), B - 1))] + [top]
+    inner = [B // 3] if groups == 2 else []
+    prefix = [P] + [P // 2 + 1] * (groups - 1)
+    c = Case(skv, kind_of(skv, kind), d, 8, 1, 64, [0, *inner, B - 2], prefix, lens, [1] * B, seed=B)
+    c.check(single=True)
+    c.check()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens,new,start,prefix", [
+    ([300, 300, 290], [300, 300, 290], [0, 3], [900]),       # whole chunks: one by one
+    ([40, 33, 50, 41], [35, 33, 37, 36], [0, 4], [2000]),    # parts of tiles: together
+    ([600, 3, 1, 1, 200], [500, 3, 1, 1, 200], [0, 1, 4], [129, 700]),
+    ([200] * 40, [9] * 40, [0, 39], [300]),
+])
+def test_chunks_together_and_one_by_one(skv, kind, lens, new, start, prefix):
+    c = Case(skv, kind_of(skv, kind), 256, 12, 2, 16, start, prefix, lens, new, seed=len(lens), first=1, pad=2)
+    c.check()
+
+
+FORMS = [([700, 64, 1, 300], [1] * 4, True), ([90, 20, 200], [3, 5, 7], False), ([300, 90, 100], [250, 90, 60], False)]
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("lens,new,single", FORMS)
+def test_value_rows_of_zeros_and_scales_of_every_size(skv, d, lens, new, single):
+    """int8: an all-zero value row has a zero scale and its weight counts; scales from the smallest subnormal to the
+    largest number, in the prefix and in the requests' own rows."""
+    for seed, lo, hi, share in ((90, -7.0, -6.0, 0.5), (91, -7.0, -6.0, 1.0), (92, -24.0, 15.9, 0.1), (93, -24.0, -20.0, 0.1),
+                                (94, 10.0, 15.9, 0.1)):
+        c = Case(skv, skv.KV_INT8, d, 8, 2, 16, [0, 2], [500], lens, new, seed=seed)
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        rand = lambda: torch.rand(c.vs.shape, generator=g, device="cuda")  # noqa: E731
+        scale = torch.exp2(lo + (hi - lo) * rand()).half()
+        scale = torch.where(rand() < 0.2, -scale, scale)
+        scale[rand() < share] = 0
+        c.v[(scale == 0) & c.owned[:, None]] = 0
+        c.vs = torch.where(c.owned[:, None], scale, c.vs)
+        ks = torch.exp2(-24.0 + 18.0 * rand()).half()
+        ks[rand() < 0.1] = 0
+        c.ks = torch.where(c.owned[:, None], ks, c.ks)
+        c.check(single=single)
+        if share == 1.0:
+            assert (c.out == 0).all()
+
+
 def test_a_prefix_of_several_groups_and_of_a_request(skv):
     """The same pages as the prefix of two groups and as the first pages of another request's own keys."""
     c = Case(skv, skv.KV_INT8, 256, 8, 2, 16, [0, 2, 4], [320, 320], [5, 40, 7, 1, 330], [1, 3, 2, 1, 4], seed=6)
