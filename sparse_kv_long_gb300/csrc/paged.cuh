@@ -1718,12 +1718,19 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
           if (!(ok = wait_all(&ax->kv_full[vs], (fv / a.stages) & 1, abort))) break;
           unsigned char* V = sKV + vs * STAGE;
           bool found = false;
+          // A single token's keys, and a prefix's, every query of the tile sees or none
+          // does: there is nothing to look for.
+          const bool alike = PRE && (pc.toks == 1 || of_prefix<PRE>(pc, j));
 #pragma unroll 1
           for (int i = tid - 128; i < STAGE / 16; i += 256) {
             const int grp = i / (VSUB * 64), row = grp * 8 + ((i >> 3) & 7);  // 64 16-byte pieces per 1024 B block
             uint4* at = reinterpret_cast<uint4*>(V + i * 16);
             const int key = t0 + row;  // seen by no query of the tile: its page may not have been read
             const bool dead = key > p_last || (a.W > 0 && key <= pc.pos0 - a.W && key >= a.S) || ((bad >> grp) & 1u);
+            if (alike) {
+              if (dead) *at = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
             uint4 w = dead ? make_uint4(0u, 0u, 0u, 0u) : *at;
             uint32_t* e = reinterpret_cast<uint32_t*>(&w);
             bool change = dead;
@@ -1790,7 +1797,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         const int pitch = whole ? 2 * D : 4 * D;
         // With a few rows each lane writes its own (a window's single tokens 19.7 ->
         // 19.3 us; with 32 rows that took 4 to 7 % of a chunk).
-        const bool few = CTAS == 1 && __popc(__ballot_sync(0xffffffffu, live)) <= 8;
+        const bool few = (CTAS == 1 || PRE) && __popc(__ballot_sync(0xffffffffu, live)) <= 8;
         char* to[4];
 #pragma unroll
         for (int x = 0; x < 4; x++) {
