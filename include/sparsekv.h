@@ -851,7 +851,8 @@ int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, int d, cons
  * play no part: keys and queries are rotated before.  A prefix may be in several
  * groups, and its pages in requests' own tables.
  *   group_start     int32 [n_groups+1], ascending (a group may have no request)
- *   prefix_table    int32 [n_groups][n_prefix_pages]
+ *   prefix_table    int32 [n_groups][n_prefix_pages], no wider than needed: its width
+ *            stands for the prefixes' lengths where these decide how the call runs
  *   prefix_lengths  int32 [n_groups]
  *   block_table     int32 [B][n_pages], and lengths int32 [B]: own keys only
  *   workspace  skv_shared_attend_workspace_size(...) bytes; nothing in it

@@ -154,13 +154,22 @@ Layout layout(int n_tok, int Hkv, int G, int d, int ctas, int sms) {
   return w;
 }
 
-// CTA pairs or single CTAs, by the query tiles of an average group (without
-// groups, of an average request) that each CTA takes: a pair's tile is two.  A
-// single CTA's costs more, as it copies and widens all of a key tile: 192 rows, two
-// tiles or a pair, over 30000 keys took 185 / 119 us (bf16 rows of 256 dims), 205 /
-// 157 (int8), 112 / 96 and 134 / 123 (128 dims).
-int ctas_for(int B, int n_groups, int n_tok, int d, int G, bool int8, bool single) {
+// CTA pairs or single CTAs.  Requests of few tokens: a pair spends as long on
+// their own keys as a single CTA, so pairs pay only where long prefixes outweigh
+// that and a single CTA's tile of 256 dims asks more of L2 than it gives.  64
+// tokens of 16 / 2 heads of 256, 100 keys of their own, single against pairs, behind
+// 8000 / 32000 / 100000 tokens: bf16 28 / 47 / 139 us against 35 / 49 / 84, int8 33 /
+// 64 / 157 against 42 / 62 / 120; of 32 / 8 heads of 128 behind 32000: bf16 63 against
+// 81, int8 91 against 120.  The prefixes' lengths are on the device; their table's
+// width stands for them.
+// Else by the query tiles of an average group (without groups, request) that each
+// CTA takes, a pair's being two, weighed by what they cost: 192 rows, two tiles or a
+// pair, over 30000 keys took 185 / 119 us (bf16 rows of 256 dims), 205 / 157 (int8),
+// 112 / 96 and 134 / 123 (128 dims).
+int ctas_for(int B, int n_groups, int n_tok, int d, int G, bool int8, bool single, int64_t prefix_keys) {
   if (n_groups == 0 && single) return 1;
+  const bool few = static_cast<int64_t>(n_tok) * G <= static_cast<int64_t>(B) * (kRows / 2);
+  if (n_groups > 0 && few && (d == 128 || prefix_keys < 32768)) return 1;
   const int n = n_groups > 0 ? n_groups : B, toks = (n_tok + n - 1) / n, tpc = kRows / G;
   const float one = static_cast<float>((toks + tpc - 1) / tpc), two = 2.f * ((toks + 2 * tpc - 1) / (2 * tpc));
   return one * (d == 256 ? (int8 ? 1.3f : 1.55f) : int8 ? 1.09f : 1.17f) <= two ? 1 : 2;
@@ -258,7 +267,7 @@ SKV_EXPORT int skv_shared_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv,
       static_cast<int64_t>(n_tok) * Hq >= 1 << 29 || n_pool_rows > (static_cast<int64_t>(1) << 33))
     return SKV_EINVAL;
   const int G = Hq / Hkv;
-  const int ctas = ctas_for(B, n_groups, n_tok, d, G, int8, !q_start);
+  const int ctas = ctas_for(B, n_groups, n_tok, d, G, int8, !q_start, n_groups > 0 ? n_prefix_pages * page : 0);
   const int tpt = ctas * (kRows / G);  // tokens per query tile
   const int kt = keys_per_tile(d, ctas);
   const int64_t pre_tiles = n_groups > 0 ? n_prefix_pages * page / kt + 1 + kRowItem : 0;

@@ -213,8 +213,11 @@ def test_pairs_share_out_single_tokens(skv, kind, d, B, groups, P, top):
     lens = [int(x) - 1 for x in np.exp(rng.uniform(0, math.log(top), B - 1))] + [top]
     inner = [B // 3] if groups == 2 else []
     prefix = [P] + [P // 2 + 1] * (groups - 1)
-    c = Case(skv, kind_of(skv, kind), d, 8, 1, 64, [0, *inner, B - 2], prefix, lens, [1] * B, seed=B)
+    # a wide table, as a server keeps for its longest prefix: pairs at 256 dims, single CTAs at 128
+    c = Case(skv, kind_of(skv, kind), d, 8, 1, 64, [0, *inner, B - 2], prefix, lens, [1] * B, seed=B, extra_pages=512)
     c.check(single=True)
+    c.check()
+    c = Case(skv, kind_of(skv, kind), d, 8, 1, 64, [0, *inner, B - 2], prefix, lens, [1] * B, seed=B)
     c.check()
 
 
