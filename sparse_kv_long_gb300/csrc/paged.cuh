@@ -87,6 +87,9 @@ constexpr int kCand = 64;          // split candidates (pairs)
 // in a window of a thousand keys 19.5 us with 2 and 4, 22.7 with 8.
 constexpr int kItem = 3;
 constexpr int kMinStretch = 4;
+// With prefixes, where each item's part counts less: eight agents behind 2000 tokens
+// 17.3 us with 2, 18.5 with 4, 21.3 with 6.
+constexpr int kMinShared = 2;
 // The same for an item in the row of pairs with prefixes: 64 samples at 131072
 // tokens took 131 us with 3, 100.7 with 5, 103.5 with 8, 112.7 with 12 (111 with all
 // pieces dealt out).
@@ -907,7 +910,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       again();
     }
     total = ax->items;
-    n_used = min(n_units, max(1, total / kMinStretch));
+    n_used = min(n_units, max(1, total / (PRE ? kMinShared : kMinStretch)));
     if (!PRE && tid == 0 && unit == 0) {
       a.ws_head[0] = n_units;
       a.ws_head[1] = ax->nmax;
