@@ -24,11 +24,18 @@
 namespace skv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 4;
-constexpr int kLoad = 4;   // heads per lane group whose loads are in flight together
-constexpr int kBatch = 2;  // of them decoded and encoded together
+constexpr int kLoad = 4;  // heads per lane group whose loads are in flight together
+// Of them decoded and encoded together, and resident CTAs (64 or 72 registers a
+// thread).  Four heads share the work on their scales; rows of 64 dims, eight of
+// them, would wait for one another.  65536 int4 rows to int8 / 32768 int8 rows
+// turned / 32768 of 64 dims / 32768 int8 rows to bf16, turned: two heads and eight
+// CTAs 108.2 / 40.9 / 31.0 / 39.6 us, four and seven 103.1 / 41.5 / 35.9 / 41.4, two
+// and six 114.6 / 45.2 / 31.0 / 45.3, one and ten 118.3 / 44.9 / 33.2 / 40.6.
+template <int D, int DST>
+constexpr int kBatch = DST != SKV_KV_BF16 && D > 64 ? 4 : 2;
+constexpr int ctas_per_sm(int d, int dst) { return dst != SKV_KV_BF16 && d > 64 ? 7 : 8; }
 
 struct RowSet {
   const unsigned char *k, *v;  // (written through on the destination's side)
@@ -148,11 +155,11 @@ __device__ __forceinline__ float lanes_max(float m) {
 }
 
 // This lane's scale's largest value: lane `sub` of LANES holds the one of step sub.
-template <int LANES>
-__device__ __forceinline__ float scale_max(const F2 (&v)[kBatch][4], int sub) {
+template <int LANES, int N>
+__device__ __forceinline__ float scale_max(const F2 (&v)[N][4], int sub) {
   float mine = 0.f;
 #pragma unroll
-  for (int u = 0; u < kBatch; u++) {
+  for (int u = 0; u < N; u++) {
     const float m = lanes_max<LANES>(amax<4>(v[u]));
     if (sub == u) mine = m;
   }
@@ -249,14 +256,14 @@ __device__ __forceinline__ float reciprocal(float s) {  // to 2^-23
 
 // Encodes the heads of a batch, v[u] of step s0 + u; every lane of the warp takes
 // part.  One lane per scale makes it and its reciprocal for all.
-template <int KIND, bool RUN, int LPH>
-__device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* dst, int64_t pitch, __half* scale, int h0,
+template <int KIND, bool RUN, int LPH, int N>
+__device__ __forceinline__ void encode(const F2 (&v)[N][4], unsigned char* dst, int64_t pitch, __half* scale, int h0,
                                        int H, int steps, int lane, int xa, int xb) {
   constexpr int D = 8 * LPH, HPW = 32 / LPH;
   const int sub = lane % LPH;
   if (KIND == SKV_KV_BF16) {
 #pragma unroll
-    for (int u = 0; u < kBatch; u++) {
+    for (int u = 0; u < N; u++) {
       const int h = h0 + u * HPW;
       if (u >= steps || h >= H) break;
       unsigned char* vec = dst + u * HPW * pitch;
@@ -271,12 +278,12 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
       }
     }
   } else if (KIND == SKV_KV_INT8) {
-    const float mine = scale_max<LPH>(v, sub);
+    const float mine = scale_max<LPH, N>(v, sub);
     const __half sh = scale_of<127>(mine);
     const float s_own = __half2float(sh), i_own = reciprocal(s_own);
     if (sub < steps && h0 + sub * HPW < H) scale[h0 + sub * HPW] = sh;
 #pragma unroll
-    for (int u = 0; u < kBatch; u++) {
+    for (int u = 0; u < N; u++) {
       if (u >= steps) break;
       const int from = lane - sub + u, h = h0 + u * HPW;
       uint32_t w[2];
@@ -296,10 +303,10 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
     const int ga = xa >> 6, gb = xb >> 6;
     float mine = 0.f;
     if constexpr (RUN) {
-      mine = scale_max<8>(v, lane & 7);
+      mine = scale_max<8, N>(v, lane & 7);
     } else {
 #pragma unroll
-      for (int u = 0; u < kBatch; u++) {
+      for (int u = 0; u < N; u++) {
         const float ma = amax<2>(&v[u][0]), mb = amax<2>(&v[u][2]);
 #pragma unroll
         for (int g = 0; g < D / 64; g++) {
@@ -313,7 +320,7 @@ __device__ __forceinline__ void encode(const F2 (&v)[kBatch][4], unsigned char* 
     if ((lane & 7) < steps)
       *reinterpret_cast<uint16_t*>(dst + (lane & 7) * pitch + D / 2 + 2 * (lane >> 3)) = __half_as_ushort(sh);
 #pragma unroll
-    for (int u = 0; u < kBatch; u++) {
+    for (int u = 0; u < N; u++) {
       if (u >= steps) break;
       uint32_t w[2];
       codes_of<7, RUN>(v[u], s_own, i_own, 8 * ga + u, 8 * gb + u, w);
@@ -350,7 +357,7 @@ __device__ __forceinline__ void store(const Raw& r, unsigned char* vec, __half* 
 template <int LPH, int SRC, int DST, bool INTER, Mode MODE>
 __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_t from, int64_t to, int lo, int hi,
                                           int lane, const float2* cs) {
-  constexpr int D = 8 * LPH, HPW = 32 / LPH;
+  constexpr int D = 8 * LPH, HPW = 32 / LPH, N = kBatch<D, DST>;
   constexpr bool RUN = MODE != kTurn || INTER;
   const int sub = lane % LPH, grp = lane / LPH, half = a.rot / 2;
   const bool rotated = MODE == kTurn && sub < a.rot / 8;
@@ -386,11 +393,11 @@ __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_
       }
     } else {
 #pragma unroll
-      for (int first = 0; first < kLoad; first += kBatch) {
+      for (int first = 0; first < kLoad; first += N) {
         if (s0 + first >= hi) break;
-        F2 v[kBatch][4];
+        F2 v[N][4];
 #pragma unroll
-        for (int u = 0; u < kBatch; u++) decode<SRC, RUN>(raw[first + u], v[u]);
+        for (int u = 0; u < N; u++) decode<SRC, RUN>(raw[first + u], v[u]);
         if constexpr (MODE == kTurn) {
           if (rotated) {  // elsewhere an infinite neighbour would make 0 * inf
 #pragma unroll
@@ -399,7 +406,7 @@ __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_
               const float2 c0 = cs[INTER ? xa / 2 + e : xa + 2 * e], c1 = INTER ? c0 : cs[xa + 2 * e + 1];
               const F2 co = f2(c0.x, c1.x), si = INTER ? f2(-c0.y, c0.y) : f2(c0.y, c1.y), ni = f2(-c0.y, -c1.y);
 #pragma unroll
-              for (int u = 0; u < kBatch; u++) {
+              for (int u = 0; u < N; u++) {
                 const F2 p = v[u][e];
                 if (INTER) {
                   const float2 x = f2_out(p);
@@ -414,14 +421,14 @@ __device__ __forceinline__ void run_heads(const MoveArgs& a, bool values, int64_
           }
         }
         encode<DST, RUN, LPH>(v, dst0 + first * HPW * dst_pitch, dst_pitch, dscale, h0 + first * HPW, a.Hkv,
-                              min(kBatch, hi - s0 - first), lane, xa, xb);
+                              min(N, hi - s0 - first), lane, xa, xb);
       }
     }
   }
 }
 
 template <int D, int SRC, int DST, bool INTER>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) move_kernel(const MoveArgs a) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, DST)) move_kernel(const MoveArgs a) {
   constexpr int LPH = D / 8;
   __shared__ uint64_t turns[2][D / 2];
   __shared__ __align__(16) float2 cs[kWarps][D / 2];  // each warp's token: (cos, sin) by frequency
@@ -548,7 +555,8 @@ SKV_EXPORT int skv_move_rows(int64_t n, int Hkv, int d, const skv_row_set* src, 
   // Work items: a token's K or V heads in pieces, so that the rounds of the
   // resident warps times the steps of a piece (each paying about three steps for
   // its rows and sines) come out lowest.
-  const int64_t warps = static_cast<int64_t>(sms) * kCtasPerSm * kWarps;
+  const int per_sm = ctas_per_sm(d, dst->kind);
+  const int64_t warps = static_cast<int64_t>(sms) * per_sm * kWarps;
   int64_t best = INT64_MAX;
   int chunks = 1;
   for (int c = 1; c <= a.steps; c++) {
@@ -565,7 +573,7 @@ SKV_EXPORT int skv_move_rows(int64_t n, int Hkv, int d, const skv_row_set* src, 
   a.chunks_v = src->v ? chunks : 0;
   if (n > (1 << 30) / (parts * chunks)) return SKV_EINVAL;  // work items are counted in 32 bits
   const int64_t want = (n * parts * chunks + kWarps - 1) / kWarps;
-  const int64_t cap = static_cast<int64_t>(sms) * kCtasPerSm;
+  const int64_t cap = static_cast<int64_t>(sms) * per_sm;
   const int grid = static_cast<int>(want < cap ? want : cap);
   cudaStream_t st = as_stream(stream);
   if (d == 64)
