@@ -503,7 +503,8 @@ int side(const skv_row_set* s, int64_t n, int Hkv, int d, const int64_t* rows, R
   if (s->kind == SKV_KV_INT4) {
     out->token_pitch = s->token_pitch;
     out->head_pitch = s->head_pitch;
-    if (s->head_pitch < d / 2 + d / 32 || s->token_pitch < Hkv * s->head_pitch) return SKV_EINVAL;
+    if (s->head_pitch < d / 2 + d / 32 || s->head_pitch > INT64_MAX / Hkv || s->token_pitch < Hkv * s->head_pitch)
+      return SKV_EINVAL;
     if ((reinterpret_cast<uintptr_t>(s->k) | reinterpret_cast<uintptr_t>(s->v) | s->token_pitch | s->head_pitch) & 3)
       return SKV_EINVAL;
     return SKV_OK;
@@ -524,7 +525,7 @@ SKV_EXPORT int skv_move_rows(int64_t n, int Hkv, int d, const skv_row_set* src, 
                              const skv_row_set* dst, const int64_t* dst_rows, int rot, int interleaved,
                              const int32_t* old_positions, const float* old_inv_freq, const int32_t* new_positions,
                              const float* new_inv_freq, int32_t* dev_status, void* stream) {
-  if (n < 0 || Hkv < 1 || Hkv > 4096 || !src || !dst) return SKV_EINVAL;
+  if (n < 0 || n > 1 << 29 || Hkv < 1 || Hkv > 4096 || !src || !dst) return SKV_EINVAL;  // 32-bit work items
   for (const skv_row_set* s : {src, dst})
     if (s->kind != SKV_KV_BF16 && s->kind != SKV_KV_INT8 && s->kind != SKV_KV_INT4) return SKV_EINVAL;
   if (d != 256 && ((d != 64 && d != 128) || src->kind == SKV_KV_INT4 || dst->kind == SKV_KV_INT4)) return SKV_EUNSUPPORTED;
@@ -571,7 +572,6 @@ SKV_EXPORT int skv_move_rows(int64_t n, int Hkv, int d, const skv_row_set* src, 
   }
   a.chunks_k = src->k ? chunks : 0;
   a.chunks_v = src->v ? chunks : 0;
-  if (n > (1 << 30) / (parts * chunks)) return SKV_EINVAL;  // work items are counted in 32 bits
   const int64_t want = (n * parts * chunks + kWarps - 1) / kWarps;
   const int64_t cap = static_cast<int64_t>(sms) * per_sm;
   const int grid = static_cast<int>(want < cap ? want : cap);

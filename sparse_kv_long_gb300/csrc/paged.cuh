@@ -2082,6 +2082,14 @@ constexpr bool fits(int d, int ctas, bool int8) {
 static_assert(fits(128, 1, false) && fits(128, 2, false) && fits(256, 1, false) && fits(256, 2, false) &&
                   fits(128, 1, true) && fits(128, 2, true) && fits(256, 1, true) && fits(256, 2, true),
               "every kind of call has its stages");
+// The ring that the batch waits in while pairs plan.
+constexpr int ring_bytes(int d, bool int8) {
+  return shared_layout(d, 2, int8, kRows * 128).stages * (keys_per_tile(d, 2) / 2 * d * 2);
+}
+constexpr int kMaxEntries = 8192;  // requests and groups
+static_assert(ring_bytes(128, false) >= 8 * kMaxEntries && ring_bytes(128, true) >= 8 * kMaxEntries &&
+                  ring_bytes(256, false) >= 8 * kMaxEntries && ring_bytes(256, true) >= 8 * kMaxEntries,
+              "eight bytes for each");
 
 }  // namespace
 }  // namespace skv

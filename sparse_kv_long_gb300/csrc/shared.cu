@@ -246,6 +246,7 @@ SKV_EXPORT int skv_shared_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv,
                                  const int32_t* q_start, const int32_t* lengths, float softmax_scale, uint16_t* out,
                                  void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
   if (kv_kind != SKV_KV_BF16 && kv_kind != SKV_KV_INT8) return SKV_EINVAL;
+  static_assert(kMaxEntries >= 2 * 4096, "requests and groups");
   if (B < 0 || B > 4096 || n_tok < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || n_groups < 0 || n_groups > 4096 || n_pages < 0 ||
       n_prefix_pages < 0)
     return SKV_EINVAL;

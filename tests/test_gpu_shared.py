@@ -422,6 +422,31 @@ def test_calls_of_many_sizes_queued_on_one_workspace(skv):
     assert all(int(c.st.item()) == 0 for c in cases)
 
 
+@pytest.mark.parametrize("kind,new,start,prefix", [
+    ("bf16", [1] * 4096, [0] + list(range(1, 4096)) + [4096], [5, 0, 64, 17] * 1024),  # a group for each request
+    ("int8", [1, 0, 2, 1] * 1024, [0, 2000, 4096], [100, 130]),
+    ("bf16", [3] * 4000, list(range(0, 4001, 40)), [70] * 100),
+])
+def test_the_largest_batches(skv, kind, new, start, prefix):
+    """4096 requests and 4096 groups: plans of many windows, as single CTAs and as pairs."""
+    lens = [m + i % 5 for i, m in enumerate(new)]
+    for wide in (0, 2100):
+        if wide and len(prefix) > 1000:
+            continue
+        c = Case(skv, kind_of(skv, kind), 256, 2, 1, 16, start, prefix, lens, new, seed=60, extra_pages=wide)
+        got = f64(c.run(single=all(m == 1 for m in new)))
+        assert int(c.st.item()) == 0
+        tok = np.random.default_rng(0).choice(len(got), 300, replace=False)
+        b = np.searchsorted(c.starts, tok, side="right") - 1
+        k, v = c.values()
+        for t, r in zip(tok, b):  # a request at a time: the plain form of one token
+            m, g = int(c.starts[r + 1] - c.starts[r]), int(np.searchsorted(c.start, r, side="right") - 1)
+            own = lens[r] - m + int(t - c.starts[r]) + 1
+            ref, spread = plain.shared_attend(f64(c.q)[t:t + 1], k, v, [0, 1], c.ptable[g:g + 1], [prefix[g]], c.table[r:r + 1], 16,
+                                              [own], c.scale, [0, 1])
+            assert (np.abs(got[t] - ref[0]) <= tolerance(ref, spread)[0]).all()
+
+
 def test_two_streams_at_once(skv):
     """Calls on two streams with a workspace each."""
     cases = [Case(skv, skv.KV_BF16, 256, 8, 2, 16, [0, 3], [3000 + 500 * i], [30, 1, 400], [1, 1, 1], seed=40 + i)
@@ -460,14 +485,15 @@ def hasty(skv, tmp_path_factory):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("d,P,lens,new,single", [
-    (256, 9000, [20, 2000, 30], [1, 1, 1], True), (128, 20000, [30], [3], False), (256, 3000, [30] * 9, [8] * 9, False),
-    (128, 9000, [300, 300], [300, 300], False),
+@pytest.mark.parametrize("d,P,lens,new,single,wide", [
+    (256, 9000, [20, 2000, 30], [1, 1, 1], True, 0), (128, 20000, [30], [3], False, 0), (256, 3000, [30] * 9, [8] * 9, False, 0),
+    (128, 9000, [300, 300], [300, 300], False, 0), (256, 9000, [20, 900, 1, 0] * 12, [1] * 48, True, 2048),
 ])
-def test_waits_that_give_up(skv, hasty, monkeypatch, kind, d, P, lens, new, single):
+def test_waits_that_give_up(skv, hasty, monkeypatch, kind, d, P, lens, new, single, wide):
     """A call whose waits give up sets SKV_DEV_TIMEOUT and touches nothing but its tokens' output and its workspace,
     whatever that held; the next call on the same buffers is right."""
-    c = Case(skv, kind_of(skv, kind), d, 8, 2, 16, [0, len(lens)], [P], lens, new, seed=50, pad=0 if single else 3)
+    c = Case(skv, kind_of(skv, kind), d, 8, 2, 16, [0, len(lens)], [P], lens, new, seed=50, pad=0 if single else 3,
+             extra_pages=wide)
     want = c.run(single=single).clone()
     need = c.ws.numel()
     ws = torch.full((need + 4096,), 0x7F, dtype=torch.uint8, device="cuda")

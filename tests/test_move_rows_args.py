@@ -40,6 +40,7 @@ MOVE = dict(n=4, Hkv=2, d=256, src=rows(INT8), srows=P(256), dst=rows(BF16), dro
     (dict(srows=None, src=rows(INT8, n_rows=3)), EINVAL), (dict(drows=None, dst=rows(BF16, n_rows=3)), EINVAL),
     (dict(oldf=None), EINVAL), (dict(newf=None), EINVAL), (dict(src=rows(INT4, k=258)), EINVAL),
     (dict(src=rows(INT4, head_pitch=270)), EINVAL), (dict(src=rows(INT4, head_pitch=132)), EINVAL),
+    (dict(src=rows(INT4, head_pitch=1 << 62, token_pitch=1 << 62)), EINVAL), (dict(n=1 << 30), EINVAL),
     (dict(src=rows(INT4, token_pitch=540)), EINVAL), (dict(dst=rows(INT4, token_pitch=546)), EINVAL),
 ])
 def test_move_rows_refuses(skv, change, want):

@@ -49,9 +49,9 @@ def test_workspace_sizes(lib):
     sizes = [size(4, 2, n, 8, 2, 256) for n in (1, 2, 31, 32, 33, 40, 400, 4000)]
     assert sizes[0] > 0 and sizes == sorted(sizes)
     assert len({size(B, g, 40, 8, 2, 256) for B in (1, 40, 4096) for g in (0, 1, 40)}) == 1
-    for n in (1, 40, 4000):  # 8 d + 24 bytes a token and query head beside the partial sums
-        more = size(4, 2, n, 8, 2, 256) - lib.skv_paged_attend_workspace_size(4, n, 8, 2, 256)
-        assert 0 < more <= n * 8 * (8 * 256 + 24) + 1024
+    for n in (1, 32, 33, 40, 4000):  # 8 d + 24 bytes a token and query head beside the partial sums
+        sums = lib.skv_paged_attend_workspace_size(4, n, 8, 2, 256)
+        assert sums < size(4, 2, n, 8, 2, 256) <= sums * (1.25 if n * 4 > 128 else 1) + n * 8 * (8 * 256 + 24) + 1024
     for bad in [(0, 1, 1, 8, 2, 256), (1, -1, 1, 8, 2, 256), (1, 1, 0, 8, 2, 256), (1, 1, 1, 8, 3, 256), (1, 1, 1, 8, 2, 96),
                 (1, 1, 1, 258, 2, 256), (1, 1, 1 << 26, 8, 2, 256)]:
         assert size(*bad) == 0
