@@ -129,10 +129,11 @@ struct Piece {
   int tok0, toks;     // first token, tokens of the whole tile
   int pos0;           // position of the first token
   int b, h;           // request; with prefixes: -1 for a group's tokens over its prefix
-  int lo, nsink;      // first window tile, sink tiles before it; with prefixes: group, prefix tiles before the request's
-  int plen;           // with prefixes: the prefix's keys
+  int lo, nsink;      // first window tile, sink tiles before it; with prefixes: the prefix's keys, its tiles before the request's
   int j0, n;          // this piece's tiles: j0 .. j0 + n of the item's list
-  int slot;           // partial slot, -1: whole item, kDense: whole, but joined with its prefix or its own keys
+  int slot;           // partial slot, -1: whole item, kDense: whole, but joined with its prefix or its own keys;
+                      // with prefixes as slot_of and group_of read it: a field more cost the kernels without
+                      // them registers (windowed int8 chunk 139.5 -> 141.5 us)
   int last;           // no piece follows
 };
 
@@ -639,6 +640,15 @@ struct Ring {  // a stage index and the parity of its current use
   }
 };
 
+constexpr int kSlotBits = 12;
+__device__ __forceinline__ int slot_and_group(int slot, int g) { return (slot - kDense) | g << kSlotBits; }
+template <bool PRE>
+__device__ __forceinline__ int slot_of(const Piece& pc) {
+  return PRE ? (pc.slot & ((1 << kSlotBits) - 1)) + kDense : pc.slot;
+}
+__device__ __forceinline__ int group_of(const Piece& pc) { return pc.slot >> kSlotBits; }
+static_assert(2 + (kSplitPerPair + 2) * kMaxPieces / 2 + 2 < 1 << kSlotBits && 2 + 2 * kMaxPieces + 2 < 1 << kSlotBits, "slots fit");
+
 // Whether tile j of a piece is of a prefix, which every row sees all of.
 template <bool PRE>
 __device__ __forceinline__ bool of_prefix(const Piece& pc, int j) {
@@ -647,7 +657,7 @@ __device__ __forceinline__ bool of_prefix(const Piece& pc, int j) {
 // The last key of tile j's part that the row of position `pos` (of the request's own keys) sees.
 template <bool PRE>
 __device__ __forceinline__ int seen(const Piece& pc, int j, int pos) {
-  return of_prefix<PRE>(pc, j) ? pc.plen - 1 : pos;
+  return of_prefix<PRE>(pc, j) ? pc.lo - 1 : pos;
 }
 template <bool PRE>
 __device__ __forceinline__ int last_seen(const Piece& pc, int j) {
@@ -658,7 +668,7 @@ template <bool PRE>
 __device__ __forceinline__ const int32_t* pages_of(const PagedArgs& a, const Piece& pc, int j, int64_t& n) {
   if (of_prefix<PRE>(pc, j)) {
     n = a.n_prefix_pages;
-    return a.prefix_table + pc.lo * n;
+    return a.prefix_table + group_of(pc) * n;
   }
   n = a.n_pages;
   return a.block_table + pc.b * n;
@@ -1172,6 +1182,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
           q.kind = __shfl_sync(full, r.kind, w);
           q.g = __shfl_sync(full, r.g, w);
           q.plen = __shfl_sync(full, r.plen, w);
+          pc.slot = -1;  // (an item passed over has left its own)
         }
         const int before = __shfl_sync(full, pp, w);
         int item, nt, first = 0, n_seg = 1, seg = 0, list = 0;  // of a split item: pieces, this one's number, its place in the list
@@ -1209,8 +1220,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
                                        : 0;
           nt = pc.nsink + own;
           pc.b = q.kind == kPrefix ? -1 : pc.b - a.n_groups;
-          pc.lo = q.g;
-          pc.plen = q.plen;
+          pc.lo = q.plen;
           if (pc.slot < 0 && (q.kind == kPrefix || q.kind == kBehind)) pc.slot = kDense;
         } else {
           tile_range<KT>(a, q, qt, pc.lo, pc.nsink, nt);
@@ -1258,6 +1268,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
               a.ws_rows[(static_cast<int64_t>(prefix ? a.n_tok : 0) + pc.tok0 + i) * a.Hkv + pc.h] =
                   make_int4(n, one + i * pitch, two + i * a.G, (stretch ? 2 : 1) * a.part_rows);
           }
+          pc.slot = slot_and_group(pc.slot, q.g);
         } else if (!pc.last && n_seg > 1 && seg == 0 && rank == 0 && lane == 0) {
           a.ws_item[2 * list] = make_int4(pc.tok0, pc.toks * a.G, pc.h, pc.slot);
           // pieces; the slots of the second and of each further one
@@ -1782,7 +1793,8 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
       }
       // ---- output: this group's half of the columns ----
       if (warp_live) {
-        const bool whole = PRE ? pc.slot == -1 : pc.slot < 0;
+        const int part = slot_of<PRE>(pc);
+        const bool whole = PRE ? part == -1 : part < 0;
         if (SUM && pc.n > 0) {
           const float2 s2 = tmem_ld2(tm + lane_base + LCOL);
           l = INT8 ? s2.x + s2.y : s2.x;
@@ -1790,9 +1802,9 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         const float inv = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
         const bool dirty = !INT8 && *reinterpret_cast<volatile int*>(&ax->dirty) != 0;
         const int64_t tok = static_cast<int64_t>(pc.tok0) + tok_i;
-        int64_t prow = static_cast<int64_t>(pc.slot) * a.part_rows + tok_i * a.G + head_r;
+        int64_t prow = static_cast<int64_t>(part) * a.part_rows + tok_i * a.G + head_r;
         if (PRE)
-          prow = pc.slot == kDense ? ((pc.b < 0 ? a.n_tok : 0) + tok) * (a.Hkv * a.G) + pc.h * a.G + head_r
+          prow = part == kDense ? ((pc.b < 0 ? a.n_tok : 0) + tok) * (a.Hkv * a.G) + pc.h * a.G + head_r
                                    : prow + a.n_dense;
         unsigned char* buf = sOut + (warp - 4) * 2048;
         const int id = !live ? -1 : whole ? static_cast<int>(tok * (a.Hkv * a.G)) + pc.h * a.G + head_r : static_cast<int>(prow);
