@@ -1733,10 +1733,11 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
           unsigned char* V = sKV + vs * STAGE;
           bool found = false;
           // A single token's keys, and a prefix's, every query of the tile sees or none
-          // does: there is nothing to look for.
+          // does: there is nothing to look for, and nothing before the first unseen row.
           const bool alike = PRE && (pc.toks == 1 || of_prefix<PRE>(pc, j));
+          const int skip = alike && bad == 0 ? (max(p_last + 1 - t0, 0) >> 3) * (VSUB * 64) : 0;
 #pragma unroll 1
-          for (int i = tid - 128; i < STAGE / 16; i += 256) {
+          for (int i = skip + tid - 128; i < STAGE / 16; i += 256) {
             const int grp = i / (VSUB * 64), row = grp * 8 + ((i >> 3) & 7);  // 64 16-byte pieces per 1024 B block
             uint4* at = reinterpret_cast<uint4*>(V + i * 16);
             const int key = t0 + row;  // seen by no query of the tile: its page may not have been read
