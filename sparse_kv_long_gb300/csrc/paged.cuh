@@ -53,14 +53,18 @@
 // K and V tiles are 5-dimensional TMA boxes of whole pages (or the largest
 // power-of-two part of one), laid out as [8-row group][64-column block][8 x
 // 128 B], 128-byte swizzle: one box per page brings all dims.  int8 rows
-// arrive in a staging ring and four warps (eight for single tokens) widen them to bf16 (exact); the K
-// scales multiply the logits, the V scales the weights.
+// arrive in a staging ring and four warps (eight for few rows) widen them to
+// bf16 (exact); the K scales multiply the logits, the V scales the weights.
 //
 // Work list: items (request, query tile, KV head), made on the device from the
 // lengths.  Single CTAs share the batch's key tiles evenly; pairs cut items
 // into pieces of about c tiles, c by the cost of a few candidates (see the
 // plan).  Whole items write bf16 output, pieces write fp32 partials that
 // merge_kernel joins in piece order.
+//
+// With prefixes that requests share (PRE; shared.cu) entries of the work list are
+// groups over their prefixes, requests over their own keys, or requests over both;
+// a piece's tiles up to nsink are then of a prefix.
 #pragma once
 
 #include <cuda.h>
