@@ -37,112 +37,139 @@ namespace {
 
 // Joins the state rows of each token and head, the prefix's first.  Launched
 // early, as the merge of paged.cu, and for the same reasons nothing here is
-// declared read-only and nothing starts early behind it.  With a warp per row as
-// soon as rows outnumber blocks, 64 samples at 131072 tokens (1024 rows) took 118
-// us, with four 110.
+// declared read-only and nothing starts early behind it.
+//
+// Bound by what follows one another: descriptors, maxima and sums, values.  A block
+// takes every gridDim-th row, reads their descriptors at once, lists those that are
+// to be joined (most of a chunk's were written directly, and the others lie side by
+// side) and shares its warps out among them: 5 questions of up to 333 tokens 53 us,
+// with warps shared out among all rows 62.5; 64 samples 102, with a warp per row 110.
+constexpr int kMergeWarps = 16;
+constexpr int kMergeRows = 128;  // listed at once
 template <int D>
-__global__ void __launch_bounds__(256) merge_kernel(const int* head, const int4* rows, const float2* ml, const float* o,
-                                                    const int32_t* q_start, int B, int n_tok, int Hkv, int G,
-                                                    uint16_t* out) {
+__global__ void __launch_bounds__(32 * kMergeWarps, 2)
+    merge_kernel(const int* head, const int4* rows, const float2* ml, const float* o, const int32_t* q_start, int B,
+                 int n_tok, int Hkv, int G, uint16_t* out) {
   constexpr int E = D / 32;  // columns per lane: float4 f at 4 (lane + 32 f)
   constexpr int Q = 2 * kMaxPieces / 32;
-  __shared__ __align__(16) float red[8][D];
-  __shared__ float weight[8][2 * kMaxPieces];
+  __shared__ __align__(16) float red[kMergeWarps][D];
+  __shared__ float weight[kMergeWarps][2 * kMaxPieces];
+  __shared__ int4 own[kMergeRows], pre[kMergeRows];
+  __shared__ int row[kMergeRows], listed[kMergeRows / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
   const int Hq = Hkv * G, tasks = n_tok * Hq;
   const int disorder = head[0];
   const int first_tok = q_start ? q_start[0] : 0, end_tok = q_start ? q_start[B] : n_tok;
-  if (disorder) return;
-  // as many warps to a row as there are for each
-  int team = 8;
-  while (team > 1 && tasks > static_cast<int>(gridDim.x) * 8 / team) team >>= 1;
-  const int s0 = warp & (team - 1), per_block = 8 / team;
 #pragma unroll 1
-  for (int w0 = blockIdx.x * per_block; w0 < tasks; w0 += gridDim.x * per_block) {
-    const int w = w0 + warp / team;
-    const int tok = min(w, tasks - 1) / Hq, hq = w - tok * Hq, h = hq / G, g = hq - h * G;
-    bool live = w < tasks && tok >= first_tok && tok < end_tok;  // padding: its rows were not listed
+  for (int64_t i0 = blockIdx.x; i0 < tasks; i0 += static_cast<int64_t>(kMergeRows) * gridDim.x) {
     int4 x = make_int4(0, 0, 0, 0), y = x;
-    if (live) {
+    const int64_t at = i0 + static_cast<int64_t>(threadIdx.x) * gridDim.x;
+    if (threadIdx.x < kMergeRows && at < tasks) {
+      const int tok = static_cast<int>(at) / Hq, h = (static_cast<int>(at) - tok * Hq) / G;
       x = rows[static_cast<int64_t>(tok) * Hkv + h];
       y = rows[(static_cast<int64_t>(n_tok) + tok) * Hkv + h];
+      if (disorder || tok < first_tok || tok >= end_tok) x.x = 0;  // padding: its rows were not listed
     }
-    const int n_own = min(x.x & (kHasPrefix - 1), kMaxPieces), n_pre = x.x & kHasPrefix ? min(y.x, kMaxPieces) : 0;
-    live &= n_own > 0;  // else written directly
-    const int n = live ? n_pre + n_own : 0;
-    auto row_of = [&](int s) -> int64_t {
-      if (s < n_pre) return g + (s == 0 ? y.y : y.z + (s - 1) * y.w);
-      s -= n_pre;
-      return g + (s == 0 ? x.y : x.z + (s - 1) * x.w);
-    };
-    float2 v[Q];
-    float m = -INFINITY;
+    const uint32_t live = __ballot_sync(0xffffffffu, (x.x & (kHasPrefix - 1)) > 0);  // the others were written directly
+    if (lane == 0 && warp < kMergeRows / 32) listed[warp] = __popc(live);
+    __syncthreads();
+    int n_rows = 0, mine = 0;
 #pragma unroll
-    for (int i = 0; i < Q; i++) {
-      v[i] = make_float2(-INFINITY, 0.f);
-      if (lane + 32 * i < n) v[i] = ml[row_of(lane + 32 * i)];
-      m = fmaxf(m, v[i].x);
+    for (int i = 0; i < kMergeRows / 32; i++) {
+      mine += i < warp ? listed[i] : 0;
+      n_rows += listed[i];
     }
-#pragma unroll
-    for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    // One without a visible key takes no part, and its o may be unwritten:
-    // marked with a weight of -1.  One whose weight vanishes beside another's
-    // does take part: what is not finite in it reaches the output.
-    float den = 0.f;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < Q; i++) {
-      const bool none = v[i].x == -INFINITY && v[i].y == 0.f;
-      const float f = none ? 0.f : exp2f(v[i].x - m);
-      den += none ? 0.f : f * v[i].y;
-      weight[warp][lane + 32 * i] = none ? -1.f : f;
+    if (live >> lane & 1u) {
+      mine += __popc(live & ((1u << lane) - 1u));
+      own[mine] = x;
+      pre[mine] = y;
+      row[mine] = static_cast<int>(at);
     }
-    __syncwarp();
+    __syncthreads();
+    int team = kMergeWarps;  // warps to a row
+    while (team > 1 && n_rows * team > kMergeWarps) team >>= 1;
+    const int s0 = warp & (team - 1);
+#pragma unroll 1
+    for (int r = warp / team; r < n_rows || team > 1; r += kMergeWarps / team) {
+      const bool there = r < n_rows;
+      x = there ? own[r] : make_int4(0, 0, 0, 0);
+      y = there ? pre[r] : x;
+      const int w = there ? row[r] : 0, g = w % G;
+      const int n_own = min(x.x & (kHasPrefix - 1), kMaxPieces), n_pre = x.x & kHasPrefix ? min(y.x, kMaxPieces) : 0;
+      const int n = n_pre + n_own;
+      auto row_of = [&](int s) -> int64_t {
+        if (s < n_pre) return g + (s == 0 ? y.y : y.z + (s - 1) * y.w);
+        s -= n_pre;
+        return g + (s == 0 ? x.y : x.z + (s - 1) * x.w);
+      };
+      float2 v[Q];
+      float m = -INFINITY;
 #pragma unroll
-    for (int i = 16; i; i >>= 1) den += __shfl_xor_sync(0xffffffffu, den, i);
-    float acc[E];
-#pragma unroll
-    for (int e = 0; e < E; e++) acc[e] = 0.f;
-#pragma unroll 8
-    for (int s = s0; s < n; s += team) {
-      const float f = weight[warp][s];
-      if (f < 0.f) continue;
-      const float* src = o + row_of(s) * D + 4 * lane;
-#pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const float4 z = *reinterpret_cast<const float4*>(src + 32 * e);
-        acc[e] += f * z.x;
-        acc[e + 1] += f * z.y;
-        acc[e + 2] += f * z.z;
-        acc[e + 3] += f * z.w;
+      for (int i = 0; i < Q; i++) {
+        v[i] = make_float2(-INFINITY, 0.f);
+        if (lane + 32 * i < n) v[i] = ml[row_of(lane + 32 * i)];
+        m = fmaxf(m, v[i].x);
       }
-    }
-    const float inv = den != 0.f ? 1.f / den : 0.f;
-    uint16_t* dst = out + static_cast<int64_t>(min(w, tasks - 1)) * D;
-    if (team > 1) {
+#pragma unroll
+      for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+      // One without a visible key takes no part, and its o may be unwritten:
+      // marked with a weight of -1.  One whose weight vanishes beside another's
+      // does take part: what is not finite in it reaches the output.
+      float den = 0.f;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < Q; i++) {
+        const bool none = v[i].x == -INFINITY && v[i].y == 0.f;
+        const float f = none ? 0.f : exp2f(v[i].x - m);
+        den += none ? 0.f : f * v[i].y;
+        if (32 * i < n) weight[warp][lane + 32 * i] = none ? -1.f : f;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 16; i; i >>= 1) den += __shfl_xor_sync(0xffffffffu, den, i);
+      float acc[E];
+#pragma unroll
+      for (int e = 0; e < E; e++) acc[e] = 0.f;
+#pragma unroll 8
+      for (int s = s0; s < n; s += team) {
+        const float f = weight[warp][s];
+        if (f < 0.f) continue;
+        const float* src = o + row_of(s) * D + 4 * lane;
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const float4 z = *reinterpret_cast<const float4*>(src + 32 * e);
+          acc[e] += f * z.x;
+          acc[e + 1] += f * z.y;
+          acc[e + 2] += f * z.z;
+          acc[e + 3] += f * z.w;
+        }
+      }
+      const float inv = den != 0.f ? 1.f / den : 0.f;
+      uint16_t* dst = out + static_cast<int64_t>(w) * D;
+      if (team == 1) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4)
+          *reinterpret_cast<uint2*>(dst + 4 * lane + 32 * e) =
+              make_uint2(pack_bf16(acc[e] * inv, acc[e + 1] * inv), pack_bf16(acc[e + 2] * inv, acc[e + 3] * inv));
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < E; e += 4)
         *reinterpret_cast<float4*>(&red[warp][4 * lane + 32 * e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
       __syncthreads();
-      if (live) {
-        for (int c = 32 * s0 + lane; c < D / 2; c += 32 * team) {
-          float2 sum = make_float2(0.f, 0.f);
-          for (int i = 0; i < team; i++) {
-            const float2 z = *reinterpret_cast<const float2*>(&red[warp - s0 + i][2 * c]);
-            sum.x += z.x;
-            sum.y += z.y;
-          }
-          *reinterpret_cast<uint32_t*>(dst + 2 * c) = pack_bf16(sum.x * inv, sum.y * inv);
+      for (int c = 32 * s0 + lane; there && c < D / 2; c += 32 * team) {
+        float2 sum = make_float2(0.f, 0.f);
+        for (int i = 0; i < team; i++) {
+          const float2 r2 = *reinterpret_cast<const float2*>(&red[warp - s0 + i][2 * c]);
+          sum.x += r2.x;
+          sum.y += r2.y;
         }
+        *reinterpret_cast<uint32_t*>(dst + 2 * c) = pack_bf16(sum.x * inv, sum.y * inv);
       }
-      __syncthreads();
-    } else if (live) {
-#pragma unroll
-      for (int e = 0; e < E; e += 4)
-        *reinterpret_cast<uint2*>(dst + 4 * lane + 32 * e) =
-            make_uint2(pack_bf16(acc[e] * inv, acc[e + 1] * inv), pack_bf16(acc[e + 2] * inv, acc[e + 3] * inv));
+      break;  // a team has one row at most
     }
+    __syncthreads();
   }
 }
 
@@ -213,8 +240,8 @@ int launch(const PagedArgs& a, const Maps<true>& maps, int smem, int sms, cudaSt
     cudaGetLastError();
     return SKV_ECUDA;
   }
-  cfg.gridDim = dim3(4 * sms, 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.gridDim = dim3(2 * sms, 1, 1);
+  cfg.blockDim = dim3(32 * kMergeWarps, 1, 1);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   const int* head = a.ws_head;
