@@ -447,6 +447,25 @@ def test_the_largest_batches(skv, kind, new, start, prefix):
             assert (np.abs(got[t] - ref[0]) <= tolerance(ref, spread)[0]).all()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_pages_past_32_bits(skv, kind):
+    """Pages more than 2^32 bytes into their pools: the same bits as from the first ones."""
+    for n in (1, 70):
+        c = Case(skv, kind_of(skv, kind), 256, 16, 8, 16, [0, 2], [300], [n + 20] * 3, [n] * 3, seed=70)
+        want, rows = c.run().clone(), c.k.shape[0]
+        first = ((1 << 32) // (8 * 256 * c.k.element_size()) // 16 + 7) * 16
+        for name in ("k", "v", "ks", "vs"):
+            x = getattr(c, name)
+            if x is not None:
+                far = torch.zeros((first + rows, *x.shape[1:]), dtype=x.dtype, device="cuda")
+                far[first:] = x
+                setattr(c, name, far)
+        for x in (c.ptable, c.table):
+            x[x >= 0] += first // 16
+        assert torch.equal(c.run(), want) and int(c.st.item()) == 0
+        del c
+
+
 def test_two_streams_at_once(skv):
     """Calls on two streams with a workspace each."""
     cases = [Case(skv, skv.KV_BF16, 256, 8, 2, 16, [0, 3], [3000 + 500 * i], [30, 1, 400], [1, 1, 1], seed=40 + i)
