@@ -1588,6 +1588,7 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
     };
 
     Piece pc;
+    bool ready = false;  // the next tile's logits (and scales) are known to be there
     ok = get(0, pc);
 #pragma unroll 1
     for (int k = 0; ok && !pc.last; k++) {
@@ -1608,8 +1609,11 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
         constexpr int HC = KT / 2;  // this group's keys of the tile
         const uint32_t scol = tm + lane_base + kSCol + (t & 1) * 128 + wg * HC;
         const uint32_t sc = t % kScaleRing;
-        if (INT8 && !(ok = wait_all(&a8->sc_full[sc], (t / kScaleRing) & 1, abort))) break;
-        if (!(ok = wait_all(&ax->s_full[t & 1], (t >> 1) & 1, abort))) break;
+        if (!(PRE && INT8) || !__all_sync(0xffffffffu, ready)) {
+          if (INT8 && !(ok = wait_all(&a8->sc_full[sc], (t / kScaleRing) & 1, abort))) break;
+          if (!(ok = wait_all(&ax->s_full[t & 1], (t >> 1) & 1, abort))) break;
+        }
+        ready = false;
         tc::tc_fence_after();
         const uint32_t bad = ax->tile_bad[t % kTileInfo];
         const bool masked = edge || bad != 0;
@@ -1685,6 +1689,14 @@ __global__ void __launch_bounds__(kThreads<INT8>, 1)
             }
             l = m_ref == -INFINITY ? 0.f : l * alpha;
             m_ref = m_new;
+          }
+          // Asked for under the exponentials, the next tile's logits and scales mostly
+          // cost no wait: 80 drafts 155 -> 148 us (with 3 wide stages), eight agents
+          // 144.7 -> 143.4.  Without prefixes the windowed chunk lost (136.4, 139.7),
+          // and bf16 rows (57.0, 59.1 for 40 tokens behind five prefixes).
+          if (PRE && INT8) {
+            ready = tc::bar_poll(&ax->s_full[(t + 1) & 1], ((t + 1) >> 1) & 1);
+            ready &= tc::bar_poll(&a8->sc_full[(t + 1) % kScaleRing], ((t + 1) / kScaleRing) & 1);
           }
           const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
           const F2 ff = f2(f, f), mm = f2(-m_use, -m_use);
@@ -2075,11 +2087,12 @@ int tile_rows(int n_tok, int G, int ctas) {
 // Shared memory of a CTA: the query tile (q_sub bytes per 64 columns), then as
 // many stages as fit.  int8 rows: four wide stages (pairs three, six of half
 // the size at 128 dims), the rest staging; where that would leave fewer than
-// two staging slots, as beside a full query tile of 256 dims, a wide stage
+// two staging slots (128 dims: three), as beside a full query tile, a wide stage
 // makes room (64 ragged requests: 3 and 6 slots 130.2 us, 4 and 4 129.3, 5 and
-// 2 156).  With q_start the tokens of a request are not known here, so a batch
-// of single tokens gets a full tile's layout: the same requests take 153 us
-// with q_start, 118 without (bf16 rows 134 either way).
+// 2 156; 80 drafts of 128 dims behind 60000 keys: 4 and 2 155, 3 and 4 148).  With
+// q_start the tokens of a request are not known here, so a batch of single tokens
+// gets a full tile's layout: the same requests take 153 us with q_start, 118
+// without (bf16 rows 134 either way).
 struct Shared {
   int q_bytes, stages, staging, total;
 };
@@ -2092,7 +2105,7 @@ constexpr Shared shared_layout(int d, int ctas, bool int8, int q_sub) {
   const int room = kMaxSmem - kOutBytes - aux - s.q_bytes;
   if (int8) {
     s.stages = ctas == 1 ? 4 : d == 128 ? 6 : 3;
-    while (s.stages > 1 && (room - s.stages * stage) / (stage / 2) < 2) s.stages--;
+    while (s.stages > 1 && (room - s.stages * stage) / (stage / 2) < (d == 128 ? 3 : 2)) s.stages--;
     s.staging = (room - s.stages * stage) / (stage / 2);
     if (s.staging > kMaxStaging) s.staging = kMaxStaging;
   } else {

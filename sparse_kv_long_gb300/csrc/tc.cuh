@@ -67,6 +67,18 @@ __device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity, bool cl
   return ok != 0;
 }
 
+// As bar_test without a scope, but answers at once.
+__device__ __forceinline__ bool bar_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Bounded wait for the phase with the given parity to complete.  Gives up
 // after `limit_ns` of wall time (or at once when *abort is set), sets *abort
 // and returns false; the caller then skips its remaining work.
