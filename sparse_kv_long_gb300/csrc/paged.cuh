@@ -34,9 +34,9 @@
 //    247 us, 0.8 PFLOP/s with their masked tiles.
 //  - int8 chunks: the same chain with scales and, beside it, the widening, which
 //    every query tile does again for the keys it sees: the issue slots are 57 %
-//    used.  4001 tokens in a window: 139 us.
+//    used.  4001 tokens in a window: 137 us.
 //  - single tokens: reading the cache.  Four requests of 131072 tokens, bf16:
-//    168 us, 94 % of the copy rate; 64 ragged int8 requests 117 us, 50 %: what
+//    168 us, 94 % of the copy rate; 64 ragged int8 requests 115 us, 51 %: what
 //    bounds them is the order of a tile's steps in the one CTA of an SM (copy,
 //    widen, product, softmax), with no pipe full (issue 52 %, ALU 49 %, memory
 //    44 %).  In a window of a thousand keys

@@ -18,11 +18,14 @@
 //
 // What bounds it, and what it measured (bf16 product rate 1916 TFLOP/s, copy rate
 // 6.79 TB/s):
-//  - eight tokens behind 250000, int8 rows of 256 dims (528 MB): 145 us, 54 % of the
-//    copy rate.  No pipe is full (issue 61 %, ALU 55 %, tensor 42 %): the widening of
+//  - eight tokens behind 250000, int8 rows of 256 dims (528 MB): 143 us, 54 % of the
+//    copy rate.  No pipe is full (issue 60 %, ALU 53 %, tensor 42 %): the widening of
 //    a tile, its products from shared memory and its softmax take some 2 K clocks
 //    each and are handed from one to the next.  With the widening cut to a move the
-//    call takes 130 us.
+//    call takes 129 us, with neither widening nor softmax 122.
+//  - 80 drafts behind 60000, int8 rows of 128 dims: 148 us.  The widening warps' chain
+//    (alone 118 us) and the softmax warps' (alone 134) share issue slots, and a step
+//    of one that gets shorter is mostly hidden by the other.
 //  - 64 tokens behind 131072, bf16 rows of 256 dims: 102 us, 1.35 PFLOP/s; long tiles
 //    take 2.3 K clocks where the products take 2.0 K, the requests' own keys and the
 //    merge the rest.
