@@ -352,6 +352,20 @@ def test_offsets_out_of_order_write_nothing(skv, kind, n, starts, group_start):
     assert torch.equal(c.run(ws=c.ws), want) and int(c.st.item()) == 0
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [1, 3, 90])
+@pytest.mark.parametrize("group_start", [[0, -1, 3], [-1, 1, 3], [-2, -1, 3], [0, -(1 << 30), 3], [-(1 << 30), 1, 3],
+                                         [-(1 << 31), 2, 3], [1, -(1 << 31), (1 << 31) - 1]])
+def test_groups_that_begin_before_the_batch_write_nothing(skv, kind, n, group_start):
+    c = Case(skv, kind_of(skv, kind), 256, 8, 2, 16, [0, 1, 3], [100, 700], [164, 700, 64], [n] * 3, seed=33)
+    want = c.run().clone()
+    good, c.start = c.start, np.array(group_start, np.int32)
+    got = c.run(ws=c.ws)
+    assert int(c.st.item()) == skv.DEV_RANGE and (got == 123).all()
+    c.start = good
+    assert torch.equal(c.run(ws=c.ws), want) and int(c.st.item()) == 0
+
+
 def test_query_views_streams_and_output_in_their_place(skv):
     c = Case(skv, skv.KV_BF16, 256, 8, 2, 16, [0, 2], [700], [300, 20, 9], [60, 3, 1], seed=13)
     want = c.run().clone()
