@@ -270,6 +270,35 @@ def test_turned_in_place(skv, kind, rot, inter):
     move(skv, a, a, n, rot, inter, rows, rows, positions(n, 25), positions(n, 26))
 
 
+@pytest.mark.parametrize("kind,d", [(k, 256) for k in ALL] + [(k, d) for k in ALL[:2] for d in (64, 128)])
+@pytest.mark.parametrize("rot,inter", [(0, False), (32, False), (64, True)])
+def test_moves_in_place_one_behind_the_other(skv, kind, d, rot, inter):
+    """Four moves of one cache onto itself, queued without a wait, leave the bits that the same moves from one cache to
+    another leave."""
+    n, rows = 3000, 4000
+    a, b = Rows(skv, kind, rows, 3, d, seed=43), Rows(skv, kind, rows, 3, d, seed=43)
+    other = Rows(skv, kind, rows, 3, d, seed=44)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    at = torch.randperm(rows, generator=gen(45), device="cuda")[:n]
+    pos = [positions(n, 46 + i) for i in range(5)]
+    f = freqs(rot) if rot else None
+
+    def step(src, dst, i):
+        skv.move_rows(src.set(), dst.set(), n, src_rows=at, dst_rows=at, old_positions=pos[i] if rot else None,
+                      old_inv_freq=f, new_positions=pos[i + 1] if rot else None, new_inv_freq=f, interleaved=inter,
+                      status=st)
+
+    for i in range(4):
+        step(a, a, i)
+    for i in range(0, 4, 2):
+        step(b, other, i)
+        step(other, b, i + 1)
+    assert int(st.item()) == 0
+    for p in range(2):
+        for x, y in zip(a.bits(p), b.bits(p)):
+            np.testing.assert_array_equal(x, y)
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_far_positions_lose_nothing(skv, inter):
     """Positions of two thousand millions and below zero: with frequencies that are powers of two the angles of the

@@ -1,6 +1,8 @@
 """Refusals of skv_move_rows: decided on the host, before anything is launched,
 so they run without a GPU; and the plain encodings against the oracle's."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -83,6 +85,12 @@ def test_binding_refuses_sets_that_do_not_match(skv, monkeypatch):
                 dict(new_positions=i[:3], new_inv_freq=f), dict(new_inv_freq=f.double()), dict(status=i.long())):
         with pytest.raises(ValueError, match="contiguous elements"):
             skv.move_rows(a, a, 4, **bad)
+
+
+def test_rows_that_may_be_written_are_not_read_as_constant(skv):
+    """A cache may be its own destination: the non-coherent loads are for memory that no one writes meanwhile."""
+    src = open(os.path.join(os.path.dirname(skv.__file__), "csrc", "move_rows.cu")).read()
+    assert not re.search(r"\.nc\b|\bld_stream|\bld_nc|__ldg\b|__restrict__", src)
 
 
 def test_plain_encodings_are_the_oracles(orc):
