@@ -857,9 +857,10 @@ int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, int d, cons
  *   block_table     int32 [B][n_pages], and lengths int32 [B]: own keys only
  *   workspace  skv_shared_attend_workspace_size(...) bytes; nothing in it
  *            outlasts a call.  Beside the partial sums of skv_paged_attend (a
- *            quarter more of them above r = 128 rows) it holds 8 d + 24 bytes per
- *            token and query head.  The size depends on n_tok and the heads alone:
- *            enough for every batch of up to n_tok tokens
+ *            quarter more of them above r = 128 rows) it holds 8 d + 16 bytes per
+ *            token and query head and 32 per token and KV head, whether or not a
+ *            batch's lengths come to need them.  The size depends on n_tok and the
+ *            heads alone: enough for every batch of up to n_tok tokens
  * The other arguments are those of skv_paged_attend.  Where q_start or
  * group_start descends or leaves [0, n_tok] or [0, B] the call writes nothing
  * and sets SKV_DEV_RANGE; pages beyond a table or the pool are skipped and set

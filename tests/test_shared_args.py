@@ -1,9 +1,13 @@
 """Refusals of skv_shared_attend: decided on the host, before anything is
 launched, so they run without a GPU."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
+
+from skvtest import ROOT
 
 P = ctypes.c_void_p
 OK, EINVAL, EUNSUPPORTED, ENOMEM = 0, 1, 2, 4
@@ -55,6 +59,19 @@ def test_workspace_sizes(lib):
     for bad in [(0, 1, 1, 8, 2, 256), (1, -1, 1, 8, 2, 256), (1, 1, 0, 8, 2, 256), (1, 1, 1, 8, 3, 256), (1, 1, 1, 8, 2, 96),
                 (1, 1, 1, 258, 2, 256), (1, 1, 1 << 26, 8, 2, 256)]:
         assert size(*bad) == 0
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (8, 4), (6, 2), (8, 2), (128, 1)])
+def test_workspace_of_a_token(lib, d, Hq, Hkv):
+    """What the header says that a token more takes: 8 d + 16 bytes per query head, 32 per KV head (the parts are
+    rounded up to 256 bytes, so over 1000 tokens, all of them past a full query tile)."""
+    size = lib.skv_shared_attend_workspace_size
+    text = re.sub(r"\s*\n \*\s*", " ", open(os.path.join(ROOT, "include", "sparsekv.h")).read())
+    head, kv = map(int, re.search(r"holds 8 d \+ (\d+) bytes per token and query head and (\d+) per token and KV head",
+                                  text).groups())
+    more = size(4, 2, 2000, Hq, Hkv, d) - size(4, 2, 1000, Hq, Hkv, d)
+    assert abs(more - 1000 * (Hq * (8 * d + head) + Hkv * kv)) <= 512
 
 
 def test_binding_refuses_other_types_strides_and_sizes():
