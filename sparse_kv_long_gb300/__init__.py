@@ -660,12 +660,9 @@ def move_rows(src, dst, n, src_rows=None, dst_rows=None, old_positions=None, old
               new_inv_freq=None, interleaved=False, status=None, stream=None):
     """Rows src_rows (int64 [n], None: row i; negative: left out) of src to rows dst_rows of dst (row_set, tier_rows),
     re-encoded; keys turned from old_positions * old_inv_freq to new_positions * new_inv_freq (int32 [n], fp32
-    [rot/2]; positions None: not rotated)."""
+    [rot/2]; None: not rotated)."""
     if src.shape != dst.shape:
         raise ValueError(f"rows of (heads, values) {src.shape} and {dst.shape}")
-    for positions, freq in ((old_positions, old_inv_freq), (new_positions, new_inv_freq)):
-        if src.k and positions is not None and freq is None:
-            raise ValueError("positions without their frequencies")
     freqs = [f for f in (old_inv_freq, new_inv_freq) if f is not None]
     rot = 2 * freqs[0].shape[0] if freqs else 0
     if any(2 * f.shape[0] != rot for f in freqs):

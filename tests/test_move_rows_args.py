@@ -87,25 +87,6 @@ def test_binding_refuses_sets_that_do_not_match(skv, monkeypatch):
             skv.move_rows(a, a, 4, **bad)
 
 
-def test_binding_refuses_positions_without_frequencies(skv, monkeypatch):
-    """They were taken for a rotation of no dims: the keys moved as they were."""
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
-    x = torch.zeros((8, 2, 256), dtype=torch.bfloat16)
-    both, values = skv.row_set(BF16, x, x), skv.row_set(BF16, None, x)
-    i, f = torch.zeros((4,), dtype=torch.int32), torch.zeros((32,))
-    for bad in (dict(old_positions=i), dict(new_positions=i), dict(old_positions=i, new_positions=i),
-                dict(old_positions=i, old_inv_freq=f, new_positions=i), dict(new_positions=i, old_inv_freq=f),
-                dict(old_positions=i, new_positions=i, new_inv_freq=f)):
-        with pytest.raises(ValueError, match="without their frequencies"):
-            skv.move_rows(both, both, 4, **bad)
-    none = torch.zeros((0,))
-    for rows_of, good in ((both, dict()), (both, dict(old_positions=i, old_inv_freq=f)),
-                          (both, dict(old_inv_freq=f, new_inv_freq=f)), (values, dict(old_positions=i)),
-                          (both, dict(old_positions=i, old_inv_freq=none, new_positions=i, new_inv_freq=none))):
-        with pytest.raises(ValueError, match="on the current CUDA device"):  # nothing else is wrong with these
-            skv.move_rows(rows_of, rows_of, 4, **good)
-
-
 def test_rows_that_may_be_written_are_not_read_as_constant(skv):
     """A cache may be its own destination: the non-coherent loads are for memory that no one writes meanwhile."""
     src = open(os.path.join(os.path.dirname(skv.__file__), "csrc", "move_rows.cu")).read()
