@@ -849,7 +849,11 @@ int skv_paged_attend(int kv_kind, int B, int n_tok, int Hq, int Hkv, int d, cons
  * (with lengths[b] - n_b + i < 0 the prefix alone, as for the last token of a
  * prefix that is asked again; zeros where there is no prefix either).  Positions
  * play no part: keys and queries are rotated before.  A prefix may be in several
- * groups, and its pages in requests' own tables.
+ * groups, and its pages in requests' own tables.  Where prefixes are short beside
+ * the own keys (500 against 5000) there is little to save: skv_paged_attend with the
+ * prefix's pages in every table takes as long, or up to a sixth less for groups of
+ * two requests; and requests without a prefix, where they are most of a batch, are
+ * better off in a call of skv_paged_attend.
  *   group_start     int32 [n_groups+1], ascending (a group may have no request)
  *   prefix_table    int32 [n_groups][n_prefix_pages], no wider than needed: its width
  *            stands for the prefixes' lengths where these decide how the call runs
@@ -928,7 +932,8 @@ typedef struct skv_row_set {
  *                   are left so (both NULL: keys keep their rotation)
  *   old_inv_freq, new_inv_freq    fp32 [rot/2], finite; NULL where the positions are
  * A row of one cache may be its own destination (keys turned in place: the same
- * addresses on both sides); otherwise no destination overlaps a source.
+ * addresses on both sides); otherwise no destination overlaps a source.  Key
+ * sketches are not moved along: skv_sketch_project makes them anew, from bf16 keys.
  * Constraints: d in {64, 128, 256}, 256 with int4 rows; rot a multiple of 16, 0 <=
  * rot <= d; Hkv <= 4096; n <= 2^29; bf16 and int8 rows 16-byte aligned; int4 rows and pitches
  * multiples of 4, head_pitch >= d/2 + d/32, token_pitch >= Hkv*head_pitch.

@@ -660,7 +660,8 @@ def move_rows(src, dst, n, src_rows=None, dst_rows=None, old_positions=None, old
               new_inv_freq=None, interleaved=False, status=None, stream=None):
     """Rows src_rows (int64 [n], None: row i; negative: left out) of src to rows dst_rows of dst (row_set, tier_rows),
     re-encoded; keys turned from old_positions * old_inv_freq to new_positions * new_inv_freq (int32 [n], fp32
-    [rot/2]; None: not rotated)."""
+    [rot/2]; positions None: not rotated).  The frequencies say how many dims are rotated: without any, none is,
+    whatever the positions."""
     if src.shape != dst.shape:
         raise ValueError(f"rows of (heads, values) {src.shape} and {dst.shape}")
     freqs = [f for f in (old_inv_freq, new_inv_freq) if f is not None]

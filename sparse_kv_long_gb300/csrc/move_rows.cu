@@ -25,7 +25,8 @@
 // slots, the rest steps that wait for one another.  Measured (copy rate 6.79 TB/s;
 // K and V of 4 heads of 256, 32768 rows): bf16 44.6 us (6.0 TB/s), int8 copied 23.5
 // (5.8), with keys turned 41.2 (3.3), bf16 to int8 37.3 (5.4), turned 45.4 (4.5), int4
-// to int8 40.7 (2.6), turned 51.9 (2.0), bf16 to int4 48.4 (3.5); 64 rows 3.4 us.
+// to int8 40.7 (2.6), turned 51.9 (2.0), int4 to bf16 33.4 (5.1), turned 40.9 (4.2), bf16
+// to int4 48.4 (3.5), turned 67.6 (2.5); 64 rows 3.3 us.
 #include "rope.cuh"
 
 namespace skv {
@@ -192,7 +193,7 @@ __device__ __forceinline__ float scale_max(const F2 (&v)[N][4], int sub) {
 
 // fp16(m / TOP), the quotient rounded to fp32 and then to fp16: q0 = m c with c =
 // 1 / TOP rounded, and q0 + (m - TOP q0) c, which rounds as the quotient does
-// (Markstein's correction; tried for every mantissa of m).  A quotient too small
+// (Markstein's correction; tested for every mantissa of m).  A quotient too small
 // for that is zero in fp16, and an infinite m is replaced by the largest number,
 // whose quotient is beyond fp16, too.
 template <int TOP>

@@ -18,9 +18,14 @@
 // more than 2^kLazy; then the row's O is rescaled.  P is bf16 because V is (or
 // widens to it exactly) and a product takes one type; the row sum adds the
 // weights as rounded, so that the weights applied sum to one.  What is left of
-// that rounding takes the error against 64 bits from the output's own (0.0017
-// of the values' size) to 0.0023 at the most; what P leaves out as a second
-// bf16 would be half as many products again.  Logits, O, m and the sums are fp32.
+// that rounding (2^-9 of a weight, each on its own) takes the error against 64
+// bits from the output's own (0.0017 of the values' size) to 0.0024.  What P
+// leaves out as a second bf16 in a second product brings 0.0017, and was not
+// taken for what it costs every kind of call: with shared prefixes, 8 single
+// tokens behind 250000 int8 rows 143 us, then 162; 64 behind 131072 bf16 rows 102,
+// 135; 80 drafts behind 60000 int8 rows 148, 173; 40 tokens behind five prefixes
+// 57, 62 to 67; 5 chunks of 333 53, 57; 16 chunks of 256 behind 32768 1.26 ms, 1.78.
+// Logits, O, m and the sums are fp32.
 //
 // What bounds it, and what it measured (bf16 product rate 1916 TFLOP/s, copy
 // rate 6.79 TB/s):
@@ -1873,7 +1878,10 @@ int tile_rows(int n_tok, int G, int ctas) {
 // the size at 128 dims), the rest staging; where that would leave fewer than
 // two staging slots (128 dims: three), as beside a full query tile, a wide stage
 // makes room (64 ragged requests: 3 and 6 slots 130.2 us, 4 and 4 129.3, 5 and
-// 2 156; 80 drafts of 128 dims behind 60000 keys: 4 and 2 155, 3 and 4 148).  With
+// 2 156; 128 dims, 80 drafts behind a shared prefix of 60000: 4 and 2 155, 3 and 4
+// 148, 16 x 5 drafts with 60000 keys each 702 and 648, 8 x 32 tokens at 30000 201 and
+// 181, 64 ragged single tokens 174 and 173, 16 x 20 in a window of 1024 34.5 and 34.6,
+// 64 x 2 ragged tokens of 8 heads a KV head 83.7 and 84.2).  With
 // q_start the tokens of a request are not known here, so a batch of single tokens
 // gets a full tile's layout: the same requests take 153 us with q_start, 118
 // without (bf16 rows 134 either way).

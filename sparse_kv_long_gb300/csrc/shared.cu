@@ -26,13 +26,21 @@
 //  - 80 drafts behind 60000, int8 rows of 128 dims: 148 us.  The widening warps' chain
 //    (alone 118 us) and the softmax warps' (alone 134) share issue slots, and a step
 //    of one that gets shorter is mostly hidden by the other.
-//  - 64 tokens behind 131072, bf16 rows of 256 dims: 102 us, 1.35 PFLOP/s; long tiles
-//    take 2.3 K clocks where the products take 2.0 K, the requests' own keys and the
-//    merge the rest.
-//  - 16 chunks of 256 tokens behind 32768: 1.25 ms, 1.77 PFLOP/s, the power limit.
+//  - 64 tokens behind 131072, bf16 rows of 256 dims: 102 us, 1.35 PFLOP/s, of one batch
+//    again and again, 112 us (1.23) of another batch each call; long tiles take 2.3 K
+//    clocks where the products take 2.0 K, the requests' own keys and the merge the
+//    rest.
+//  - 16 chunks of 256 tokens behind 32768: 1.26 to 1.29 ms, 1.71 to 1.76 PFLOP/s, the
+//    power limit.
 //  - 40 tokens, 5 prefixes, bf16 rows of 128 dims (236 MB): 57 to 63 us; memory, behind
 //    the launch, the plan and the merge.
 //  - small calls (eight tokens behind 2000: 17 us): what follows one another.
+// Where it pays: what it saves is the reading of a prefix once per request, what it
+// costs a second item and a merge of state rows per request.  40 single tokens in
+// five groups, up to 5000 keys of their own, int8 rows of 256 dims, against the paged
+// attention with the prefixes' pages in every table: behind 500 keys 46.5 / 45.8 us,
+// 5000 64 / 134, 50000 207 / 990; 64 in pairs behind 500 74 / 63, 5000 163 / 199.
+// (Several groups get the layout of a full query tile, as q_start does.)
 #include "paged.cuh"
 
 namespace skv {
@@ -207,10 +215,18 @@ Layout layout(int n_tok, int Hkv, int G, int d, int ctas, int sms) {
 // 64 / 157 against 42 / 62 / 120; of 32 / 8 heads of 128 behind 32000: bf16 63 against
 // 81, int8 91 against 120.  The prefixes' lengths are on the device; their table's
 // width stands for them.
+// The rule for 128 dims leaves long prefixes to single CTAs, too: 64 requests of 1 / 5 /
+// 16 tokens of 32 / 8 heads, single against pairs, bf16 behind 8000 39 / 80 / 179 us
+// against 64 / 99 / 181, behind 32000 69 / 182 / 540 against 90 / 196 / 497, behind
+// 100000 140 / 546 / 1880 against 142 / 465 / 1355.
 // Else by the query tiles of an average group (without groups, request) that each
 // CTA takes, a pair's being two, weighed by what they cost: 192 rows, two tiles or a
 // pair, over 30000 keys took 185 / 119 us (bf16 rows of 256 dims), 205 / 157 (int8),
-// 112 / 96 and 134 / 123 (128 dims).
+// 112 / 96 and 134 / 123 (128 dims).  All tokens count as the groups', so a batch of
+// which few requests are in a group may run as pairs where single CTAs would do: 2
+// requests behind 8000 and 62 alone with 4000 keys, 20 tokens each of 32 / 8 heads of
+// 128, single against pairs 199 / 264 us (bf16), 237 / 358 (int8); 40 tokens each 373 /
+// 280 and 440 / 380.
 int ctas_for(int B, int n_groups, int n_tok, int d, int G, bool int8, bool single, int64_t prefix_keys) {
   if (n_groups == 0 && single) return 1;
   const bool few = static_cast<int64_t>(n_tok) * G <= static_cast<int64_t>(B) * (kRows / 2);
