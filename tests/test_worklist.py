@@ -134,5 +134,6 @@ def check(tmp_path_factory):
 
 
 def test_offsets_of_any_value_are_read_within_their_arrays(check):
-    r = subprocess.run([check], capture_output=True, text=True, timeout=300)
+    env = {**os.environ, "ASAN_OPTIONS": "detect_leaks=0"}  # looking for leaks takes rights that a container may not have
+    r = subprocess.run([check], capture_output=True, text=True, timeout=300, env=env)
     assert r.returncode == 0, (r.stdout + r.stderr)[:3000]
